@@ -425,6 +425,106 @@ int moe_gate_backward_parts(const float* gate_part, const int32_t* pair_row, int
                             int32_t d, const float* w, const int32_t* ids, int64_t T, int32_t k,
                             int32_t E, float* d_gate, float* d_logits, hipStream_t stream);
 
+/* ---- dense products around the routed experts ("RL at 1T scale", section
+ * "Wide Expert Parallelism": what every token passes besides its routed
+ * experts) -- the router's projection and a shared expert ------------------ */
+
+/* Element-wise functions of the products' epilogues. GELU is z * Phi(z) with
+ * Phi the normal distribution function (erf, not its tanh approximation).    */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_SIGMOID = 4 };
+/* How moe_gated_ffn keeps [G, U] for moe_gated_ffn_backward.                  */
+enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_INT8 = 2 };
+
+/* Shared rules of the functions below.  Matrices are row-major; a row stride ld
+ * (elements) is at least the row's length and at most 2^22, and a multiple of 8
+ * where the matrix is an operand of a product; operand and gradient pointers are
+ * 16-byte aligned (rows are moved in 16-byte pieces). K, d and f are multiples
+ * of 8, N is any number >= 1, all at most 2^20; 0 <= T <= 2^30. Products
+ * are bf16 x bf16 accumulated in fp32 (matrix instructions); a long K may be
+ * summed in several fp32 pieces added in a fixed order. A NaN or infinity in a
+ * row of x (or W) reaches that row (column) of the result only.
+ * MOE_ERR_SHAPE for sizes, strides and alignment, MOE_ERR_UNSUPPORTED for
+ * unknown enum values, MOE_ERR_WORKSPACE for a workspace smaller than the
+ * *_workspace function says (which depends on the sizes and the current
+ * device's compute units).  Calls that share a workspace must not overlap.    */
+
+/* out[t, n] = act(sum_k x[t, k] W[n, k] + bias[n]) + residual[t, n]
+ *   x [T, K] bf16 (stride ldx), W [N, K] bf16 (ldw), bias [N] bf16 or NULL,
+ *   residual [T, N] bf16 (ldr) or NULL, out [T, N] (ldo) bf16 (out_type
+ *   MOE_SRC_BF16) or fp32 (MOE_SRC_F32). out may be the residual's memory
+ *   (bf16, ldo == ldr); it overlaps no other input.
+ *   pre: NULL, or [T, N] bf16 dense: the argument of act, rounded, which
+ *   moe_linear_backward takes where act is not MOE_ACT_NONE.
+ * T = 0 is a no-op.                                                           */
+int moe_linear_workspace(int64_t T, int64_t N, int64_t K, size_t* bytes);
+int moe_linear(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, const uint16_t* bias,
+               const uint16_t* residual, int64_t ldr, int64_t T, int64_t N, int64_t K, int32_t act,
+               void* out, int32_t out_type, int64_t ldo, uint16_t* pre,
+               void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of moe_linear. With dz[t, n] = dy[t, n] * act'(pre[t, n]) (rounded
+ * to bf16 for the products; dy itself is the residual's gradient):
+ *     dx[t, k] = sum_n dz[t, n] W[n, k] + dx_add[t, k]
+ *     dW[n, k] = sum_t dz[t, n] x[t, k]      dbias[n] = sum_t dz[t, n]
+ *   dy [T, N] dense, bf16 or fp32 (dy_type); pre as saved (NULL for
+ *   MOE_ACT_NONE); dx [T, K], dW [N, K], dbias [N] bf16 dense, each NULL to
+ *   skip it; dx_add [T, K] bf16 dense or NULL (may be dx). T = 0 writes zeros
+ *   to dW and dbias.                                                          */
+int moe_linear_backward_workspace(int64_t T, int64_t N, int64_t K, size_t* bytes);
+int moe_linear_backward(const void* dy, int32_t dy_type, const uint16_t* pre, const uint16_t* x, int64_t ldx,
+                        const uint16_t* W, int64_t ldw, const uint16_t* dx_add, int64_t T, int64_t N, int64_t K,
+                        int32_t act, uint16_t* dx, uint16_t* dW, uint16_t* dbias,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gated feed-forward block (a shared expert). With W13 [2f, d] = [Wg; Wu] and
+ * b13 [2f] = [bg; bu]:
+ *     G = x Wg^T + bg,  U = x Wu^T + bu,  h = act(G) * U      (one kernel)
+ *     y = h W2^T + b2 + residual
+ *   x [T, d] (ldx), W13, W2 [d, f], b13, b2 (NULL = 0), residual [T, d] (NULL =
+ *   0, may be y), h [T, f], y [T, d] bf16, dense but for x. h is written and
+ *   read by the call; y == NULL stops after h (W2, b2 and residual are then
+ *   not read).
+ * save: MOE_SAVE_BF16 writes gu [T, 2f] = [G, U] in bf16; MOE_SAVE_INT8 (f % 128
+ *   == 0) writes it as moe_act_save writes rows of 2f columns: gu [T, 2f] int8
+ *   codes, gu_s [2f/128, T] fp32.                                             */
+int moe_gated_ffn_workspace(int64_t T, int64_t d, int64_t f, size_t* bytes);
+int moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* W13, const uint16_t* b13, const uint16_t* W2,
+                  const uint16_t* b2, const uint16_t* residual, int64_t T, int64_t d, int64_t f, int32_t act,
+                  uint16_t* h, uint16_t* y, int32_t save, void* gu, float* gu_s,
+                  void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients of moe_gated_ffn from the saved [G, U] (h is recomputed from it):
+ *     dh = dy W2,  dG = dh * U * act'(G),  dU = dh * act(G)   (one kernel; dh
+ *                                      stays in fp32, [dG, dU] is rounded to bf16)
+ *     dx = [dG, dU] W13 + dx_add       dW13 = [dG, dU]^T x     db13 = sum_t [dG, dU]
+ *     dW2 = dy^T (act(G) * U)          db2 = sum_t dy
+ *   dy [T, d], x [T, d] (ldx), dx_add as above; dx [T, d], dW13 [2f, d], dW2
+ *   [d, f], db13 [2f], db2 [d] bf16 dense, each NULL to skip it; save, gu, gu_s
+ *   as given to the forward (MOE_SAVE_BF16 or MOE_SAVE_INT8). T = 0 writes zeros
+ *   to the weights' and biases' gradients.                                    */
+int moe_gated_ffn_backward_workspace(int64_t T, int64_t d, int64_t f, size_t* bytes);
+int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t ldx, const uint16_t* W13,
+                           const uint16_t* W2, int32_t save, const void* gu, const float* gu_s,
+                           const uint16_t* dx_add, int64_t T, int64_t d, int64_t f, int32_t act,
+                           uint16_t* dx, uint16_t* dW13, uint16_t* dW2, uint16_t* db13, uint16_t* db2,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- activations kept in 8 bits between forward and backward ---------------
+ * Rows in blocks of 128 columns (the last one shorter if cols % 128 != 0), one
+ * fp32 scale each:
+ *     a = max(max|v|, 2^-100),  s = a / 127,  q = round_half_even(v * (127 / a))
+ * restored as bf16(q * s).  A block with a NaN or an infinity is restored as
+ * NaN throughout.  (8-bit integers rather than e4m3: the backward uses these
+ * values through smooth functions and sums, where the error relative to the
+ * block counts; for values spread like a normal distribution it is a quarter of
+ * e4m3's, and e4m3 is ahead only past outliers of about 11 standard deviations.)
+ *   src [rows, cols] bf16 (row stride ld), q [rows, cols] int8 dense, s
+ *   [ceil(cols/128), rows] fp32; cols % 8 == 0; dst [rows, cols] bf16 dense.   */
+int moe_act_save(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols, int8_t* q, float* s,
+                 hipStream_t stream);
+int moe_act_restore(const int8_t* q, const float* s, int64_t rows, int64_t cols, uint16_t* dst,
+                    hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,306 @@
+// bf16 matrix products on gfx950 MFMA with fused epilogues: the shared parts of
+// linear.hip and gated_ffn.hip.
+//
+//   C[m, n] = sum_k A(m, k) B(n, k)
+//
+// Each operand is stored either with k contiguous ("KC": A [M, K]) or with k as
+// the row index ("KS": A [K, M]), so that forward (KC, KC), data-gradient (KC,
+// KS) and weight-gradient (KS, KS) products read every matrix as it lies in
+// memory; no transposed copy is made.
+#pragma once
+
+#include "mfma_common.hpp"
+
+namespace moe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int DBK = 64;  // K step: 128 bytes of a KC row, 64 rows of a KS matrix
+
+enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3 };
+
+struct DenseArgs {
+    const uint16_t* a;  // KC [M, lda] / KS [K, lda]
+    const uint16_t* b;  // KC [N, ldb] / KS [K, ldb]
+    int64_t lda, ldb;
+    int M, N, K;     // EPI_GATE: N = 2f, the B rows are [G; U]
+    int a_cols, b_cols;  // KS operands: columns that may be read (a multiple of 8, >= M / N)
+    int mt, nt;      // tiles along M and N
+    int ksteps;      // K steps of one split
+    // EPI_LINEAR
+    const uint16_t* bias;  // [N]
+    const uint16_t* res;   // [M, ldr]
+    int64_t ldr;
+    void* out;             // [M, ldo] bf16 / fp32
+    int64_t ldo;
+    uint16_t* pre;         // [M, N] bf16
+    int act, out_f32, vec;  // vec: N, strides and pointers allow four elements at a time
+    // EPI_PART: part[split][m][part_ld]
+    float* part;
+    int64_t part_ld;
+    // EPI_GATE / EPI_DGATE
+    int f, save;
+    uint16_t* h;    // [M, f]
+    void* gu;       // [M, 2f] bf16 or int8 codes
+    float* gu_s;    // [2f/128, M]
+    uint16_t* dgu;  // [M, 2f]
+};
+
+// ---------------------------------------------------------------- activations
+// act(z) and act'(z); `act` is uniform.  sigmoid from the hardware exp2 and
+// reciprocal (about 1 ulp each).
+__device__ __forceinline__ float act_value(int act, float z) {
+    switch (act) {
+        case MOE_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);  // NaN stays NaN
+        case MOE_ACT_SILU: return silu(z);
+        case MOE_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+        case MOE_ACT_SIGMOID: return sigmoid_fast(z);
+        default: return z;
+    }
+}
+__device__ __forceinline__ void act_both(int act, float z, float& v, float& slope) {
+    switch (act) {
+        case MOE_ACT_RELU:
+            v = z > 0.f ? z : (z == z ? 0.f : z);
+            slope = z > 0.f ? 1.f : 0.f;
+            return;
+        case MOE_ACT_SILU: {
+            const float s = sigmoid_fast(z);
+            v = z * s;
+            slope = s * (1.f + z * (1.f - s));
+            return;
+        }
+        case MOE_ACT_GELU: {
+            const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+            v = z * c;
+            slope = c + z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z) * 0.39894228040143268f;
+            return;
+        }
+        case MOE_ACT_SIGMOID: {
+            const float s = sigmoid_fast(z);
+            v = s;
+            slope = s * (1.f - s);
+            return;
+        }
+        default: v = z; slope = 1.f; return;
+    }
+}
+
+// ---------------------------------------------------------------- 8-bit blocks
+// Scale of an 8-bit block from the largest |v| as a bit pattern (taken with an
+// unsigned maximum, so a NaN wins over every number): s = a / 127 and the
+// factor 127 / a, both correctly rounded.
+struct Keep8 {
+    float s, inv;
+};
+__device__ __forceinline__ Keep8 keep8_scale(uint32_t amax_bits) {
+    const float lo = 7.888609052210118e-31f;  // 2^-100
+    float a = __uint_as_float(amax_bits);
+    if (a < lo) a = lo;  // false for NaN
+    return Keep8{a / 127.f, 127.f / a};
+}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// |v * inv| <= 127 (1 + 2^-23), which rounds to at most 127; NaN converts to 0
+// and is restored as NaN through the scale
+__device__ __forceinline__ int keep8_code(float v, float inv) { return (int)__builtin_rintf(v * inv); }
+__device__ __forceinline__ uint32_t pack_s8x4(int a, int b, int c, int d) {
+    return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8) | ((uint32_t)(c & 0xFF) << 16) | ((uint32_t)d << 24);
+}
+__device__ __forceinline__ float s8_of(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
+
+// ---------------------------------------------------------------- operand moves
+// 16 bytes per lane, global -> LDS (lane l to LDS m0 + 16 l), through a buffer
+// descriptor: a lane whose offset is OOB reads nothing and writes zeros, which
+// is how row, column and K tails are filled.
+constexpr uint32_t OOB = 0x80000000u;
+__device__ __forceinline__ u32x4 buf_desc(const void* base) {
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xFFFFu)), 0x7FFFFFF0u,
+                 0x00020000u};
+}
+__device__ __forceinline__ void dma16b(const u32x4& desc, uint32_t voff, uint32_t lds) {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(desc), "{m0}"(lds) : "memory");
+}
+
+// Transposing LDS read: the 16 lanes of a group supply 4 K rows x 16 columns
+// (lane i: row i / 4, columns 4 (i % 4) .. + 3) and lane i receives column i's
+// four K values.
+template <int OFF>
+__device__ __forceinline__ v2u lds_tr16(uint32_t addr) {
+    typedef __attribute__((address_space(3))) s16x4* ptr;
+    return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((ptr)(uintptr_t)(addr + OFF)));
+}
+
+__device__ __forceinline__ v4f mfma_bf16(const u32x4& a, const u32x4& b, const v4f& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// LDS images of one operand's K step, R rows (KC) or columns (KS):
+//   KC: row r at 128 r; its eight 16-byte chunks c at c ^ (r & 7).
+//   KS: per 128 columns a 16 KB image, K row k at 256 k; its sixteen chunks c
+//       at c ^ 2 f(k), f(k) = (k & 3) | (k >> 3 & 1) << 2: the eight K rows a
+//       half-wave reads of one 16-column fragment fall on distinct banks.
+// One 1 KB segment (one DMA instruction) is 8 KC rows or 4 K rows.
+struct KcLane {
+    uint32_t off;  // this lane's byte offset in a segment
+    uint32_t row, k;  // its row in a segment, its first K value
+    __device__ __forceinline__ KcLane(int lane, int64_t ld) {
+        row = (uint32_t)lane >> 3;
+        const uint32_t c = ((uint32_t)lane & 7) ^ row;
+        k = c * 8;
+        off = row * (uint32_t)(ld * 2) + c * 16;
+    }
+};
+__device__ __forceinline__ uint32_t ks_f(uint32_t k) { return (k & 3) | ((k >> 3 & 1) << 2); }
+
+// KC fragment of 16 rows from row r0 (a multiple of 16), K values 32 s + 8 g ..
+// + 7 (g = lane / 16): the byte offset of this lane for s = 0; s = 1 is it ^ 64.
+__device__ __forceinline__ uint32_t kc_frag(int lane, int r0) {
+    const uint32_t r = (uint32_t)(r0 + (lane & 15));
+    return r * 128 + ((((uint32_t)lane >> 4) ^ (r & 7)) << 4);
+}
+// KS fragment of 16 columns (16-column group c16 of the image): this lane's byte
+// offset for K values 8 g .. + 3; + 1024 the next four, + 8192 per s.
+__device__ __forceinline__ uint32_t ks_frag(int lane, int c16) {
+    const uint32_t l15 = (uint32_t)lane & 15;
+    const uint32_t k = ((uint32_t)lane >> 4) * 8 + (l15 >> 2);
+    return k * 256 + (((uint32_t)c16 ^ ks_f(k)) << 5) + (l15 & 3) * 8;
+}
+
+// ---------------------------------------------------------------- epilogues
+__device__ __forceinline__ void load_bf16x4(const uint16_t* p, float* v) {
+    const v2u w = *reinterpret_cast<const v2u*>(p);
+    v[0] = bf16_lo(w.x);
+    v[1] = bf16_hi(w.x);
+    v[2] = bf16_lo(w.y);
+    v[3] = bf16_hi(w.y);
+}
+__device__ __forceinline__ v2u pack_bf16x4(float a, float b, float c, float d) {
+    return v2u{cvt_bf16x2(a, b), cvt_bf16x2(c, d)};
+}
+
+// EPI_LINEAR for C[m, n .. n + 3]
+__device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n, v4f c) {
+    if (g.vec) {
+        if (n >= g.N) return;
+        float v[4] = {c.x, c.y, c.z, c.w}, t[4];
+        if (g.bias) {
+            load_bf16x4(g.bias + n, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += t[i];
+        }
+        if (g.pre) *reinterpret_cast<v2u*>(g.pre + m * g.N + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
+        if (g.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = act_value(g.act, v[i]);
+        }
+        if (g.res) {
+            load_bf16x4(g.res + m * g.ldr + n, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += t[i];
+        }
+        if (g.out_f32)
+            *reinterpret_cast<v4f*>((float*)g.out + m * g.ldo + n) = v4f{v[0], v[1], v[2], v[3]};
+        else
+            *reinterpret_cast<v2u*>((uint16_t*)g.out + m * g.ldo + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= g.N) return;
+        float v = c[i];
+        if (g.bias) v += bf16_to_f32(g.bias[n + i]);
+        if (g.pre) g.pre[m * g.N + n + i] = (uint16_t)cvt_bf16x2(v, 0.f);
+        v = act_value(g.act, v);
+        if (g.res) v += bf16_to_f32(g.res[m * g.ldr + n + i]);
+        if (g.out_f32)
+            ((float*)g.out)[m * g.ldo + n + i] = v;
+        else
+            ((uint16_t*)g.out)[m * g.ldo + n + i] = (uint16_t)cvt_bf16x2(v, 0.f);
+    }
+}
+
+// EPI_DGATE for dh[m, n .. n + 3] (n < f, f % 8 == 0): [dG, dU] and h from the
+// saved G, U
+__device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh) {
+    if (n >= g.f) return;
+    float G[4], U[4];
+    const int64_t at = m * (2 * (int64_t)g.f) + n;
+    if (g.save == MOE_SAVE_INT8) {
+        const int64_t blk = n >> 7, nb = g.f >> 7;
+        const float sg = g.gu_s[blk * g.M + m], su = g.gu_s[(nb + blk) * g.M + m];
+        const uint32_t qg = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at);
+        const uint32_t qu = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at + g.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            G[i] = s8_of(qg, i) * sg;
+            U[i] = s8_of(qu, i) * su;
+        }
+    } else {
+        load_bf16x4((const uint16_t*)g.gu + at, G);
+        load_bf16x4((const uint16_t*)g.gu + at + g.f, U);
+    }
+    float dG[4], dU[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v, sl;
+        act_both(g.act, G[i], v, sl);
+        dG[i] = dh[i] * U[i] * sl;
+        dU[i] = dh[i] * v;
+        h[i] = v * U[i];
+    }
+    *reinterpret_cast<v2u*>(g.dgu + at) = pack_bf16x4(dG[0], dG[1], dG[2], dG[3]);
+    *reinterpret_cast<v2u*>(g.dgu + at + g.f) = pack_bf16x4(dU[0], dU[1], dU[2], dU[3]);
+    if (g.h) *reinterpret_cast<v2u*>(g.h + m * g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
+}
+
+// EPI_GATE without the 8-bit save for G, U[m, n .. n + 3] (bias already added)
+__device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, const v4f& G, const v4f& U) {
+    if (n >= g.f) return;
+    float h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = act_value(g.act, G[i]) * U[i];
+    *reinterpret_cast<v2u*>(g.h + m * g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
+    if (g.save == MOE_SAVE_BF16) {
+        uint16_t* p = (uint16_t*)g.gu + m * (2 * (int64_t)g.f) + n;
+        *reinterpret_cast<v2u*>(p) = pack_bf16x4(G[0], G[1], G[2], G[3]);
+        *reinterpret_cast<v2u*>(p + g.f) = pack_bf16x4(U[0], U[1], U[2], U[3]);
+    }
+}
+__device__ __forceinline__ void add_gate_bias(const DenseArgs& g, int n, v4f& G, v4f& U) {
+    if (!g.bias || n >= g.f) return;
+    float t[4];
+    load_bf16x4(g.bias + n, t);
+    G += v4f{t[0], t[1], t[2], t[3]};
+    load_bf16x4(g.bias + g.f + n, t);
+    U += v4f{t[0], t[1], t[2], t[3]};
+}
+
+// ---------------------------------------------------------------- host side
+// A product: fills in tiles, splits and workspace use and launches it (and, for
+// a split K, the sum of the pieces with the epilogue).
+enum { OP_KC = 0, OP_KS = 1 };
+int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes, hipStream_t stream);
+// fp32 workspace of a product with M x N results and K summands
+size_t dense_ws(int64_t M, int64_t N, int64_t K, int epi);
+
+// column sums of src [T, N] bf16 (row stride ld, N % 4 == 0) as bf16; part: fp32
+// workspace of colsum_ws bytes
+size_t colsum_ws(int64_t T, int64_t N);
+int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_t* out, float* part,
+                  hipStream_t stream);
+// dz = dy * act'(pre) [T, ldz] bf16 (dz may be NULL) and its column sums (dbias
+// may be NULL; part then unused); ldz = N rounded up to 8
+int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
+              float* part, uint16_t* dbias, hipStream_t stream);
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+// fill of n bf16 (or other 2-byte) zeros by a kernel (memset nodes stay out of graphs)
+int zero16_launch(uint16_t* p, int64_t n, hipStream_t stream);
+
+}  // namespace moe

@@ -1,0 +1,177 @@
+// Matrix product with bias, activation and residual in its epilogue, and its
+// gradients: the router's projection and a shared expert's second projection.
+#include "dense_gemm.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int64_t MAX_DIM = 1 << 20, MAX_LD = 1 << 22, MAX_T = 1 << 30;
+
+// dz is made where dy cannot be the products' operand itself
+bool needs_dz(int32_t dy_type, int64_t N, int32_t act) {
+    return act != MOE_ACT_NONE || dy_type == MOE_SRC_F32 || N % 8 != 0;
+}
+
+int check_sizes(int64_t T, int64_t N, int64_t K) {
+    MOE_REQUIRE(T >= 0 && T <= MAX_T, MOE_ERR_SHAPE, "T=%lld outside [0, 2^30]", (long long)T);
+    MOE_REQUIRE(N >= 1 && N <= MAX_DIM, MOE_ERR_SHAPE, "N=%lld outside [1, 2^20]", (long long)N);
+    MOE_REQUIRE(K >= 8 && K <= MAX_DIM && K % 8 == 0, MOE_ERR_SHAPE, "K=%lld: a multiple of 8 up to 2^20", (long long)K);
+    return MOE_OK;
+}
+bool operand_ok(const void* p, int64_t ld, int64_t cols) {
+    return aligned16(p) && ld >= cols && ld <= MAX_LD && ld % 8 == 0;
+}
+
+struct BackwardWs {
+    size_t dz, part, gemm, total;
+};
+BackwardWs backward_ws(int64_t T, int64_t N, int64_t K) {
+    BackwardWs w;
+    const int64_t ldz = round_up(N, 8);
+    w.dz = 0;
+    w.part = (size_t)round_up(T * ldz * 2, 256);
+    w.gemm = w.part + (size_t)round_up((int64_t)colsum_ws(T, ldz), 256);
+    size_t g = dense_ws(T, K, N, EPI_LINEAR);
+    const size_t g2 = dense_ws(N, K, T, EPI_LINEAR);
+    if (g2 > g) g = g2;
+    w.total = w.gemm + g;
+    return w;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_linear_workspace(int64_t T, int64_t N, int64_t K, size_t* bytes) {
+    clear_error();
+    MOE_REQUIRE(bytes, MOE_ERR_NULL, "bytes is NULL");
+    if (const int rc = check_sizes(T, N, K)) return rc;
+    *bytes = dense_ws(T, N, K, EPI_LINEAR);
+    return MOE_OK;
+}
+
+extern "C" int moe_linear(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, const uint16_t* bias,
+                          const uint16_t* residual, int64_t ldr, int64_t T, int64_t N, int64_t K, int32_t act,
+                          void* out, int32_t out_type, int64_t ldo, uint16_t* pre, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+    clear_error();
+    if (const int rc = check_sizes(T, N, K)) return rc;
+    MOE_REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_SIGMOID, MOE_ERR_UNSUPPORTED, "unknown activation %d", act);
+    MOE_REQUIRE(out_type == MOE_SRC_BF16 || out_type == MOE_SRC_F32, MOE_ERR_UNSUPPORTED, "unknown output type %d",
+                out_type);
+    if (T == 0) return MOE_OK;
+    MOE_REQUIRE(x && W && out, MOE_ERR_NULL, "x, W or out is NULL");
+    MOE_REQUIRE(operand_ok(x, ldx, K), MOE_ERR_SHAPE, "x: 16-byte aligned, ldx=%lld a multiple of 8 in [K, 2^22]",
+                (long long)ldx);
+    MOE_REQUIRE(operand_ok(W, ldw, K), MOE_ERR_SHAPE, "W: 16-byte aligned, ldw=%lld a multiple of 8 in [K, 2^22]",
+                (long long)ldw);
+    MOE_REQUIRE(ldo >= N && ldo <= MAX_LD, MOE_ERR_SHAPE, "ldo=%lld outside [N, 2^22]", (long long)ldo);
+    MOE_REQUIRE(!residual || (ldr >= N && ldr <= MAX_LD), MOE_ERR_SHAPE, "ldr=%lld outside [N, 2^22]", (long long)ldr);
+    DenseArgs g = {};
+    g.a = x;
+    g.lda = ldx;
+    g.b = W;
+    g.ldb = ldw;
+    g.M = (int)T;
+    g.N = (int)N;
+    g.K = (int)K;
+    g.bias = bias;
+    g.res = residual;
+    g.ldr = ldr;
+    g.out = out;
+    g.ldo = ldo;
+    g.pre = pre;
+    g.act = act;
+    g.out_f32 = out_type == MOE_SRC_F32;
+    g.vec = N % 4 == 0 && ldo % 4 == 0 && aligned16(out) && aligned16(bias) && aligned16(pre) &&
+            (!residual || (ldr % 4 == 0 && aligned16(residual)));
+    return dense_launch(g, OP_KC, OP_KC, EPI_LINEAR, ws, ws_bytes, stream);
+}
+
+extern "C" int moe_linear_backward_workspace(int64_t T, int64_t N, int64_t K, size_t* bytes) {
+    clear_error();
+    MOE_REQUIRE(bytes, MOE_ERR_NULL, "bytes is NULL");
+    if (const int rc = check_sizes(T, N, K)) return rc;
+    *bytes = backward_ws(T, N, K).total;
+    return MOE_OK;
+}
+
+extern "C" int moe_linear_backward(const void* dy, int32_t dy_type, const uint16_t* pre, const uint16_t* x, int64_t ldx,
+                                   const uint16_t* W, int64_t ldw, const uint16_t* dx_add, int64_t T, int64_t N,
+                                   int64_t K, int32_t act, uint16_t* dx, uint16_t* dW, uint16_t* dbias, void* ws,
+                                   size_t ws_bytes, hipStream_t stream) {
+    clear_error();
+    if (const int rc = check_sizes(T, N, K)) return rc;
+    MOE_REQUIRE(act >= MOE_ACT_NONE && act <= MOE_ACT_SIGMOID, MOE_ERR_UNSUPPORTED, "unknown activation %d", act);
+    MOE_REQUIRE(dy_type == MOE_SRC_BF16 || dy_type == MOE_SRC_F32, MOE_ERR_UNSUPPORTED, "unknown gradient type %d",
+                dy_type);
+    MOE_REQUIRE(aligned16(dx) && aligned16(dW) && aligned16(dx_add), MOE_ERR_SHAPE,
+                "dx, dW and dx_add: 16-byte aligned");
+    if (T == 0) {
+        int rc = MOE_OK;
+        if (dW) rc = zero16_launch(dW, N * K, stream);
+        if (rc == MOE_OK && dbias) rc = zero16_launch(dbias, N, stream);
+        return rc;
+    }
+    MOE_REQUIRE(dy && (!dW || x) && (!dx || W), MOE_ERR_NULL, "dy, x or W is NULL");
+    MOE_REQUIRE(act == MOE_ACT_NONE || pre, MOE_ERR_NULL, "pre is NULL with an activation");
+    MOE_REQUIRE(aligned16(dy) && aligned16(pre), MOE_ERR_SHAPE, "dy and pre: 16-byte aligned");
+    MOE_REQUIRE(!dW || operand_ok(x, ldx, K), MOE_ERR_SHAPE, "x: 16-byte aligned, ldx=%lld a multiple of 8 in [K, 2^22]",
+                (long long)ldx);
+    MOE_REQUIRE(!dx || operand_ok(W, ldw, K), MOE_ERR_SHAPE, "W: 16-byte aligned, ldw=%lld a multiple of 8 in [K, 2^22]",
+                (long long)ldw);
+    const BackwardWs w = backward_ws(T, N, K);
+    MOE_REQUIRE((ws && aligned16(ws)) || !w.total, MOE_ERR_NULL, "ws is NULL or not 16-byte aligned");
+    MOE_REQUIRE(ws_bytes >= w.total, MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, w.total);
+    uint8_t* wp = (uint8_t*)ws;
+    void* gw = wp + w.gemm;
+    const size_t gwb = ws_bytes - w.gemm;
+
+    const uint16_t* dz = (const uint16_t*)dy;
+    int64_t ldz = N;
+    const bool own = needs_dz(dy_type, N, act);
+    if (own || dbias) {
+        const int64_t ldp = round_up(N, 8);
+        if (const int rc = dz_launch(dy, dy_type == MOE_SRC_F32, act == MOE_ACT_NONE ? nullptr : pre, act, T, N, ldp,
+                                     own && (dx || dW) ? (uint16_t*)(wp + w.dz) : nullptr, (float*)(wp + w.part), dbias,
+                                     stream))
+            return rc;
+        if (own) {
+            dz = (const uint16_t*)(wp + w.dz);
+            ldz = ldp;
+        }
+    }
+    DenseArgs g = {};
+    g.vec = 1;  // K % 8 == 0 and dense outputs
+    g.ldo = K;
+    if (dx) {  // [T, N] x [N, K]
+        g.a = dz;
+        g.lda = ldz;
+        g.b = W;
+        g.ldb = ldw;
+        g.M = (int)T;
+        g.N = (int)K;
+        g.K = (int)N;
+        g.b_cols = (int)K;
+        g.res = dx_add;
+        g.ldr = K;
+        g.out = dx;
+        if (const int rc = dense_launch(g, OP_KC, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
+    }
+    if (dW) {  // [T, N]^T x [T, K]
+        g.a = dz;
+        g.lda = ldz;
+        g.b = x;
+        g.ldb = ldx;
+        g.M = (int)N;
+        g.N = (int)K;
+        g.K = (int)T;
+        g.a_cols = (int)ldz;
+        g.b_cols = (int)K;
+        g.res = nullptr;
+        g.out = dW;
+        if (const int rc = dense_launch(g, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
+    }
+    return MOE_OK;
+}

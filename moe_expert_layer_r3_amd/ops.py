@@ -22,6 +22,8 @@ GEMM_TILE128 = 0x400  # 128 x 256 GEMM tiles instead of 256 x 256, OR'ed into a 
 GEMM_B_KN = 0x800     # weights given as [L, K, N] (a dgrad product on the forward weights), OR'ed likewise
 GEMM_THIN_SPLIT = 0x1000  # thin last 288-row m-tiles of a SwiGLU product split along K (workspace in out3)
 SRC_BF16, SRC_F32 = 0, 1
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}  # MOE_ACT_*
+SAVES = {"none": 0, "bf16": 1, "int8": 2}  # MOE_SAVE_*
 FLAG_BAD_ID, FLAG_DUP_ID, FLAG_ROW_CAP = 1, 2, 4
 ROW_ALIGN = 128
 
@@ -67,6 +69,20 @@ _SIGS = {
     "moe_gate_backward_parts": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_quant_fp8_rows_both": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _I32,
                                                _P]),
+    "moe_linear_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_linear": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I32, _I64, _P,
+                                  _P, _SZ, _P]),
+    "moe_linear_backward_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_linear_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _P,
+                                           _P, _SZ, _P]),
+    "moe_gated_ffn_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_gated_ffn": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _P,
+                                     _P, _SZ, _P]),
+    "moe_gated_ffn_backward_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_gated_ffn_backward": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P,
+                                              _P, _P, _P, _P, _SZ, _P]),
+    "moe_act_save": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_act_restore": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
 }
 
 GATE_PARTS = 16  # MOE_GATE_PARTS
@@ -480,3 +496,79 @@ def combine_backward(dy, y_perm, pair_row, w, rcap=None, quant=True, pow2=False)
     _call("moe_combine_backward", _p(dy), _p(y_perm), _p(pair_row), _p(w), T, k, d, rcap, _p(dyq), _p(dys),
           _p(d_gate), _flag(pow2), _stream(dev))
     return dyq, dys, d_gate
+
+
+# ---------------------------------------------------------------- activations in 8 bits
+
+class _Device:
+    """Makes a tensor's device current around a launch (kernels go to the
+    current device's queue); free when it is current already."""
+
+    def __init__(self, dev):
+        self.guard = None if dev.index is None or torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def rows_of(t, shape, dtype, name, dev=None):
+    """Row stride of a matrix whose rows may lie apart (a column slice of a wider
+    buffer); raises unless it has this shape and type, rows of adjacent
+    elements, and lives on ``dev``."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected shape {tuple(shape)} with adjacent row elements, got {tuple(t.shape)} "
+                         f"with strides {tuple(t.stride())}")
+    if not t.is_cuda or (dev is not None and t.device != dev):
+        raise ValueError(f"{name}: must live on the GPU{'' if dev is None else f' {dev}'}, got {t.device}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def act_save(x, out=None):
+    """Rows of bf16 x [rows, cols] in 8 bits: (q int8 [rows, cols], s fp32
+    [ceil(cols/128), rows]); ``out`` = (q, s) receives them without allocating."""
+    ld = rows_of(x, x.shape, torch.bfloat16, "x")
+    rows, cols = x.shape
+    dev = x.device
+    nb = (cols + 127) // 128
+    if out is None:
+        out = (torch.empty((rows, cols), dtype=torch.int8, device=dev),
+               torch.empty((nb, rows), dtype=torch.float32, device=dev))
+    q, s = out
+    _dense(q, (rows, cols), torch.int8, "q", dev)
+    _dense(s, (nb, rows), torch.float32, "s", dev)
+    with _Device(dev):
+        _call("moe_act_save", _p(x), ld, rows, cols, _p(q), _p(s), _stream(dev))
+    return q, s
+
+
+def act_restore(q, s, out=None):
+    """bf16 [rows, cols] that act_save's (q, s) stand for."""
+    rows, cols = q.shape
+    dev = _dev(q)
+    _dense(q, (rows, cols), torch.int8, "q", dev)
+    _dense(s, ((cols + 127) // 128, rows), torch.float32, "s", dev)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if out is None else out
+    _dense(x, (rows, cols), torch.bfloat16, "out", dev)
+    with _Device(dev):
+        _call("moe_act_restore", _p(q), _p(s), rows, cols, _p(x), _stream(dev))
+    return x
+
+
+def _dense(t, shape, dtype, name, dev):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def workspace_bytes(fn, *sizes):
+    """What a *_workspace function says for these sizes."""
+    n = _SZ(0)
+    _call(fn, *sizes, ctypes.byref(n))
+    return n.value
