@@ -20,6 +20,45 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& g, int& mt, int& nt,
     mt = grp * GM + in - nt * gm;
 }
 
+// Epilogue of ROWS x COLS fp32 results that the workgroup has put into LDS: rows
+// leave in order, 16 bytes of LDS (four columns) per thread and step, so that
+// global accesses are whole lines and the element-wise code exists once (written
+// out for every accumulator register it is too long to be unrolled).
+// 16-byte chunk c of row r lies at c ^ (r & 15), which spreads the 16 rows that a
+// wave's accumulators write together over the banks.
+__device__ __forceinline__ uint32_t stage_at(int cols, int r, int c) { return (uint32_t)(r * cols * 4 + ((c ^ (r & 15)) << 4)); }
+
+template <int EPI, int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void tile_epilogue(const DenseArgs& g, const uint8_t* sm, int64_t m0, int n0, int split) {
+    constexpr int PER_ROW = (EPI == EPI_GATE ? COLS / 2 : COLS) / 4, STEPS = ROWS * PER_ROW / THREADS, BATCH = 4;
+    static_assert(STEPS % BATCH == 0, "whole batches");
+    const int c = threadIdx.x % PER_ROW, r0 = threadIdx.x / PER_ROW;
+    const int n = n0 + c * 4;
+#pragma unroll 1
+    for (int s = 0; s < STEPS; s += BATCH) {
+        EpiIn<EPI> in[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) in[i].load(g, m0 + (s + i) * (THREADS / PER_ROW) + r0, n);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = (s + i) * (THREADS / PER_ROW) + r0;
+            const int64_t m = m0 + r;
+            const v4f v = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c));
+            if constexpr (EPI == EPI_GATE) {
+                const v4f u = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c + PER_ROW));
+                epi_gate(g, m, n, v, u, m < g.M && n < g.f);
+            } else if constexpr (EPI == EPI_LINEAR) {
+                if (m < g.M && n < g.N) epi_linear(g, m, n, v, in[i]);
+            } else if constexpr (EPI == EPI_DGATE) {
+                if (m < g.M && n < g.f) epi_dgate(g, m, n, v, in[i]);
+            } else {
+                if (m < g.M && n < g.part_ld)
+                    *reinterpret_cast<v4f*>(g.part + ((int64_t)split * g.M + m) * g.part_ld + n) = v;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- 64 x 64 wave tiles
 // WM x WN waves of 64 x 64, K steps of 64 double-buffered in LDS: while a step is
 // multiplied the next one is on its way.
@@ -168,76 +207,256 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
         phase_barrier();  // every wave has read this stage: the next issue may overwrite it
     }
 
-    // ---- epilogue: this lane holds C[m][n .. n + 3]
-    const int l15 = lane & 15, g4 = (lane >> 4) * 4;
-    if constexpr (EPI == EPI_GATE) {
-        const int nb = n0 + wn * 32 + g4;
+    // ---- epilogue: this lane holds C[m][n .. n + 3]; the K loop's last barrier freed LDS
+    const int l15 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) add_gate_bias(g, nb + j * 16, acc[i][j], acc[i][j + 2]);
-        if (g.save == MOE_SAVE_INT8) {
-            uint32_t* rowmax = reinterpret_cast<uint32_t*>(smem);  // [4 waves][2][BM]
+        for (int j = 0; j < 4; ++j) {
+            const int col = EPI == EPI_GATE ? (j >> 1) * 128 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16;
+            *reinterpret_cast<v4f*>(smem + stage_at(BN, wm * 64 + i * 16 + l15, col / 4 + g4)) = acc[i][j];
+        }
+    __syncthreads();
+    tile_epilogue<EPI, BM, BN, NW * 64>(g, smem, m0, n0, split);
+}
+
+// ---------------------------------------------------------------- 256 x 256 tiles
+// Eight waves as 2 (M) x 4 (N); a wave owns, of each 128-row half of A and each
+// 128-column half of B, 64 rows x 32 columns.  A K step of 64 is four phases of
+// 16 MFMAs, one per pair of halves, and the two waves of a SIMD (one of each M
+// half) run one half-phase apart: while one multiplies, the other reads its next
+// fragments from LDS and issues its share of the DMA, so the matrix core sees
+// MFMAs throughout.  Barriers separate the half-phases.
+//
+//   phase   fragments read     multiplies   DMA issued (2 per wave)
+//     0     A0, B0 of step k    A0 x B0     B1 of step k + 1
+//     1     B1                  A0 x B1     A1 of step k + 1
+//     2     A1                  A1 x B1     A0 of step k + 2
+//     3     -                   A1 x B0     B0 of step k + 2
+//
+// Two LDS stages of 64 KB.  A half's reads of phase p are complete for every wave
+// two phases later, which is when its refill is issued; a refill is awaited
+// (vmcnt(8): the four younger halves stay in flight) in the phase before it is
+// read, behind a barrier.  Steps past the end fill zeros without reading memory,
+// so the counts hold to the last step.
+template <int LA, int LB, int EPI>
+__global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
+    constexpr int HALF = 16384, STAGE = 4 * HALF;
+    static_assert(EPI != EPI_GATE || LB == OP_KC, "gated tiles pair 128 G with 128 U rows of W13");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    int mt, nt, split;
+    dense_tile(g, mt, nt, split);
+    const int64_t m0 = (int64_t)mt * 256;
+    const int n0 = nt * (EPI == EPI_GATE ? 128 : 256);
+    const int ks0 = split * g.ksteps;
+    const int ks1 = min(ks0 + g.ksteps, (g.K + DBK - 1) / DBK);
+    const int kend = min(g.K, ks1 * DBK);
+    const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+    // DMA: wave w moves segments 2w, 2w + 1 of every half: KC rows 16w .. + 15
+    // (one K chunk per lane), KS K rows 8w .. + 7
+    uint32_t va[2][2], vb[2][2];
+    const uint8_t *pa[2], *pb[2];
+    const KcLane la(lane, g.lda), lb(lane, g.ldb);
+    const uint32_t kseg = wave * 8 + (lane >> 4);  // KS: K row of segment 0, + 4 of segment 1
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (LA == OP_KC) {
+            const int64_t r0 = m0 + h * 128 + wave * 16;
+            pa[h] = (const uint8_t*)(g.a + r0 * g.lda);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                va[h][i] = r0 + 8 * i + la.row < g.M ? la.off + (uint32_t)(8 * i * g.lda * 2) : OOB;
+        } else {
+            const int64_t c0 = m0 + h * 128;
+            pa[h] = (const uint8_t*)(g.a + c0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
+                va[h][i] = c0 + c * 8 < g.a_cols ? k * (uint32_t)(g.lda * 2) + c * 16 : OOB;
+            }
+        }
+        if constexpr (LB == OP_KC) {
+            const int64_t r0 = (EPI == EPI_GATE ? (int64_t)h * g.f + n0 : n0 + (int64_t)h * 128) + wave * 16;
+            const int64_t lim = EPI == EPI_GATE ? (int64_t)(h + 1) * g.f : g.N;
+            pb[h] = (const uint8_t*)(g.b + r0 * g.ldb);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                vb[h][i] = r0 + 8 * i + lb.row < lim ? lb.off + (uint32_t)(8 * i * g.ldb * 2) : OOB;
+        } else {
+            const int64_t c0 = n0 + h * 128;
+            pb[h] = (const uint8_t*)(g.b + c0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
+                vb[h][i] = c0 + c * 8 < g.b_cols ? k * (uint32_t)(g.ldb * 2) + c * 16 : OOB;
+            }
+        }
+    }
+    const int64_t step_a = LA == OP_KC ? 128 : (int64_t)DBK * g.lda * 2;
+    const int64_t step_b = LB == OP_KC ? 128 : (int64_t)DBK * g.ldb * 2;
+    // half h of A (B) of K step ks into stage st
+    auto issue_a = [&](int st, int h, int ks) {
+        const int left = kend - ks * DBK;
+        const u32x4 d = buf_desc(pa[h] + ks * step_a);
+        const uint32_t s = sbase + st * STAGE + h * HALF + wave * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = LA == OP_KC ? (int)la.k : (int)kseg + 4 * i;
+            dma16b(d, k < left ? va[h][i] : OOB, s + i * 1024);
+        }
+    };
+    auto issue_b = [&](int st, int h, int ks) {
+        const int left = kend - ks * DBK;
+        const u32x4 d = buf_desc(pb[h] + ks * step_b);
+        const uint32_t s = sbase + st * STAGE + (2 + h) * HALF + wave * 2048;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = LB == OP_KC ? (int)lb.k : (int)kseg + 4 * i;
+            dma16b(d, k < left ? vb[h][i] : OOB, s + i * 1024);
+        }
+    };
+
+    // fragment read offsets in a half.  KC: 16-row subtiles are 2048 apart, the
+    // two K halves of a step one bit (64) apart.  KS: per subtile, K halves 8192
+    // apart.
+    uint32_t ra[4], rb[2];
+    if constexpr (LA == OP_KC) {
+        ra[0] = kc_frag(lane, wm * 64);
+        ra[1] = ra[0] ^ 64;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ra[i] = ks_frag(lane, wm * 4 + i);
+    }
+    if constexpr (LB == OP_KC) {
+        rb[0] = 2 * HALF + kc_frag(lane, wn * 32);
+        rb[1] = rb[0] ^ 64;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rb[j] = 2 * HALF + ks_frag(lane, wn * 2 + j);
+    }
+    u32x4 fa[4][2], fb[2][2][2];  // [subtile][K half], B: [half][subtile][K half]
+    auto read_a = [&](auto off_c, uint32_t base) {
+        constexpr int OFF = decltype(off_c)::value;
+        static_for<0, 4>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (LA == OP_KC) {
+                fa[i][0] = lds16<OFF + i * 2048>(base + ra[0]);
+                fa[i][1] = lds16<OFF + i * 2048>(base + ra[1]);
+            } else {
+                static_for<0, 2>([&](auto sc) {
+                    constexpr int s = decltype(sc)::value;
+                    const v2u lo = lds_tr16<OFF + s * 8192>(base + ra[i]), hi = lds_tr16<OFF + s * 8192 + 1024>(base + ra[i]);
+                    fa[i][s] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                });
+            }
+        });
+    };
+    auto read_b = [&](auto off_c, auto hc, uint32_t base) {
+        constexpr int OFF = decltype(off_c)::value, h = decltype(hc)::value;
+        static_for<0, 2>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            if constexpr (LB == OP_KC) {
+                fb[h][j][0] = lds16<OFF + j * 2048>(base + rb[0]);
+                fb[h][j][1] = lds16<OFF + j * 2048>(base + rb[1]);
+            } else {
+                static_for<0, 2>([&](auto sc) {
+                    constexpr int s = decltype(sc)::value;
+                    const v2u lo = lds_tr16<OFF + s * 8192>(base + rb[j]), hi = lds_tr16<OFF + s * 8192 + 1024>(base + rb[j]);
+                    fb[h][j][s] = u32x4{lo.x, lo.y, hi.x, hi.y};
+                });
+            }
+        });
+    };
+
+    v4f acc[2][2][4][2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    uint32_t mx = 0;
+                for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    auto multiply = [&](auto ac, auto bc) {
+        constexpr int a = decltype(ac)::value, b = decltype(bc)::value;
+        phase_barrier();
+        wait_lgkm0();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) mx = umax(mx, abs_bits(acc[i][2 * w + j][r]));
-                    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 16));
-                    mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 32));
-                    if (lane < 16) rowmax[(wn * 2 + w) * BM + wm * 64 + i * 16 + l15] = mx;
-                }
-            __syncthreads();
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = wm * 64 + i * 16 + l15;
-                const int64_t m = m0 + r;
+                for (int j = 0; j < 2; ++j) acc[a][b][i][j] = mfma_bf16(fb[b][j][s], fa[i][s], acc[a][b][i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        phase_barrier();
+    };
+    constexpr std::integral_constant<int, 0> c0;
+    constexpr std::integral_constant<int, 1> c1;
+    auto kstep = [&](auto st_c, int ks) {
+        constexpr int st = decltype(st_c)::value;
+        constexpr std::integral_constant<int, 0> s0;
+        constexpr std::integral_constant<int, HALF> s1;
+        uint32_t base = sbase + st * STAGE;
+        pin(base);
+        read_a(s0, base);
+        read_b(s0, c0, base);
+        issue_b(st ^ 1, 1, ks + 1);
+        wait_vmcnt<8>();  // B1 of this step
+        multiply(c0, c0);
+        pin(base);
+        read_b(s1, c1, base);
+        issue_a(st ^ 1, 1, ks + 1);
+        wait_vmcnt<8>();  // A1 of this step
+        multiply(c0, c1);
+        pin(base);
+        read_a(s1, base);
+        issue_a(st, 0, ks + 2);
+        multiply(c1, c1);
+        issue_b(st, 0, ks + 2);
+        wait_vmcnt<8>();  // A0, B0 of the next step
+        multiply(c1, c0);
+    };
+
+    issue_a(0, 0, ks0);
+    issue_b(0, 0, ks0);
+    issue_b(0, 1, ks0);
+    issue_a(0, 1, ks0);
+    issue_a(1, 0, ks0 + 1);
+    issue_b(1, 0, ks0 + 1);
+    wait_vmcnt<8>();
+    phase_barrier();
+    if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
+    for (int ks = ks0; ks < ks1; ks += 2) {
+        kstep(c0, ks);
+        if (ks + 1 < ks1) kstep(c1, ks + 1);
+    }
+    if (wm == 0) phase_barrier();
+    wait_vmcnt<0>();  // the fills past the end have landed: LDS may be reused or given up
+    phase_barrier();
+
+    // ---- epilogue, a 128-row half at a time
+    const int l15 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    uint32_t mx = 0;
+    for (int a = 0; a < 2; ++a) {
+        if (a) __syncthreads();
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) mx = umax(mx, rowmax[(v * 2 + w) * BM + r]);
-                    const Keep8 k = keep8_scale(mx);
-                    if (m >= g.M) continue;
-                    if (wn == 0 && lane < 16) g.gu_s[((int64_t)(w * (g.f >> 7)) + nt) * g.M + m] = k.s;
-                    int8_t* q = (int8_t*)g.gu + m * (2 * (int64_t)g.f) + (int64_t)w * g.f + nb;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const v4f v = acc[i][2 * w + j];
-                        *reinterpret_cast<uint32_t*>(q + j * 16) =
-                            pack_s8x4(keep8_code(v.x, k.inv), keep8_code(v.y, k.inv), keep8_code(v.z, k.inv),
-                                      keep8_code(v.w, k.inv));
-                    }
-                }
-            }
-        }
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + wm * 64 + i * 16 + l15;
-            if (m >= g.M) continue;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) epi_gate(g, m, nb + j * 16, acc[i][j], acc[i][j + 2]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + wm * 64 + i * 16 + l15;
-            if (m >= g.M) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + wn * 64 + j * 16 + g4;
-                if constexpr (EPI == EPI_LINEAR)
-                    epi_linear(g, m, n, acc[i][j]);
-                else if constexpr (EPI == EPI_DGATE)
-                    epi_dgate(g, m, n, acc[i][j]);
-                else if (n < g.part_ld)
-                    *reinterpret_cast<v4f*>(g.part + ((int64_t)split * g.M + m) * g.part_ld + n) = acc[i][j];
-            }
-        }
+                for (int j = 0; j < 2; ++j)
+                    *reinterpret_cast<v4f*>(smem + stage_at(256, wm * 64 + i * 16 + l15, b * 32 + wn * 8 + j * 4 + g4)) =
+                        acc[a][b][i][j];
+        __syncthreads();
+        tile_epilogue<EPI, 128, 256, 512>(g, smem, m0 + a * 128, n0, split);
     }
 }
 
@@ -260,33 +479,17 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs g, int splits)
         return s;
     };
     if constexpr (EPI == EPI_GATE) {
-        v4f G = sum(n), U = sum(g.f + n);
-        if (on) add_gate_bias(g, n, G, U);
-        if (g.save == MOE_SAVE_INT8) {
-            // f % 128 == 0: 32 lanes hold one block of a row
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const v4f v = w ? U : G;
-                uint32_t mx = umax(umax(abs_bits(v.x), abs_bits(v.y)), umax(abs_bits(v.z), abs_bits(v.w)));
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, o));
-                const Keep8 k = keep8_scale(mx);
-                if (on) {
-                    if ((threadIdx.x & 31) == 0) g.gu_s[((int64_t)(w * (g.f >> 7)) + (n >> 7)) * g.M + m] = k.s;
-                    *reinterpret_cast<uint32_t*>((int8_t*)g.gu + m * (2 * (int64_t)g.f) + (int64_t)w * g.f + n) =
-                        pack_s8x4(keep8_code(v.x, k.inv), keep8_code(v.y, k.inv), keep8_code(v.z, k.inv),
-                                  keep8_code(v.w, k.inv));
-                }
-            }
-        }
-        if (on) epi_gate(g, m, n, G, U);
+        const v4f G = sum(n), U = sum(g.f + n);
+        epi_gate(g, m, n, G, U, on);
     } else {
         if (!on) return;
+        EpiIn<EPI> in;
+        in.load(g, m, n);
         const v4f s = sum(n);
         if constexpr (EPI == EPI_DGATE)
-            epi_dgate(g, m, n, s);
+            epi_dgate(g, m, n, s, in);
         else
-            epi_linear(g, m, n, s);
+            epi_linear(g, m, n, s, in);
     }
 }
 
@@ -296,12 +499,23 @@ struct Shape {
     int64_t mt, nt;
     int bm, bn;  // bn: columns of C (h columns for EPI_GATE)
     int splits, ksteps;
+    bool wide;   // 256 x 256 tiles
 };
 // Tiles and K splits of an M x N product over K.  A product with fewer tiles
 // than two per compute unit is split along K, each piece at least 8 K steps.
 Shape dense_shape(int64_t M, int64_t N, int64_t K, int epi) {
     Shape s;
     const int64_t cols = epi == EPI_GATE ? N / 2 : N;
+    const int64_t wide_n = epi == EPI_GATE ? 128 : 256;
+    const int64_t wide_tiles = (M + 255) / 256 * ((cols + wide_n - 1) / wide_n);
+    s.wide = wide_tiles * 4 >= num_cus() * 3;
+    if (s.wide) {
+        s.mt = (M + 255) / 256;
+        s.nt = (cols + wide_n - 1) / wide_n;
+        s.splits = 1;
+        s.ksteps = (int)((K + DBK - 1) / DBK);
+        return s;
+    }
     s.bm = epi == EPI_GATE ? 64 : 128;
     s.bn = 128;
     s.mt = (M + s.bm - 1) / s.bm;
@@ -329,6 +543,12 @@ int launch_one(const DenseArgs& g, int splits, hipStream_t stream) {
     const int64_t grid = (int64_t)g.mt * g.nt * splits;
     dense_kernel<WM, WN, LA, LB, EPI><<<dim3((unsigned)grid), dim3(WM * WN * 64), 0, stream>>>(g);
     MOE_LAUNCH_CHECK("dense_kernel");
+    return MOE_OK;
+}
+template <int LA, int LB, int EPI>
+int launch_wide(const DenseArgs& g, hipStream_t stream) {
+    dense_wide_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt)), dim3(512), 0, stream>>>(g);
+    MOE_LAUNCH_CHECK("dense_wide_kernel");
     return MOE_OK;
 }
 template <int EPI>
@@ -368,6 +588,13 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         if (epi == EPI_GATE) return launch_sum<EPI_GATE>(g, s.splits, stream);
         if (epi == EPI_DGATE) return launch_sum<EPI_DGATE>(g, s.splits, stream);
         return launch_sum<EPI_LINEAR>(g, s.splits, stream);
+    }
+    if (s.wide) {
+        if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, stream);
+        if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, stream);
+        if (lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, stream);
+        if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI_LINEAR>(g, stream);
+        return launch_wide<OP_KS, OP_KS, EPI_LINEAR>(g, stream);
     }
     if (epi == EPI_GATE) return launch_one<1, 4, OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
     if (epi == EPI_DGATE) return launch_one<2, 2, OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);

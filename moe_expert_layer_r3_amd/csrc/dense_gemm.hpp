@@ -183,66 +183,118 @@ __device__ __forceinline__ v2u pack_bf16x4(float a, float b, float c, float d) {
     return v2u{cvt_bf16x2(a, b), cvt_bf16x2(c, d)};
 }
 
-// EPI_LINEAR for C[m, n .. n + 3]
-__device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n, v4f c) {
-    if (g.vec) {
-        if (n >= g.N) return;
-        float v[4] = {c.x, c.y, c.z, c.w}, t[4];
-        if (g.bias) {
+// What the epilogue of C[m, n .. n + 3] reads from memory, loaded ahead of its use.
+template <int EPI>
+struct EpiIn {
+    v2u a = {0u, 0u}, b = {0u, 0u};  // residual; saved G, U
+    float sa = 0.f, sb = 0.f;        // their 8-bit scales
+    __device__ __forceinline__ void load(const DenseArgs& g, int64_t m, int n) {
+        if constexpr (EPI == EPI_LINEAR) {
+            if (m >= g.M || n >= g.N || !g.res) return;
+            const uint16_t* p = g.res + m * g.ldr + n;
+            if (g.vec) {
+                a = *reinterpret_cast<const v2u*>(p);
+            } else {
+                const int left = g.N - n;
+                a.x = p[0] | (left > 1 ? (uint32_t)p[1] << 16 : 0u);
+                a.y = (left > 2 ? p[2] : 0u) | (left > 3 ? (uint32_t)p[3] << 16 : 0u);
+            }
+        } else if constexpr (EPI == EPI_DGATE) {
+            if (m >= g.M || n >= g.f) return;
+            const int64_t at = m * (2 * (int64_t)g.f) + n;
+            if (g.save == MOE_SAVE_INT8) {
+                const int64_t blk = n >> 7, nb = g.f >> 7;
+                sa = g.gu_s[blk * g.M + m];
+                sb = g.gu_s[(nb + blk) * g.M + m];
+                a.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at);
+                b.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at + g.f);
+            } else {
+                a = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + at);
+                b = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + at + g.f);
+            }
+        }
+    }
+};
+__device__ __forceinline__ void unpack_bf16x4(v2u w, float* v) {
+    v[0] = bf16_lo(w.x);
+    v[1] = bf16_hi(w.x);
+    v[2] = bf16_lo(w.y);
+    v[3] = bf16_hi(w.y);
+}
+
+// EPI_LINEAR for C[m, n .. n + 3], m < M, n < N
+__device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_LINEAR>& in) {
+    const int left = g.N - n;
+    float v[4] = {c.x, c.y, c.z, c.w}, t[4];
+    if (g.bias) {
+        if (g.vec) {
             load_bf16x4(g.bias + n, t);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += t[i];
-        }
-        if (g.pre) *reinterpret_cast<v2u*>(g.pre + m * g.N + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
-        if (g.act != MOE_ACT_NONE) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = act_value(g.act, v[i]);
+            for (int i = 0; i < 4; ++i)
+                if (i < left) v[i] += bf16_to_f32(g.bias[n + i]);
         }
-        if (g.res) {
-            load_bf16x4(g.res + m * g.ldr + n, t);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += t[i];
-        }
-        if (g.out_f32)
-            *reinterpret_cast<v4f*>((float*)g.out + m * g.ldo + n) = v4f{v[0], v[1], v[2], v[3]};
-        else
-            *reinterpret_cast<v2u*>((uint16_t*)g.out + m * g.ldo + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
-        return;
     }
+    if (g.pre) {
+        uint16_t* p = g.pre + m * g.N + n;
+        const v2u w = pack_bf16x4(v[0], v[1], v[2], v[3]);
+        if (g.vec) {
+            *reinterpret_cast<v2u*>(p) = w;
+        } else {
+            p[0] = (uint16_t)w.x;
+            if (left > 1) p[1] = (uint16_t)(w.x >> 16);
+            if (left > 2) p[2] = (uint16_t)w.y;
+            if (left > 3) p[3] = (uint16_t)(w.y >> 16);
+        }
+    }
+    if (g.act != MOE_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= g.N) return;
-        float v = c[i];
-        if (g.bias) v += bf16_to_f32(g.bias[n + i]);
-        if (g.pre) g.pre[m * g.N + n + i] = (uint16_t)cvt_bf16x2(v, 0.f);
-        v = act_value(g.act, v);
-        if (g.res) v += bf16_to_f32(g.res[m * g.ldr + n + i]);
-        if (g.out_f32)
-            ((float*)g.out)[m * g.ldo + n + i] = v;
-        else
-            ((uint16_t*)g.out)[m * g.ldo + n + i] = (uint16_t)cvt_bf16x2(v, 0.f);
+        for (int i = 0; i < 4; ++i) v[i] = act_value(g.act, v[i]);
+    }
+    if (g.res) {
+        unpack_bf16x4(in.a, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += t[i];
+    }
+    if (g.out_f32) {
+        float* p = (float*)g.out + m * g.ldo + n;
+        if (g.vec) {
+            *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) p[i] = v[i];
+        }
+    } else {
+        uint16_t* p = (uint16_t*)g.out + m * g.ldo + n;
+        const v2u w = pack_bf16x4(v[0], v[1], v[2], v[3]);
+        if (g.vec) {
+            *reinterpret_cast<v2u*>(p) = w;
+        } else {
+            p[0] = (uint16_t)w.x;
+            if (left > 1) p[1] = (uint16_t)(w.x >> 16);
+            if (left > 2) p[2] = (uint16_t)w.y;
+            if (left > 3) p[3] = (uint16_t)(w.y >> 16);
+        }
     }
 }
 
-// EPI_DGATE for dh[m, n .. n + 3] (n < f, f % 8 == 0): [dG, dU] and h from the
-// saved G, U
-__device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh) {
-    if (n >= g.f) return;
+// EPI_DGATE for dh[m, n .. n + 3], m < M, n < f (f % 8 == 0): [dG, dU] and h from
+// the saved G, U
+__device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh, const EpiIn<EPI_DGATE>& in) {
     float G[4], U[4];
     const int64_t at = m * (2 * (int64_t)g.f) + n;
     if (g.save == MOE_SAVE_INT8) {
-        const int64_t blk = n >> 7, nb = g.f >> 7;
-        const float sg = g.gu_s[blk * g.M + m], su = g.gu_s[(nb + blk) * g.M + m];
-        const uint32_t qg = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at);
-        const uint32_t qu = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at + g.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            G[i] = s8_of(qg, i) * sg;
-            U[i] = s8_of(qu, i) * su;
+            G[i] = s8_of(in.a.x, i) * in.sa;
+            U[i] = s8_of(in.b.x, i) * in.sb;
         }
     } else {
-        load_bf16x4((const uint16_t*)g.gu + at, G);
-        load_bf16x4((const uint16_t*)g.gu + at + g.f, U);
+        unpack_bf16x4(in.a, G);
+        unpack_bf16x4(in.b, U);
     }
     float dG[4], dU[4], h[4];
 #pragma unroll
@@ -258,9 +310,34 @@ __device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, 
     if (g.h) *reinterpret_cast<v2u*>(g.h + m * g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
 }
 
-// EPI_GATE without the 8-bit save for G, U[m, n .. n + 3] (bias already added)
-__device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, const v4f& G, const v4f& U) {
-    if (n >= g.f) return;
+// EPI_GATE for the sums G, U[m, n .. n + 3]; `on`: m < M and n < f.  With the 8-bit
+// save (f % 128 == 0) 32 adjacent lanes hold one 128-column block of a row, and
+// every lane of a wave calls.
+__device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v4f G, v4f U, bool on) {
+    if (on && g.bias) {
+        float t[4];
+        load_bf16x4(g.bias + n, t);
+        G += v4f{t[0], t[1], t[2], t[3]};
+        load_bf16x4(g.bias + g.f + n, t);
+        U += v4f{t[0], t[1], t[2], t[3]};
+    }
+    if (g.save == MOE_SAVE_INT8) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const v4f v = w ? U : G;
+            uint32_t mx = umax(umax(abs_bits(v.x), abs_bits(v.y)), umax(abs_bits(v.z), abs_bits(v.w)));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) mx = umax(mx, (uint32_t)__shfl_xor((int)mx, o));
+            const Keep8 k = keep8_scale(mx);
+            if (on) {
+                if ((threadIdx.x & 31) == 0) g.gu_s[((int64_t)(w * (g.f >> 7)) + (n >> 7)) * g.M + m] = k.s;
+                *reinterpret_cast<uint32_t*>((int8_t*)g.gu + m * (2 * (int64_t)g.f) + (int64_t)w * g.f + n) =
+                    pack_s8x4(keep8_code(v.x, k.inv), keep8_code(v.y, k.inv), keep8_code(v.z, k.inv),
+                              keep8_code(v.w, k.inv));
+            }
+        }
+    }
+    if (!on) return;
     float h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = act_value(g.act, G[i]) * U[i];
@@ -270,14 +347,6 @@ __device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, c
         *reinterpret_cast<v2u*>(p) = pack_bf16x4(G[0], G[1], G[2], G[3]);
         *reinterpret_cast<v2u*>(p + g.f) = pack_bf16x4(U[0], U[1], U[2], U[3]);
     }
-}
-__device__ __forceinline__ void add_gate_bias(const DenseArgs& g, int n, v4f& G, v4f& U) {
-    if (!g.bias || n >= g.f) return;
-    float t[4];
-    load_bf16x4(g.bias + n, t);
-    G += v4f{t[0], t[1], t[2], t[3]};
-    load_bf16x4(g.bias + g.f + n, t);
-    U += v4f{t[0], t[1], t[2], t[3]};
 }
 
 // ---------------------------------------------------------------- host side

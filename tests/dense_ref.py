@@ -19,8 +19,11 @@ ACT_ERR = 2.0 ** -20
 SLOPE = 1.13          # largest |act'| of silu (1.0998), gelu (1.1290), relu, sigmoid
 
 
+REF = ["cpu"]         # where the 64-bit forms are computed (large cases: on the GPU)
+
+
 def d64(t):
-    return None if t is None else t.detach().double().cpu()
+    return None if t is None else t.detach().to(REF[0]).double()
 
 
 def acc_err(K, a, b):

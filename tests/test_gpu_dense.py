@@ -6,6 +6,7 @@ import ctypes
 import pytest
 import torch
 
+import dense_ref
 from dense_ref import ACT_ERR, SLOPE, U16, acc_err, act, close, d64, keep8, spread
 from gpu_util import DEV, say
 from moe_expert_layer_r3_amd import ops
@@ -179,7 +180,7 @@ def check_ffn(T, d, f, name, save, bias, res, pad=0):
         close(p.gu, gu, e + U16 * (gu.abs() + e) + 1e-30, "gu")
         kept = d64(p.gu)
     else:
-        q, s = p.gu.cpu(), p.gu_s.cpu()
+        q, s = p.gu.to(X.device), p.gu_s.to(X.device)
         assert q.abs().max() <= 127
         amax = gu.abs().view(T, 2 * f // 128, 128).amax(2).t()
         worst = e.view(T, 2 * f // 128, 128).amax(2).t()
@@ -304,6 +305,30 @@ def test_ffn_gradient_against_differences():
             m = [mag @ A, mag.t() @ X, DY.abs().t() @ (gu[:, :f] * gu[:, f:] * SLOPE)][i]
             tol = 3 * U16 * 1.01 * (m * v.abs()).sum()
             assert abs((G * v).sum() - want) <= tol, (i, float((G * v).sum()), float(want), float(tol))
+
+
+# ---------------------------------------------------------------- 256 x 256 tiles
+
+@pytest.fixture
+def on_gpu():
+    dense_ref.REF[0] = DEV
+    yield
+    dense_ref.REF[0] = "cpu"
+
+
+@pytest.mark.parametrize("T, K, N", [(3300, 200, 4200), (3300, 4200, 72), (100, 4200, 3304), (64, 4104, 3301),
+                                     (4096, 64, 4096), (2305, 8, 5000), (3841, 136, 3841)])
+def test_linear_wide(on_gpu, T, K, N):
+    """Forward, data- and weight-gradient products of at least 192 tiles in turn;
+    K from less than one step to several, odd and even numbers of steps."""
+    check_linear(T, K, N, "silu", False, True, True, True, pad=8)
+    check_linear(T, K, N, "none", True, False, False, True)
+
+
+@pytest.mark.parametrize("T, d, f, save", [(3300, 72, 2104, "bf16"), (3300, 200, 4200, "bf16"), (3300, 136, 2176, "int8"),
+                                           (3300, 64, 4224, "int8"), (6000, 1000, 1032, "none")])
+def test_ffn_wide(on_gpu, T, d, f, save):
+    check_ffn(T, d, f, "silu", save, save == "bf16", True)
 
 
 # ---------------------------------------------------------------- 8-bit activations
