@@ -222,23 +222,21 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
 
 // ---------------------------------------------------------------- 256 x 256 tiles
 // Eight waves as 2 (M) x 4 (N); a wave owns, of each 128-row half of A and each
-// 128-column half of B, 64 rows x 32 columns.  A K step of 64 is four phases of
-// 16 MFMAs, one per pair of halves, and the two waves of a SIMD (one of each M
-// half) run one half-phase apart: while one multiplies, the other reads its next
-// fragments from LDS and issues its share of the DMA, so the matrix core sees
-// MFMAs throughout.  Barriers separate the half-phases.
+// 128-column half of B, 64 rows x 32 columns.  A K step of 64 is two phases of 32
+// MFMAs (one half of A against both halves of B), and the two waves of a SIMD (one
+// of each M half) run one half-phase apart: while one multiplies, the other reads
+// its next fragments from LDS and issues its share of the DMA, so the matrix core
+// sees MFMAs throughout.  Barriers separate the half-phases.
 //
-//   phase   fragments read     multiplies   DMA issued (2 per wave)
-//     0     A0, B0 of step k    A0 x B0     B1 of step k + 1
-//     1     B1                  A0 x B1     A1 of step k + 1
-//     2     A1                  A1 x B1     A0 of step k + 2
-//     3     -                   A1 x B0     B0 of step k + 2
+//   phase   fragments read          multiplies     DMA issued (2 per wave and half)
+//     0     A0, B0, B1 of step k     A0 x B0, B1    A1 of step k + 1
+//     1     A1                       A1 x B0, B1    A0, B0, B1 of step k + 2
 //
-// Two LDS stages of 64 KB.  A half's reads of phase p are complete for every wave
-// two phases later, which is when its refill is issued; a refill is awaited
-// (vmcnt(8): the four younger halves stay in flight) in the phase before it is
-// read, behind a barrier.  Steps past the end fill zeros without reading memory,
-// so the counts hold to the last step.
+// Two LDS stages of 64 KB.  A wave's reads are complete before the barrier that
+// ends its reading half-phase, so what phase p read is refilled in phase p + 1; a
+// refill is awaited (vmcnt(8): the younger ones stay in flight) one phase before it
+// is read, ahead of a barrier.  Steps past the end fill zeros without reading
+// memory, so the counts hold to the last step.
 template <int LA, int LB, int EPI>
 __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     constexpr int HALF = 16384, STAGE = 4 * HALF;
@@ -383,46 +381,42 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](auto ac, auto bc) {
-        constexpr int a = decltype(ac)::value, b = decltype(bc)::value;
-        phase_barrier();
+    auto multiply = [&](auto ac) {
+        constexpr int a = decltype(ac)::value;
         wait_lgkm0();
-        __builtin_amdgcn_sched_barrier(0);
+        phase_barrier();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[a][b][i][j] = mfma_bf16(fb[b][j][s], fa[i][s], acc[a][b][i][j]);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[a][b][i][j] = mfma_bf16(fb[b][j][s], fa[i][s], acc[a][b][i][j]);
         __builtin_amdgcn_s_setprio(0);
         phase_barrier();
     };
     constexpr std::integral_constant<int, 0> c0;
     constexpr std::integral_constant<int, 1> c1;
+    constexpr std::integral_constant<int, HALF> half1;
     auto kstep = [&](auto st_c, int ks) {
         constexpr int st = decltype(st_c)::value;
-        constexpr std::integral_constant<int, 0> s0;
-        constexpr std::integral_constant<int, HALF> s1;
         uint32_t base = sbase + st * STAGE;
         pin(base);
-        read_a(s0, base);
-        read_b(s0, c0, base);
-        issue_b(st ^ 1, 1, ks + 1);
-        wait_vmcnt<8>();  // B1 of this step
-        multiply(c0, c0);
-        pin(base);
-        read_b(s1, c1, base);
+        read_a(c0, base);
+        read_b(c0, c0, base);
+        read_b(half1, c1, base);
         issue_a(st ^ 1, 1, ks + 1);
         wait_vmcnt<8>();  // A1 of this step
-        multiply(c0, c1);
+        multiply(c0);
         pin(base);
-        read_a(s1, base);
+        read_a(half1, base);
         issue_a(st, 0, ks + 2);
-        multiply(c1, c1);
         issue_b(st, 0, ks + 2);
-        wait_vmcnt<8>();  // A0, B0 of the next step
-        multiply(c1, c0);
+        issue_b(st, 1, ks + 2);
+        wait_vmcnt<8>();  // A0, B0, B1 of the next step
+        multiply(c1);
     };
 
     issue_a(0, 0, ks0);
@@ -431,6 +425,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     issue_a(0, 1, ks0);
     issue_a(1, 0, ks0 + 1);
     issue_b(1, 0, ks0 + 1);
+    issue_b(1, 1, ks0 + 1);
     wait_vmcnt<8>();
     phase_barrier();
     if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
