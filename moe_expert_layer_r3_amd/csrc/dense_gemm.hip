@@ -228,15 +228,16 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
 // its next fragments from LDS and issues its share of the DMA, so the matrix core
 // sees MFMAs throughout.  Barriers separate the half-phases.
 //
-//   phase   fragments read          multiplies     DMA issued (2 per wave and half)
-//     0     A0, B0, B1 of step k     A0 x B0, B1    A1 of step k + 1
-//     1     A1                       A1 x B0, B1    A0, B0, B1 of step k + 2
+//   phase   fragments read              multiplies     DMA issued (2 per wave and half)
+//     0     A0, B1 of step k             A0 x B0, B1    A1 of step k + 1, B0 of step k + 2
+//     1     A1 of step k, B0 of k + 1    A1 x B0, B1    A0, B1 of step k + 2
 //
+// so that both phases read 12 fragments and issue four instructions per wave.
 // Two LDS stages of 64 KB.  A wave's reads are complete before the barrier that
 // ends its reading half-phase, so what phase p read is refilled in phase p + 1; a
-// refill is awaited (vmcnt(8): the younger ones stay in flight) one phase before it
-// is read, ahead of a barrier.  Steps past the end fill zeros without reading
-// memory, so the counts hold to the last step.
+// refill is awaited (vmcnt(8): those of the last two phases stay in flight) one
+// phase before it is read, ahead of a barrier.  Steps past the end fill zeros
+// without reading memory, so the counts hold to the last step.
 template <int LA, int LB, int EPI>
 __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     constexpr int HALF = 16384, STAGE = 4 * HALF;
@@ -337,7 +338,8 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) rb[j] = 2 * HALF + ks_frag(lane, wn * 2 + j);
     }
-    u32x4 fa[4][2], fb[2][2][2];  // [subtile][K half], B: [half][subtile][K half]
+    // [subtile][K half]; B: half 0 of even and odd steps, half 1
+    u32x4 fa[4][2], fb[3][2][2];
     auto read_a = [&](auto off_c, uint32_t base) {
         constexpr int OFF = decltype(off_c)::value;
         static_for<0, 4>([&](auto ic) {
@@ -355,7 +357,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
         });
     };
     auto read_b = [&](auto off_c, auto hc, uint32_t base) {
-        constexpr int OFF = decltype(off_c)::value, h = decltype(hc)::value;
+        constexpr int OFF = decltype(off_c)::value, h = decltype(hc)::value;  // h: index in fb
         static_for<0, 2>([&](auto jc) {
             constexpr int j = decltype(jc)::value;
             if constexpr (LB == OP_KC) {
@@ -381,8 +383,8 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    auto multiply = [&](auto ac) {
-        constexpr int a = decltype(ac)::value;
+    auto multiply = [&](auto ac, auto st_c) {
+        constexpr int a = decltype(ac)::value, st = decltype(st_c)::value;
         wait_lgkm0();
         phase_barrier();
         __builtin_amdgcn_s_setprio(1);
@@ -393,41 +395,52 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[a][b][i][j] = mfma_bf16(fb[b][j][s], fa[i][s], acc[a][b][i][j]);
+                    for (int j = 0; j < 2; ++j)
+                        acc[a][b][i][j] = mfma_bf16(fb[b ? 2 : st][j][s], fa[i][s], acc[a][b][i][j]);
         __builtin_amdgcn_s_setprio(0);
         phase_barrier();
     };
     constexpr std::integral_constant<int, 0> c0;
     constexpr std::integral_constant<int, 1> c1;
+    constexpr std::integral_constant<int, 2> c2;
     constexpr std::integral_constant<int, HALF> half1;
     auto kstep = [&](auto st_c, int ks) {
         constexpr int st = decltype(st_c)::value;
-        uint32_t base = sbase + st * STAGE;
+        constexpr std::integral_constant<int, st ^ 1> other;
+        uint32_t base = sbase + st * STAGE, next = sbase + (st ^ 1) * STAGE;
         pin(base);
         read_a(c0, base);
-        read_b(c0, c0, base);
-        read_b(half1, c1, base);
-        issue_a(st ^ 1, 1, ks + 1);
-        wait_vmcnt<8>();  // A1 of this step
-        multiply(c0);
-        pin(base);
-        read_a(half1, base);
-        issue_a(st, 0, ks + 2);
+        read_b(half1, c2, base);
         issue_b(st, 0, ks + 2);
+        issue_a(st ^ 1, 1, ks + 1);
+        wait_vmcnt<8>();  // A1 of this step, B0 of the next
+        multiply(c0, st_c);
+        pin(base);
+        pin(next);
+        read_a(half1, base);
+        read_b(c0, other, next);
+        issue_a(st, 0, ks + 2);
         issue_b(st, 1, ks + 2);
-        wait_vmcnt<8>();  // A0, B0, B1 of the next step
-        multiply(c1);
+        wait_vmcnt<8>();  // A0, B1 of the next step
+        multiply(c1, st_c);
     };
 
-    issue_a(0, 0, ks0);
     issue_b(0, 0, ks0);
+    issue_a(0, 0, ks0);
     issue_b(0, 1, ks0);
+    issue_b(1, 0, ks0 + 1);
     issue_a(0, 1, ks0);
     issue_a(1, 0, ks0 + 1);
-    issue_b(1, 0, ks0 + 1);
     issue_b(1, 1, ks0 + 1);
     wait_vmcnt<8>();
     phase_barrier();
+    {
+        uint32_t base = sbase;
+        pin(base);
+        read_b(c0, c0, base);
+        wait_lgkm0();
+        phase_barrier();
+    }
     if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
     for (int ks = ks0; ks < ks1; ks += 2) {
         kstep(c0, ks);
