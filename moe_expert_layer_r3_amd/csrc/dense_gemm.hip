@@ -16,8 +16,10 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& g, int& mt, int& nt,
     const int grp = t / (GM * g.nt);
     const int gm = min(GM, g.mt - grp * GM);
     const int in = t - grp * GM * g.nt;
-    nt = in / gm;
-    mt = grp * GM + in - nt * gm;
+    // uniform values, kept in SGPRs so that operand addresses are scalar arithmetic
+    split = __builtin_amdgcn_readfirstlane(split);
+    nt = __builtin_amdgcn_readfirstlane(in / gm);
+    mt = __builtin_amdgcn_readfirstlane(grp * GM + in - nt * gm);
 }
 
 // Epilogue of ROWS x COLS fp32 results that the workgroup has put into LDS: rows
@@ -29,35 +31,57 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& g, int& mt, int& nt,
 __device__ __forceinline__ uint32_t stage_at(int cols, int r, int c) { return (uint32_t)(r * cols * 4 + ((c ^ (r & 15)) << 4)); }
 
 template <int EPI, int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void tile_epilogue(const DenseArgs& g, const uint8_t* sm, int64_t m0, int n0, int split) {
-    constexpr int PER_ROW = (EPI == EPI_GATE ? COLS / 2 : COLS) / 4, STEPS = ROWS * PER_ROW / THREADS, BATCH = 4;
+struct TileEpilogue {
+    static constexpr int PER_ROW = (EPI == EPI_GATE ? COLS / 2 : COLS) / 4, STEPS = ROWS * PER_ROW / THREADS;
+    // What the steps read from memory is loaded a batch ahead (the first one before
+    // the results are staged).  The loop stays rolled: its code is long.
+    static constexpr bool READS = EPI == EPI_LINEAR || is_dgate(EPI) || EPI == EPI_PLAIN;
+    static constexpr int BATCH = EPI == EPI_PLAIN && STEPS % 8 == 0 ? 8 : 4;
     static_assert(STEPS % BATCH == 0, "whole batches");
-    const int c = threadIdx.x % PER_ROW, r0 = threadIdx.x / PER_ROW;
-    const int n = n0 + c * 4;
-#pragma unroll 1
-    for (int s = 0; s < STEPS; s += BATCH) {
-        EpiIn<EPI> in[BATCH];
+    EpiIn<EPI> in[READS ? BATCH : 1];
+    // this thread's first row; where a wave takes one row, a scalar
+    static __device__ __forceinline__ int first_row() {
+        const int r = threadIdx.x / PER_ROW;
+        return PER_ROW % 64 == 0 ? __builtin_amdgcn_readfirstlane(r) : r;
+    }
+    __device__ __forceinline__ void load(const DenseArgs& g, int64_t m0, int n0, int s = 0) {
+        if constexpr (READS) {
+            const int c = threadIdx.x % PER_ROW, r0 = first_row();
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) in[i].load(g, m0 + (s + i) * (THREADS / PER_ROW) + r0, n);
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int r = (s + i) * (THREADS / PER_ROW) + r0;
-            const int64_t m = m0 + r;
-            const v4f v = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c));
-            if constexpr (EPI == EPI_GATE) {
-                const v4f u = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c + PER_ROW));
-                epi_gate(g, m, n, v, u, m < g.M && n < g.f);
-            } else if constexpr (EPI == EPI_LINEAR) {
-                if (m < g.M && n < g.N) epi_linear(g, m, n, v, in[i]);
-            } else if constexpr (EPI == EPI_DGATE) {
-                if (m < g.M && n < g.f) epi_dgate(g, m, n, v, in[i]);
-            } else {
-                if (m < g.M && n < g.part_ld)
-                    *reinterpret_cast<v4f*>(g.part + ((int64_t)split * g.M + m) * g.part_ld + n) = v;
-            }
+            for (int i = 0; i < BATCH; ++i) in[i].load(g, m0 + (s + i) * (THREADS / PER_ROW) + r0, n0 + c * 4);
         }
     }
-}
+    __device__ __forceinline__ void step(const DenseArgs& g, const uint8_t* sm, int64_t m0, int n0, int split, int s,
+                                         const EpiIn<EPI>& in) {
+        const int c = threadIdx.x % PER_ROW, r = s * (THREADS / PER_ROW) + first_row();
+        const int n = n0 + c * 4;
+        const int64_t m = m0 + r;
+        const v4f v = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c));
+        if constexpr (EPI == EPI_GATE) {
+            const v4f u = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c + PER_ROW));
+            epi_gate(g, m, n, v, u, m < g.M && n < g.f);
+        } else if constexpr (EPI == EPI_LINEAR) {
+            if (m < g.M && n < g.N) epi_linear(g, m, n, v, in);
+        } else if constexpr (EPI == EPI_PLAIN) {
+            if (m < g.M && n < g.N) epi_plain(g, m, n, v, in);
+        } else if constexpr (is_dgate(EPI)) {
+            if (m < g.M && n < g.f) epi_dgate(g, m, n, v, in);
+        } else {
+            if (m < g.M && n < g.part_ld)
+                *reinterpret_cast<v4f*>(g.part + ((int64_t)split * g.M + m) * g.part_ld + n) = v;
+        }
+    }
+    __device__ __forceinline__ void run(const DenseArgs& g, const uint8_t* sm, int64_t m0, int n0, int split) {
+#pragma unroll 1
+        for (int s = 0; s < STEPS; s += BATCH) {
+            TileEpilogue next;
+            if (READS && s + BATCH < STEPS) next.load(g, m0, n0, s + BATCH);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) step(g, sm, m0, n0, split, s + i, in[READS ? i : 0]);
+            *this = next;
+        }
+    }
+};
 
 // ---------------------------------------------------------------- 64 x 64 wave tiles
 // WM x WN waves of 64 x 64, K steps of 64 double-buffered in LDS: while a step is
@@ -67,6 +91,7 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
     constexpr int BM = WM * 64, BN = WN * 64, NW = WM * WN;
     constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
     constexpr int ASEG = BM / 8 / NW, BSEG = BN / 8 / NW;
+    static_assert(ASEG % 2 == 0 && BSEG % 2 == 0, "segments move in pairs");
     static_assert(LA == OP_KC || BM % 128 == 0, "KS images are 128 columns wide");
     static_assert(LB == OP_KC || BN % 128 == 0, "KS images are 128 columns wide");
     static_assert(EPI != EPI_GATE || (WN == 4 && LB == OP_KC), "gated tiles pair 128 G with 128 U columns");
@@ -140,9 +165,11 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
         const uint32_t sA = sbase + st * STAGE + wave * ASEG * 1024;
         const uint32_t sB = sbase + st * STAGE + A_BYTES + wave * BSEG * 1024;
 #pragma unroll
-        for (int i = 0; i < ASEG; ++i) dma16b(da, ka[i] < left ? va[i] : OOB, sA + i * 1024);
+        for (int i = 0; i < ASEG; i += 2)
+            dma16b2(da, ka[i] < left ? va[i] : OOB, ka[i + 1] < left ? va[i + 1] : OOB, sA + i * 1024);
 #pragma unroll
-        for (int i = 0; i < BSEG; ++i) dma16b(db, kb[i] < left ? vb[i] : OOB, sB + i * 1024);
+        for (int i = 0; i < BSEG; i += 2)
+            dma16b2(db, kb[i] < left ? vb[i] : OOB, kb[i + 1] < left ? vb[i + 1] : OOB, sB + i * 1024);
         pa += step_a;
         pb += step_b;
     };
@@ -209,6 +236,8 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
 
     // ---- epilogue: this lane holds C[m][n .. n + 3]; the K loop's last barrier freed LDS
     const int l15 = lane & 15, g4 = lane >> 4;
+    TileEpilogue<EPI, BM, BN, NW * 64> epi;
+    epi.load(g, m0, n0);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -217,7 +246,7 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
             *reinterpret_cast<v4f*>(smem + stage_at(BN, wm * 64 + i * 16 + l15, col / 4 + g4)) = acc[i][j];
         }
     __syncthreads();
-    tile_epilogue<EPI, BM, BN, NW * 64>(g, smem, m0, n0, split);
+    epi.run(g, smem, m0, n0, split);
 }
 
 // ---------------------------------------------------------------- 256 x 256 tiles
@@ -303,21 +332,15 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
         const int left = kend - ks * DBK;
         const u32x4 d = buf_desc(pa[h] + ks * step_a);
         const uint32_t s = sbase + st * STAGE + h * HALF + wave * 2048;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = LA == OP_KC ? (int)la.k : (int)kseg + 4 * i;
-            dma16b(d, k < left ? va[h][i] : OOB, s + i * 1024);
-        }
+        const int k0 = LA == OP_KC ? (int)la.k : (int)kseg, k1 = LA == OP_KC ? (int)la.k : (int)kseg + 4;
+        dma16b2(d, k0 < left ? va[h][0] : OOB, k1 < left ? va[h][1] : OOB, s);
     };
     auto issue_b = [&](int st, int h, int ks) {
         const int left = kend - ks * DBK;
         const u32x4 d = buf_desc(pb[h] + ks * step_b);
         const uint32_t s = sbase + st * STAGE + (2 + h) * HALF + wave * 2048;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int k = LB == OP_KC ? (int)lb.k : (int)kseg + 4 * i;
-            dma16b(d, k < left ? vb[h][i] : OOB, s + i * 1024);
-        }
+        const int k0 = LB == OP_KC ? (int)lb.k : (int)kseg, k1 = LB == OP_KC ? (int)lb.k : (int)kseg + 4;
+        dma16b2(d, k0 < left ? vb[h][0] : OOB, k1 < left ? vb[h][1] : OOB, s);
     };
 
     // fragment read offsets in a half.  KC: 16-row subtiles are 2048 apart, the
@@ -454,6 +477,8 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     const int l15 = lane & 15, g4 = lane >> 4;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
+        TileEpilogue<EPI, 128, 256, 512> epi;
+        epi.load(g, m0 + a * 128, n0);
         if (a) __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -464,7 +489,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
                     *reinterpret_cast<v4f*>(smem + stage_at(256, wm * 64 + i * 16 + l15, b * 32 + wn * 8 + j * 4 + g4)) =
                         acc[a][b][i][j];
         __syncthreads();
-        tile_epilogue<EPI, 128, 256, 512>(g, smem, m0 + a * 128, n0, split);
+        epi.run(g, smem, m0 + a * 128, n0, split);
     }
 }
 
@@ -494,8 +519,10 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs g, int splits)
         EpiIn<EPI> in;
         in.load(g, m, n);
         const v4f s = sum(n);
-        if constexpr (EPI == EPI_DGATE)
+        if constexpr (is_dgate(EPI))
             epi_dgate(g, m, n, s, in);
+        else if constexpr (EPI == EPI_PLAIN)
+            epi_plain(g, m, n, s, in);
         else
             epi_linear(g, m, n, s, in);
     }
@@ -583,6 +610,8 @@ size_t dense_ws(int64_t M, int64_t N, int64_t K, int epi) {
 
 int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes, hipStream_t stream) {
     const Shape s = dense_shape(g.M, g.N, g.K, epi);
+    if (epi == EPI_DGATE && g.save == MOE_SAVE_INT8) epi = EPI_DGATE8;
+    if (epi == EPI_LINEAR && g.vec && !g.out_f32 && !g.pre && g.act == MOE_ACT_NONE) epi = EPI_PLAIN;
     MOE_REQUIRE(s.mt * s.nt * s.splits < (1ll << 31), MOE_ERR_SHAPE, "product of %d x %d has too many tiles", g.M, g.N);
     g.mt = (int)s.mt;
     g.nt = (int)s.nt;
@@ -595,18 +624,25 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         if (rc != MOE_OK) return rc;
         if (epi == EPI_GATE) return launch_sum<EPI_GATE>(g, s.splits, stream);
         if (epi == EPI_DGATE) return launch_sum<EPI_DGATE>(g, s.splits, stream);
+        if (epi == EPI_DGATE8) return launch_sum<EPI_DGATE8>(g, s.splits, stream);
+        if (epi == EPI_PLAIN) return launch_sum<EPI_PLAIN>(g, s.splits, stream);
         return launch_sum<EPI_LINEAR>(g, s.splits, stream);
     }
     if (s.wide) {
         if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, stream);
         if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, stream);
-        if (lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, stream);
-        if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI_LINEAR>(g, stream);
-        return launch_wide<OP_KS, OP_KS, EPI_LINEAR>(g, stream);
+        if (epi == EPI_DGATE8) return launch_wide<OP_KC, OP_KS, EPI_DGATE8>(g, stream);
+        // (data and weight gradients are always EPI_PLAIN)
+        if (epi == EPI_LINEAR) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, stream);
+        if (lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI_PLAIN>(g, stream);
+        if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI_PLAIN>(g, stream);
+        return launch_wide<OP_KS, OP_KS, EPI_PLAIN>(g, stream);
     }
     if (epi == EPI_GATE) return launch_one<1, 4, OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
     if (epi == EPI_DGATE) return launch_one<2, 2, OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);
-    return launch_layout<EPI_LINEAR>(g, la, lb, 1, stream);
+    if (epi == EPI_DGATE8) return launch_one<2, 2, OP_KC, OP_KS, EPI_DGATE8>(g, 1, stream);
+    if (epi == EPI_LINEAR) return launch_one<2, 2, OP_KC, OP_KC, EPI_LINEAR>(g, 1, stream);
+    return launch_layout<EPI_PLAIN>(g, la, lb, 1, stream);
 }
 
 // ---------------------------------------------------------------- column sums, zeros
@@ -716,12 +752,10 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, con
                     }
             }
             if (act != MOE_ACT_NONE) {
+                float val[4], sl[4];
+                act_both4(act, p, val, sl);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float val, sl;
-                    act_both(act, p[i], val, sl);
-                    v[i] *= sl;
-                }
+                for (int i = 0; i < 4; ++i) v[i] *= sl[i];
             }
             if (dz) *reinterpret_cast<v2u*>(dz + t * ldz + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
 #pragma unroll

@@ -18,7 +18,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int DBK = 64;  // K step: 128 bytes of a KC row, 64 rows of a KS matrix
 
-enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3 };
+// EPI_PLAIN: EPI_LINEAR's common form (bf16 out = C + bias + residual, vec);
+// EPI_DGATE8: EPI_DGATE from the 8-bit [G, U]
+enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3, EPI_PLAIN = 4, EPI_DGATE8 = 5 };
+constexpr bool is_dgate(int epi) { return epi == EPI_DGATE || epi == EPI_DGATE8; }
 
 struct DenseArgs {
     const uint16_t* a;  // KC [M, lda] / KS [K, lda]
@@ -48,42 +51,71 @@ struct DenseArgs {
 };
 
 // ---------------------------------------------------------------- activations
-// act(z) and act'(z); `act` is uniform.  sigmoid from the hardware exp2 and
-// reciprocal (about 1 ulp each).
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case MOE_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);  // NaN stays NaN
-        case MOE_ACT_SILU: return silu(z);
-        case MOE_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        case MOE_ACT_SIGMOID: return sigmoid_fast(z);
-        default: return z;
-    }
-}
-__device__ __forceinline__ void act_both(int act, float z, float& v, float& slope) {
+// act(z) and act'(z) of four values; `act` is uniform.  sigmoid from the hardware
+// exp2 and reciprocal (about 1 ulp each).
+__device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * (1.f + erff(z * 0.70710678118654752f)); }
+__device__ __forceinline__ float relu(float z) { return z > 0.f ? z : (z == z ? 0.f : z); }  // NaN stays NaN
+__device__ __forceinline__ void act_value4(int act, const float* z, float* v) {
     switch (act) {
         case MOE_ACT_RELU:
-            v = z > 0.f ? z : (z == z ? 0.f : z);
-            slope = z > 0.f ? 1.f : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = relu(z[i]);
             return;
-        case MOE_ACT_SILU: {
-            const float s = sigmoid_fast(z);
-            v = z * s;
-            slope = s * (1.f + z * (1.f - s));
+        case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = silu(z[i]);
             return;
-        }
-        case MOE_ACT_GELU: {
-            const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-            v = z * c;
-            slope = c + z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z) * 0.39894228040143268f;
+        case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = z[i] * gelu_cdf(z[i]);
             return;
-        }
-        case MOE_ACT_SIGMOID: {
-            const float s = sigmoid_fast(z);
-            v = s;
-            slope = s * (1.f - s);
+        case MOE_ACT_SIGMOID:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = sigmoid_fast(z[i]);
             return;
-        }
-        default: v = z; slope = 1.f; return;
+        default:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = z[i];
+    }
+}
+__device__ __forceinline__ void act_both4(int act, const float* z, float* v, float* slope) {
+    switch (act) {
+        case MOE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = relu(z[i]);
+                slope[i] = z[i] > 0.f ? 1.f : 0.f;
+            }
+            return;
+        case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = sigmoid_fast(z[i]);
+                v[i] = z[i] * s;
+                slope[i] = s + v[i] * (1.f - s);
+            }
+            return;
+        case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float c = gelu_cdf(z[i]);
+                v[i] = z[i] * c;
+                slope[i] = c + z[i] * __builtin_amdgcn_exp2f(-0.72134752044448170f * z[i] * z[i]) * 0.39894228040143268f;
+            }
+            return;
+        case MOE_ACT_SIGMOID:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = sigmoid_fast(z[i]);
+                slope[i] = v[i] * (1.f - v[i]);
+            }
+            return;
+        default:
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = z[i];
+                slope[i] = 1.f;
+            }
     }
 }
 
@@ -121,8 +153,20 @@ __device__ __forceinline__ u32x4 buf_desc(const void* base) {
                  (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xFFFFu)), 0x7FFFFFF0u,
                  0x00020000u};
 }
-__device__ __forceinline__ void dma16b(const u32x4& desc, uint32_t voff, uint32_t lds) {
-    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(desc), "{m0}"(lds) : "memory");
+// Two 1 KB segments to adjacent LDS (lds, lds + 1024).  The waits that the
+// compiler cannot insert around inline assembly are part of it: five states
+// between a vector instruction's write of a descriptor SGPR (v_readfirstlane) and
+// the load that reads it, one between a write of M0 and the load.
+__device__ __forceinline__ void dma16b2(const u32x4& desc, uint32_t voff0, uint32_t voff1, uint32_t lds) {
+    asm volatile(
+        "s_nop 4\n\t"
+        "buffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+        "s_add_u32 m0, m0, 0x400\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, 0 offen lds"
+        : "+{m0}"(lds)
+        : "v"(voff0), "v"(voff1), "s"(desc)
+        : "memory", "scc");
 }
 
 // Transposing LDS read: the 16 lanes of a group supply 4 K rows x 16 columns
@@ -184,33 +228,36 @@ __device__ __forceinline__ v2u pack_bf16x4(float a, float b, float c, float d) {
 }
 
 // What the epilogue of C[m, n .. n + 3] reads from memory, loaded ahead of its use.
+// Loads are not predicated (places past the matrix read its last row or first
+// columns instead), so that a batch of them is in flight at a time.
 template <int EPI>
 struct EpiIn {
     v2u a = {0u, 0u}, b = {0u, 0u};  // residual; saved G, U
     float sa = 0.f, sb = 0.f;        // their 8-bit scales
     __device__ __forceinline__ void load(const DenseArgs& g, int64_t m, int n) {
-        if constexpr (EPI == EPI_LINEAR) {
-            if (m >= g.M || n >= g.N || !g.res) return;
-            const uint16_t* p = g.res + m * g.ldr + n;
-            if (g.vec) {
-                a = *reinterpret_cast<const v2u*>(p);
-            } else {
-                const int left = g.N - n;
-                a.x = p[0] | (left > 1 ? (uint32_t)p[1] << 16 : 0u);
-                a.y = (left > 2 ? p[2] : 0u) | (left > 3 ? (uint32_t)p[3] << 16 : 0u);
-            }
-        } else if constexpr (EPI == EPI_DGATE) {
-            if (m >= g.M || n >= g.f) return;
-            const int64_t at = m * (2 * (int64_t)g.f) + n;
-            if (g.save == MOE_SAVE_INT8) {
+        if (m >= g.M) m = g.M - 1;
+        if constexpr (is_dgate(EPI)) {
+            if (n >= g.f) n = 0;
+            const int64_t row = m * (2 * (int64_t)g.f);
+            if constexpr (EPI == EPI_DGATE8) {
                 const int64_t blk = n >> 7, nb = g.f >> 7;
                 sa = g.gu_s[blk * g.M + m];
                 sb = g.gu_s[(nb + blk) * g.M + m];
-                a.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at);
-                b.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + at + g.f);
+                a.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + row + n);
+                b.x = *reinterpret_cast<const uint32_t*>((const int8_t*)g.gu + row + g.f + n);
             } else {
-                a = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + at);
-                b = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + at + g.f);
+                a = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + row + n);
+                b = *reinterpret_cast<const v2u*>((const uint16_t*)g.gu + row + g.f + n);
+            }
+        } else if constexpr (EPI == EPI_PLAIN || EPI == EPI_LINEAR) {
+            if (!g.res) return;
+            const uint16_t* p = g.res + m * g.ldr;
+            if (EPI == EPI_PLAIN || g.vec) {
+                a = *reinterpret_cast<const v2u*>(p + (n < g.N ? n : 0));
+            } else {
+                const int last = g.N - 1;
+                a.x = p[min(n, last)] | (uint32_t)p[min(n + 1, last)] << 16;
+                a.y = p[min(n + 2, last)] | (uint32_t)p[min(n + 3, last)] << 16;
             }
         }
     }
@@ -249,10 +296,7 @@ __device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n,
             if (left > 3) p[3] = (uint16_t)(w.y >> 16);
         }
     }
-    if (g.act != MOE_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = act_value(g.act, v[i]);
-    }
+    act_value4(g.act, v, v);
     if (g.res) {
         unpack_bf16x4(in.a, t);
 #pragma unroll
@@ -281,12 +325,27 @@ __device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n,
     }
 }
 
+// EPI_PLAIN for C[m, n .. n + 3], m < M, n < N
+__device__ __forceinline__ void epi_plain(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_PLAIN>& in) {
+    float t[4];
+    if (g.bias) {
+        load_bf16x4(g.bias + n, t);
+        c += v4f{t[0], t[1], t[2], t[3]};
+    }
+    if (g.res) {
+        unpack_bf16x4(in.a, t);
+        c += v4f{t[0], t[1], t[2], t[3]};
+    }
+    uint16_t* p = (uint16_t*)g.out + m * g.ldo;
+    *reinterpret_cast<v2u*>(p + n) = pack_bf16x4(c.x, c.y, c.z, c.w);
+}
+
 // EPI_DGATE for dh[m, n .. n + 3], m < M, n < f (f % 8 == 0): [dG, dU] and h from
 // the saved G, U
-__device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh, const EpiIn<EPI_DGATE>& in) {
+template <int EPI>
+__device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh, const EpiIn<EPI>& in) {
     float G[4], U[4];
-    const int64_t at = m * (2 * (int64_t)g.f) + n;
-    if (g.save == MOE_SAVE_INT8) {
+    if constexpr (EPI == EPI_DGATE8) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             G[i] = s8_of(in.a.x, i) * in.sa;
@@ -296,18 +355,18 @@ __device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, 
         unpack_bf16x4(in.a, G);
         unpack_bf16x4(in.b, U);
     }
-    float dG[4], dU[4], h[4];
+    float dG[4], dU[4], h[4], v[4], sl[4];
+    act_both4(g.act, G, v, sl);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float v, sl;
-        act_both(g.act, G[i], v, sl);
-        dG[i] = dh[i] * U[i] * sl;
-        dU[i] = dh[i] * v;
-        h[i] = v * U[i];
+        dG[i] = dh[i] * U[i] * sl[i];
+        dU[i] = dh[i] * v[i];
+        h[i] = v[i] * U[i];
     }
-    *reinterpret_cast<v2u*>(g.dgu + at) = pack_bf16x4(dG[0], dG[1], dG[2], dG[3]);
-    *reinterpret_cast<v2u*>(g.dgu + at + g.f) = pack_bf16x4(dU[0], dU[1], dU[2], dU[3]);
-    if (g.h) *reinterpret_cast<v2u*>(g.h + m * g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
+    uint16_t* p = g.dgu + m * (2 * (int64_t)g.f);
+    *reinterpret_cast<v2u*>(p + n) = pack_bf16x4(dG[0], dG[1], dG[2], dG[3]);
+    *reinterpret_cast<v2u*>(p + g.f + n) = pack_bf16x4(dU[0], dU[1], dU[2], dU[3]);
+    if (g.h) *reinterpret_cast<v2u*>(g.h + m * (int64_t)g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
 }
 
 // EPI_GATE for the sums G, U[m, n .. n + 3]; `on`: m < M and n < f.  With the 8-bit
@@ -338,9 +397,11 @@ __device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v
         }
     }
     if (!on) return;
+    const float z[4] = {G.x, G.y, G.z, G.w};
     float h[4];
+    act_value4(g.act, z, h);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = act_value(g.act, G[i]) * U[i];
+    for (int i = 0; i < 4; ++i) h[i] *= U[i];
     *reinterpret_cast<v2u*>(g.h + m * g.f + n) = pack_bf16x4(h[0], h[1], h[2], h[3]);
     if (g.save == MOE_SAVE_BF16) {
         uint16_t* p = (uint16_t*)g.gu + m * (2 * (int64_t)g.f) + n;
