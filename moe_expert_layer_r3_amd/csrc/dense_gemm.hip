@@ -612,6 +612,7 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
     const Shape s = dense_shape(g.M, g.N, g.K, epi);
     if (epi == EPI_DGATE && g.save == MOE_SAVE_INT8) epi = EPI_DGATE8;
     if (epi == EPI_LINEAR && g.vec && !g.out_f32 && !g.pre && g.act == MOE_ACT_NONE) epi = EPI_PLAIN;
+    if (la == OP_KC && lb == OP_KC && dense_is_thin(g.M, epi, g.save)) return dense_thin_launch(g, epi, stream);
     MOE_REQUIRE(s.mt * s.nt * s.splits < (1ll << 31), MOE_ERR_SHAPE, "product of %d x %d has too many tiles", g.M, g.N);
     g.mt = (int)s.mt;
     g.nt = (int)s.nt;
@@ -646,120 +647,77 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
 }
 
 // ---------------------------------------------------------------- column sums, zeros
+// Column sums in two launches: fp32 sums of chunks of rows, then the chunks'
+// sums in a fixed order.  Bound by the bytes read; what matters is loads in
+// flight: a wave takes 256 columns and CS_ROWS / 4 rows of a chunk, all loaded
+// before the first is added.
 namespace {
-constexpr int CS_ROWS = 64;  // least rows of one partial sum
-int64_t colsum_chunks(int64_t T) {
-    int64_t c = (T + CS_ROWS - 1) / CS_ROWS;
-    return c > 256 ? 256 : (c < 1 ? 1 : c);
+constexpr int CS_ROWS = 32;  // rows of a chunk that are loaded at a time
+struct Chunks {
+    int n;
+    int64_t rows;
+};
+// at most 1024 chunks, each a multiple of CS_ROWS rows
+Chunks colsum_chunks(int64_t T) {
+    int64_t rows = round_up((T + 1023) / 1024, CS_ROWS);
+    if (rows < CS_ROWS) rows = CS_ROWS;
+    const int64_t n = (T + rows - 1) / rows;
+    return Chunks{(int)(n < 1 ? 1 : n), rows};
 }
 }  // namespace
 
-// Partial column sums (fp32) of src over a chunk of rows: a wave takes 256
-// columns, the four waves every fourth row.
-__global__ __launch_bounds__(256) void colsum_kernel(const uint16_t* src, int64_t ld, int64_t T, int64_t N,
-                                                     int64_t rows, float* part) {
-    __shared__ float sm[4][256];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
-    const int64_t t1 = min((int64_t)(blockIdx.y + 1) * rows, T);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (n < N) {
-        for (int64_t t = (int64_t)blockIdx.y * rows + w; t < t1; t += 4) {
-            float v[4];
-            load_bf16x4(src + t * ld + n, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += v[i];
+// v4f of four columns n .. n + 3 of a row (fp32 or bf16), zeros past N; vec: N % 4 == 0
+__device__ __forceinline__ v4f load4(const void* src, int f32, int64_t at, int64_t n, int64_t N, bool vec) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+        if (n < N) {
+            if (f32) return *reinterpret_cast<const v4f*>((const float*)src + at);
+            load_bf16x4((const uint16_t*)src + at, v);
         }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sm[w][lane * 4 + i] = s[i];
-    __syncthreads();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c < N)
-        part[blockIdx.y * N + c] =
-            (sm[0][threadIdx.x] + sm[1][threadIdx.x]) + (sm[2][threadIdx.x] + sm[3][threadIdx.x]);
-}
-
-// out[n] = bf16 of the chunks' sums, added in order
-__global__ __launch_bounds__(256) void colsum_finish_kernel(const float* part, int chunks, int64_t ld, int64_t N,
-                                                            uint16_t* out) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
-    float s = 0.f;
-    for (int c = 0; c < chunks; ++c) s += part[c * ld + n];
-    out[n] = (uint16_t)cvt_bf16x2(s, 0.f);
-}
-
-__global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
-}
-
-size_t colsum_ws(int64_t T, int64_t N) { return (size_t)colsum_chunks(T) * N * 4; }
-
-int colsum_finish(const float* part, int chunks, int64_t ld, int64_t N, uint16_t* out, hipStream_t stream) {
-    colsum_finish_kernel<<<dim3((unsigned)((N + 255) / 256)), dim3(256), 0, stream>>>(part, chunks, ld, N, out);
-    MOE_LAUNCH_CHECK("colsum_finish_kernel");
-    return MOE_OK;
-}
-
-int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_t* out, float* part,
-                  hipStream_t stream) {
-    const int chunks = (int)colsum_chunks(T);
-    const int64_t rows = (T + chunks - 1) / chunks;
-    colsum_kernel<<<dim3((unsigned)((N + 255) / 256), chunks), dim3(256), 0, stream>>>(src, ld, T, N, rows, part);
-    MOE_LAUNCH_CHECK("colsum_kernel");
-    return colsum_finish(part, chunks, N, N, out, stream);
-}
-
-int zero16_launch(uint16_t* p, int64_t n, hipStream_t stream) {
-    const int64_t blocks = (n + 255) / 256;
-    zero16_kernel<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream>>>(p, n);
-    MOE_LAUNCH_CHECK("zero16_kernel");
-    return MOE_OK;
+        for (int i = 0; i < 4; ++i)
+            if (n + i < N) v[i] = f32 ? ((const float*)src)[at + i] : bf16_to_f32(((const uint16_t*)src)[at + i]);
+    }
+    return v4f{v[0], v[1], v[2], v[3]};
 }
 
 // dz = dy * act'(pre) of moe_linear_backward: bf16 rows of stride ldz (columns
-// past N zero) and, if part is given, fp32 column sums over chunks of rows
-// (summed before the rounding).  One thread per four columns of a row.
-__global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T,
-                                                 int64_t N, int64_t ldz, int64_t rows, uint16_t* dz, float* part) {
+// past N zero) if dz is given, and fp32 column sums over chunks of rows (before
+// the rounding) if part is given.  One thread per four columns of a row.
+template <bool ACT>
+__global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act,
+                                                 int64_t T, int64_t N, int64_t ldz, int64_t rows, uint16_t* dz,
+                                                 float* part) {
     __shared__ float sm[4][256];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
-    const int64_t t1 = min((int64_t)(blockIdx.y + 1) * rows, T);
+    const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = min(t0 + rows, T);
     const bool vec = (N & 3) == 0;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int R = CS_ROWS / 4;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
     if (n < ldz) {
-        for (int64_t t = (int64_t)blockIdx.y * rows + w; t < t1; t += 4) {
-            float v[4] = {0.f, 0.f, 0.f, 0.f}, p[4] = {0.f, 0.f, 0.f, 0.f};
-            const int64_t at = t * N + n;
-            if (vec) {
-                if (n < N) {
-                    if (dy_f32) {
-                        const v4f q = *reinterpret_cast<const v4f*>((const float*)dy + at);
-                        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-                    } else {
-                        load_bf16x4((const uint16_t*)dy + at, v);
-                    }
-                    if (pre) load_bf16x4(pre + at, p);
+        for (int64_t t = t0 + w; t < t1; t += CS_ROWS) {
+            v4f v[R], p[ACT ? R : 1];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int64_t r = min(t + 4 * i, t1 - 1);
+                v[i] = load4(dy, dy_f32, r * ld + n, n, N, vec);
+                if (ACT) p[i] = load4(pre, 0, r * N + n, n, N, vec);
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if (t + 4 * i >= t1) break;
+                if (ACT) {
+                    const float z[4] = {p[i].x, p[i].y, p[i].z, p[i].w};
+                    float val[4], sl[4];
+                    act_both4(act, z, val, sl);
+                    v[i] *= v4f{sl[0], sl[1], sl[2], sl[3]};
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n + i < N) {
-                        v[i] = dy_f32 ? ((const float*)dy)[at + i] : bf16_to_f32(((const uint16_t*)dy)[at + i]);
-                        if (pre) p[i] = bf16_to_f32(pre[at + i]);
-                    }
+                if (dz)
+                    *reinterpret_cast<v2u*>(dz + (t + 4 * i) * ldz + n) = pack_bf16x4(v[i].x, v[i].y, v[i].z, v[i].w);
+                s += v[i];
             }
-            if (act != MOE_ACT_NONE) {
-                float val[4], sl[4];
-                act_both4(act, p, val, sl);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] *= sl[i];
-            }
-            if (dz) *reinterpret_cast<v2u*>(dz + t * ldz + n) = pack_bf16x4(v[0], v[1], v[2], v[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += v[i];
         }
     }
     if (!part) return;
@@ -772,14 +730,58 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, con
             (sm[0][threadIdx.x] + sm[1][threadIdx.x]) + (sm[2][threadIdx.x] + sm[3][threadIdx.x]);
 }
 
-int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
-              float* part, uint16_t* dbias, hipStream_t stream) {
-    const int chunks = (int)colsum_chunks(T);
-    const int64_t rows = (T + chunks - 1) / chunks;
-    dz_kernel<<<dim3((unsigned)((ldz + 255) / 256), chunks), dim3(256), 0, stream>>>(
-        dy, dy_f32, pre, act, T, N, ldz, rows, dz, dbias ? part : nullptr);
+// out[n] = bf16 of the chunks' sums: 16 columns per block, 16 threads to a column
+__global__ __launch_bounds__(256) void colsum_finish_kernel(const float* part, int chunks, int64_t ld, int64_t N,
+                                                            uint16_t* out) {
+    __shared__ float sm[16][17];
+    const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
+    const int64_t n = (int64_t)blockIdx.x * 16 + c;
+    float s = 0.f;
+    if (n < N) {
+#pragma unroll 8
+        for (int i = q; i < chunks; i += 16) s += part[i * ld + n];
+    }
+    sm[q][c] = s;
+    __syncthreads();
+    if (q == 0 && n < N) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += sm[i][c];
+        out[n] = (uint16_t)cvt_bf16x2(s, 0.f);
+    }
+}
+
+__global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+size_t colsum_ws(int64_t T, int64_t N) { return (size_t)colsum_chunks(T).n * N * 4; }
+
+int dz_launch(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz,
+              uint16_t* dz, float* part, uint16_t* dbias, hipStream_t stream) {
+    const Chunks c = colsum_chunks(T);
+    const dim3 grid((unsigned)((ldz + 255) / 256), c.n);
+    float* p = dbias ? part : nullptr;
+    if (act != MOE_ACT_NONE)
+        dz_kernel<true><<<grid, dim3(256), 0, stream>>>(dy, dy_f32, ld, pre, act, T, N, ldz, c.rows, dz, p);
+    else
+        dz_kernel<false><<<grid, dim3(256), 0, stream>>>(dy, dy_f32, ld, nullptr, act, T, N, ldz, c.rows, dz, p);
     MOE_LAUNCH_CHECK("dz_kernel");
-    return dbias ? colsum_finish(part, chunks, ldz, N, dbias, stream) : MOE_OK;
+    if (!dbias) return MOE_OK;
+    colsum_finish_kernel<<<dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream>>>(part, c.n, ldz, N, dbias);
+    MOE_LAUNCH_CHECK("colsum_finish_kernel");
+    return MOE_OK;
+}
+
+int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_t* out, float* part,
+                  hipStream_t stream) {
+    return dz_launch(src, 0, ld, nullptr, MOE_ACT_NONE, T, N, N, nullptr, part, out, stream);
+}
+
+int zero16_launch(uint16_t* p, int64_t n, hipStream_t stream) {
+    const int64_t blocks = (n + 255) / 256;
+    zero16_kernel<<<dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream>>>(p, n);
+    MOE_LAUNCH_CHECK("zero16_kernel");
+    return MOE_OK;
 }
 
 }  // namespace moe

@@ -415,6 +415,10 @@ __device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v
 // a split K, the sum of the pieces with the epilogue).
 enum { OP_KC = 0, OP_KS = 1 };
 int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes, hipStream_t stream);
+// dense_thin.hip: products of few rows with both operands K-contiguous
+constexpr int THIN_ROWS = 64;
+bool dense_is_thin(int64_t M, int epi, int save);
+int dense_thin_launch(const DenseArgs& g, int epi, hipStream_t stream);
 // fp32 workspace of a product with M x N results and K summands
 size_t dense_ws(int64_t M, int64_t N, int64_t K, int epi);
 
@@ -425,8 +429,8 @@ int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_
                   hipStream_t stream);
 // dz = dy * act'(pre) [T, ldz] bf16 (dz may be NULL) and its column sums (dbias
 // may be NULL; part then unused); ldz = N rounded up to 8
-int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
-              float* part, uint16_t* dbias, hipStream_t stream);
+int dz_launch(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz,
+              uint16_t* dz, float* part, uint16_t* dbias, hipStream_t stream);
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }

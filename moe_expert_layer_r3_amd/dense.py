@@ -9,9 +9,13 @@ import torch
 
 from . import ops
 from .layer import capture_graph
-from .ops import _call, _dense, _Device, _p, _stream, rows_of, workspace_bytes
+from .ops import _dense, _Device, launch, rows_of, workspace_bytes
 
 BF16 = torch.bfloat16
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _code(table, name, what):
@@ -44,6 +48,8 @@ class LinearPlan:
         self.dx = torch.empty((T, K), dtype=BF16, device=dv) if train else None
         self.dW = torch.empty((N, K), dtype=BF16, device=dv) if train else None
         self.db = torch.empty(N, dtype=BF16, device=dv) if train and bias else None
+        self._out, self._pre, self._ws, self.ws_bytes = self.out.data_ptr(), _ptr(self.pre), _ptr(self.ws), self.ws.numel()
+        self._grads = (_ptr(self.dx), _ptr(self.dW), _ptr(self.db))
 
     def forward(self, x, W, bias=None, residual=None):
         dv, T, K, N = self.device, self.T, self.K, self.N
@@ -52,9 +58,8 @@ class LinearPlan:
         if bias is not None:
             _dense(bias, (N,), BF16, "bias", dv)
         ldr = N if residual is None else rows_of(residual, (T, N), BF16, "residual", dv)
-        with _Device(dv):
-            _call("moe_linear", _p(x), ldx, _p(W), ldw, _p(bias), _p(residual), ldr, T, N, K, self.act, _p(self.out),
-                  self.f32, N, _p(self.pre), _p(self.ws), self.ws.numel(), _stream(dv))
+        launch("moe_linear", dv, x.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(bias), _ptr(residual), ldr, T, N, K, self.act,
+               self._out, self.f32, N, self._pre, self._ws, self.ws_bytes)
         return self.out
 
     def backward(self, dy, x, W, dx_add=None):
@@ -68,9 +73,8 @@ class LinearPlan:
         ldw = rows_of(W, (N, K), BF16, "W", dv)
         if dx_add is not None:
             _dense(dx_add, (T, K), BF16, "dx_add", dv)
-        with _Device(dv):
-            _call("moe_linear_backward", _p(dy), self.f32, _p(self.pre), _p(x), ldx, _p(W), ldw, _p(dx_add), T, N, K,
-                  self.act, _p(self.dx), _p(self.dW), _p(self.db), _p(self.ws), self.ws.numel(), _stream(dv))
+        launch("moe_linear_backward", dv, dy.data_ptr(), self.f32, self._pre, x.data_ptr(), ldx, W.data_ptr(), ldw,
+               _ptr(dx_add), T, N, K, self.act, *self._grads, self._ws, self.ws_bytes)
         return self.dx, self.dW, self.db
 
     def capture(self, x, W, bias=None, residual=None, warmup=1):
@@ -114,6 +118,9 @@ class GatedFFNPlan:
         self.dW2 = e((d, f)) if train else None
         self.db13 = e(2 * f) if train and bias else None
         self.db2 = e(d) if train and bias else None
+        self._h, self._y, self._gu, self._gu_s = _ptr(self.h), _ptr(self.y), _ptr(self.gu), _ptr(self.gu_s)
+        self._ws, self.ws_bytes = _ptr(self.ws), self.ws.numel()
+        self._grads = tuple(_ptr(t) for t in (self.dx, self.dW13, self.dW2, self.db13, self.db2))
 
     def _weights(self, W13, W2):
         _dense(W13, (2 * self.f, self.d), BF16, "W13", self.device)
@@ -129,10 +136,9 @@ class GatedFFNPlan:
             _dense(b2, (d,), BF16, "b2", dv)
         if residual is not None:
             _dense(residual, (T, d), BF16, "residual", dv)
-        with _Device(dv):
-            _call("moe_gated_ffn", _p(x), ldx, _p(W13), _p(b13), _p(W2), _p(b2), _p(residual), T, d, f, self.act,
-                  _p(self.h), _p(self.y), self.save, _p(self.gu), _p(self.gu_s), _p(self.ws), self.ws.numel(),
-                  _stream(dv))
+        launch("moe_gated_ffn", dv, x.data_ptr(), ldx, W13.data_ptr(), _ptr(b13), W2.data_ptr(), _ptr(b2),
+               _ptr(residual), T, d, f, self.act, self._h, self._y, self.save, self._gu, self._gu_s, self._ws,
+               self.ws_bytes)
         return self.y
 
     def backward(self, dy, x, W13, W2, dx_add=None):
@@ -147,10 +153,8 @@ class GatedFFNPlan:
         self._weights(W13, W2)
         if dx_add is not None:
             _dense(dx_add, (T, d), BF16, "dx_add", dv)
-        with _Device(dv):
-            _call("moe_gated_ffn_backward", _p(dy), _p(x), ldx, _p(W13), _p(W2), self.save, _p(self.gu), _p(self.gu_s),
-                  _p(dx_add), T, d, f, self.act, _p(self.dx), _p(self.dW13), _p(self.dW2), _p(self.db13), _p(self.db2),
-                  _p(self.ws), self.ws.numel(), _stream(dv))
+        launch("moe_gated_ffn_backward", dv, dy.data_ptr(), x.data_ptr(), ldx, W13.data_ptr(), W2.data_ptr(), self.save,
+               self._gu, self._gu_s, _ptr(dx_add), T, d, f, self.act, *self._grads, self._ws, self.ws_bytes)
         return self.dx, self.dW13, self.dW2, self.db13, self.db2
 
     def capture(self, x, W13, W2, b13=None, b2=None, residual=None, warmup=1):

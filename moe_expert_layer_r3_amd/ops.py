@@ -502,32 +502,41 @@ def combine_backward(dy, y_perm, pair_row, w, rcap=None, quant=True, pow2=False)
 
 class _Device:
     """Makes a tensor's device current around a launch (kernels go to the
-    current device's queue); free when it is current already."""
+    current device's queue)."""
 
     def __init__(self, dev):
-        self.guard = None if dev.index is None or torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        self.guard = torch.cuda.device(dev)
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        self.guard.__enter__()
 
     def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+        self.guard.__exit__(*a)
+
+
+def launch(name, dev, *args):
+    """One C-ABI call on ``dev``'s current stream; pointers are plain integers (0
+    or None: NULL).  The device is switched only if another one is current."""
+    if torch.cuda.current_device() != dev.index:
+        with _Device(dev):
+            return launch(name, dev, *args)
+    rc = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise MoeError(name, rc, last_error())
 
 
 def rows_of(t, shape, dtype, name, dev=None):
     """Row stride of a matrix whose rows may lie apart (a column slice of a wider
     buffer); raises unless it has this shape and type, rows of adjacent
     elements, and lives on ``dev``."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected shape {tuple(shape)} with adjacent row elements, got {tuple(t.shape)} "
                          f"with strides {tuple(t.stride())}")
     if not t.is_cuda or (dev is not None and t.device != dev):
         raise ValueError(f"{name}: must live on the GPU{'' if dev is None else f' {dev}'}, got {t.device}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def act_save(x, out=None):
@@ -540,11 +549,11 @@ def act_save(x, out=None):
     if out is None:
         out = (torch.empty((rows, cols), dtype=torch.int8, device=dev),
                torch.empty((nb, rows), dtype=torch.float32, device=dev))
+    else:
+        _dense(out[0], (rows, cols), torch.int8, "q", dev)
+        _dense(out[1], (nb, rows), torch.float32, "s", dev)
     q, s = out
-    _dense(q, (rows, cols), torch.int8, "q", dev)
-    _dense(s, (nb, rows), torch.float32, "s", dev)
-    with _Device(dev):
-        _call("moe_act_save", _p(x), ld, rows, cols, _p(q), _p(s), _stream(dev))
+    launch("moe_act_save", dev, x.data_ptr(), ld, rows, cols, q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -554,17 +563,19 @@ def act_restore(q, s, out=None):
     dev = _dev(q)
     _dense(q, (rows, cols), torch.int8, "q", dev)
     _dense(s, ((cols + 127) // 128, rows), torch.float32, "s", dev)
-    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if out is None else out
-    _dense(x, (rows, cols), torch.bfloat16, "out", dev)
-    with _Device(dev):
-        _call("moe_act_restore", _p(q), _p(s), rows, cols, _p(x), _stream(dev))
+    if out is None:
+        x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    else:
+        x = _dense(out, (rows, cols), torch.bfloat16, "out", dev)
+    launch("moe_act_restore", dev, q.data_ptr(), s.data_ptr(), rows, cols, x.data_ptr())
     return x
 
 
 def _dense(t, shape, dtype, name, dev):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or t.device != dev:
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} of shape {tuple(shape)} on {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
 
 
 def workspace_bytes(fn, *sizes):
