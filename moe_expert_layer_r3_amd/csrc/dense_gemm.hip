@@ -36,7 +36,7 @@ struct TileEpilogue {
     // What the steps read from memory is loaded a batch ahead (the first one before
     // the results are staged).  The loop stays rolled: its code is long.
     static constexpr bool READS = EPI == EPI_LINEAR || is_dgate(EPI) || EPI == EPI_PLAIN;
-    static constexpr int BATCH = EPI == EPI_PLAIN && STEPS % 8 == 0 ? 8 : 4;
+    static constexpr int BATCH = EPI == EPI_PLAIN && STEPS % 8 == 0 ? 8 : STEPS < 4 ? STEPS : 4;
     static_assert(STEPS % BATCH == 0, "whole batches");
     EpiIn<EPI> in[READS ? BATCH : 1];
     // this thread's first row; where a wave takes one row, a scalar
@@ -244,6 +244,138 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
         for (int j = 0; j < 4; ++j) {
             const int col = EPI == EPI_GATE ? (j >> 1) * 128 + wn * 32 + (j & 1) * 16 : wn * 64 + j * 16;
             *reinterpret_cast<v4f*>(smem + stage_at(BN, wm * 64 + i * 16 + l15, col / 4 + g4)) = acc[i][j];
+        }
+    __syncthreads();
+    epi.run(g, smem, m0, n0, split);
+}
+
+// ---------------------------------------------------------------- 64 x 64 tiles
+// Small problems, where a K loop's time is its loads' latency: four waves of 32 x 32,
+// a ring of five K steps in LDS (80 KB, two workgroups per compute unit), four of
+// them in flight while one is multiplied, one barrier per step.
+constexpr int RING = 5;
+template <int LA, int LB, int EPI>
+__global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
+    constexpr int HALF = 8192, STAGE = 2 * HALF;  // A, B: 64 rows (columns) of a step
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    int mt, nt, split;
+    dense_tile(g, mt, nt, split);
+    const int64_t m0 = (int64_t)mt * 64;
+    const int n0 = nt * (EPI == EPI_GATE ? 32 : 64);
+    const int ks0 = split * g.ksteps;
+    const int ks1 = min(ks0 + g.ksteps, (g.K + DBK - 1) / DBK);
+    const int kend = min(g.K, ks1 * DBK);
+    const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+    // DMA: wave w moves segments 2w, 2w + 1 of both operands: KC rows 16w .. + 15, KS
+    // K rows 16w .. + 15
+    uint32_t va[2], vb[2];
+    const uint8_t *pa, *pb;
+    const KcLane la(lane, g.lda), lb(lane, g.ldb);
+    const uint32_t kseg = wave * 16 + (lane >> 3);  // KS: K row of segment 2w, + 8 of 2w + 1
+    auto ks_off = [&](int i, int64_t c0, int cols, int64_t ld) {
+        const uint32_t k = kseg + 8 * i, c = (lane & 7) ^ (2 * ks_f64(k));
+        return c0 + c * 8 < cols ? k * (uint32_t)(ld * 2) + c * 16 : OOB;
+    };
+    if constexpr (LA == OP_KC) {
+        const int64_t r0 = m0 + wave * 16;
+        pa = (const uint8_t*)(g.a + r0 * g.lda);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) va[i] = r0 + 8 * i + la.row < g.M ? la.off + (uint32_t)(8 * i * g.lda * 2) : OOB;
+    } else {
+        pa = (const uint8_t*)(g.a + m0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) va[i] = ks_off(i, m0, g.a_cols, g.lda);
+    }
+    if constexpr (LB == OP_KC) {
+        int64_t r0 = n0 + wave * 16, lim = g.N;
+        if constexpr (EPI == EPI_GATE) {  // 32 G rows, then the 32 U rows of the same h columns
+            r0 = n0 + (wave & 1) * 16 + (wave >> 1) * (int64_t)g.f;
+            lim = (wave >> 1) ? 2 * (int64_t)g.f : g.f;
+        }
+        pb = (const uint8_t*)(g.b + r0 * g.ldb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) vb[i] = r0 + 8 * i + lb.row < lim ? lb.off + (uint32_t)(8 * i * g.ldb * 2) : OOB;
+    } else {
+        pb = (const uint8_t*)(g.b + n0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) vb[i] = ks_off(i, n0, g.b_cols, g.ldb);
+    }
+    const int64_t step_a = LA == OP_KC ? 128 : (int64_t)DBK * g.lda * 2;
+    const int64_t step_b = LB == OP_KC ? 128 : (int64_t)DBK * g.ldb * 2;
+    // steps past the end fill zeros without reading memory
+    auto issue = [&](int slot, int ks) {
+        const int left = kend - ks * DBK;
+        const u32x4 da = buf_desc(pa + ks * step_a), db = buf_desc(pb + ks * step_b);
+        const uint32_t s = sbase + slot * STAGE + wave * 2048;
+        const int a0 = LA == OP_KC ? (int)la.k : (int)kseg, a1 = LA == OP_KC ? a0 : a0 + 8;
+        const int b0 = LB == OP_KC ? (int)lb.k : (int)kseg, b1 = LB == OP_KC ? b0 : b0 + 8;
+        dma16b2(da, a0 < left ? va[0] : OOB, a1 < left ? va[1] : OOB, s);
+        dma16b2(db, b0 < left ? vb[0] : OOB, b1 < left ? vb[1] : OOB, s + HALF);
+    };
+
+    uint32_t ra[2], rb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        ra[i] = LA == OP_KC ? kc_frag(lane, wm * 32 + i * 16) : ks_frag64(lane, wm * 2 + i);
+        const int c = EPI == EPI_GATE ? i * 32 + wn * 16 : wn * 32 + i * 16;
+        rb[i] = HALF + (LB == OP_KC ? kc_frag(lane, c) : ks_frag64(lane, c / 16));
+    }
+    auto frag = [&](auto layout, uint32_t addr, auto sc) {
+        constexpr int s = decltype(sc)::value;
+        if constexpr (decltype(layout)::value == OP_KC) {
+            return lds16<0>(addr ^ (s * 64));
+        } else {
+            const v2u lo = lds_tr16<s * 4096>(addr), hi = lds_tr16<s * 4096 + 512>(addr);
+            return u32x4{lo.x, lo.y, hi.x, hi.y};
+        }
+    };
+    v4f acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) issue(i, ks0 + i);
+    int slot = 0;
+    for (int ks = ks0; ks < ks1; ++ks) {
+        wait_vmcnt<(RING - 2) * 4>();  // this step has landed; the next three are in flight
+        wait_lgkm0();
+        phase_barrier();  // for every wave, which has also read the previous step
+        issue(slot == 0 ? RING - 1 : slot - 1, ks + RING - 1);
+        uint32_t base = sbase + slot * STAGE;
+        pin(base);
+        static_for<0, 2>([&](auto sc) {
+            u32x4 fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = frag(std::integral_constant<int, LA>{}, base + ra[i], sc);
+                fb[i] = frag(std::integral_constant<int, LB>{}, base + rb[i], sc);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
+        });
+        slot = slot == RING - 1 ? 0 : slot + 1;
+    }
+    wait_lgkm0();
+    wait_vmcnt<0>();  // the fills past the end have landed
+    phase_barrier();
+
+    const int l15 = lane & 15, g4 = lane >> 4;
+    TileEpilogue<EPI, 64, 64, 256> epi;
+    epi.load(g, m0, n0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int col = EPI == EPI_GATE ? j * 32 + wn * 16 : wn * 32 + j * 16;
+            *reinterpret_cast<v4f*>(smem + stage_at(64, wm * 32 + i * 16 + l15, col / 4 + g4)) = acc[i][j];
         }
     __syncthreads();
     epi.run(g, smem, m0, n0, split);
@@ -496,9 +628,9 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
 // ---------------------------------------------------------------- split K: sum and epilogue
 // One thread per four columns; the pieces are added in order.
 template <int EPI>
-__global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs g, int splits) {
+__global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits) {
     const int cols = EPI == EPI_GATE ? g.f : (int)g.part_ld;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t idx = (int64_t)blockIdx.x * 128 + threadIdx.x;
     const int64_t m = idx / (cols / 4);
     const int n = (int)(idx - m * (cols / 4)) * 4;
     const bool on = m < g.M;
@@ -507,7 +639,15 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs g, int splits)
         v4f s = {0.f, 0.f, 0.f, 0.f};
         if (on) {
             const float* p = g.part + m * g.part_ld + col;
-            for (int i = 0; i < splits; ++i) s += *reinterpret_cast<const v4f*>(p + i * plane);
+            // eight loads in flight; past the last piece it is read again, not added
+            for (int i = 0; i < splits; i += 8) {
+                v4f t[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] = *reinterpret_cast<const v4f*>(p + min(i + j, splits - 1) * plane);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (i + j < splits) s += t[j];
+            }
         }
         return s;
     };
@@ -530,47 +670,73 @@ __global__ __launch_bounds__(256) void dense_sum_kernel(DenseArgs g, int splits)
 
 // ---------------------------------------------------------------- host side
 namespace {
+enum Kind { THIN, SLAB, SMALL, TILES, WIDE };
 struct Shape {
+    Kind kind;
     int64_t mt, nt;
-    int bm, bn;  // bn: columns of C (h columns for EPI_GATE)
     int splits, ksteps;
-    bool wide;   // 256 x 256 tiles
+    bool pieces;  // results go through the workspace and dense_sum_kernel
 };
-// Tiles and K splits of an M x N product over K.  A product with fewer tiles
-// than two per compute unit is split along K, each piece at least 8 K steps.
-Shape dense_shape(int64_t M, int64_t N, int64_t K, int epi) {
-    Shape s;
-    const int64_t cols = epi == EPI_GATE ? N / 2 : N;
-    const int64_t wide_n = epi == EPI_GATE ? 128 : 256;
-    const int64_t wide_tiles = (M + 255) / 256 * ((cols + wide_n - 1) / wide_n);
-    s.wide = wide_tiles * 4 >= num_cus() * 3;
-    if (s.wide) {
-        s.mt = (M + 255) / 256;
-        s.nt = (cols + wide_n - 1) / wide_n;
-        s.splits = 1;
-        s.ksteps = (int)((K + DBK - 1) / DBK);
-        return s;
-    }
-    s.bm = epi == EPI_GATE ? 64 : 128;
-    s.bn = 128;
-    s.mt = (M + s.bm - 1) / s.bm;
-    s.nt = (cols + s.bn - 1) / s.bn;
+// K in at most `sp` pieces of at least `least` steps
+void set_splits(Shape& s, int64_t K, int64_t sp, int64_t least) {
     const int64_t steps = (K + DBK - 1) / DBK;
-    const int64_t want = 2 * num_cus();
-    int64_t sp = 1;
-    // pieces go through 128 x 128 tiles
-    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
-    if (tiles * 2 <= want) sp = want / tiles;
-    if (sp > steps / 8) sp = steps / 8;
+    if (sp > steps / least) sp = steps / least;
     if (sp > 32) sp = 32;
     if (sp < 1) sp = 1;
     s.ksteps = (int)((steps + sp - 1) / sp);
     s.splits = (int)((steps + s.ksteps - 1) / s.ksteps);
-    if (s.splits > 1) {
-        s.bm = 128;
-        s.mt = (M + 127) / 128;
+}
+// The kernel for an M x N product over K:
+//   THIN   up to 4 rows, one launch
+//   SLAB   up to 128 rows, K in pieces
+//   SMALL  64 x 64 tiles
+//   WIDE   256 x 256 tiles where they fill three quarters of the compute units
+//   TILES  64 x 64 wave tiles; with fewer tiles than two per compute unit K is
+//          split, pieces of at least 8 steps on 128 x 128 tiles
+Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
+    Shape s;
+    const bool gate = epi == EPI_GATE || epi == EPI_GATE8;
+    const int64_t cols = gate ? N / 2 : N;
+    const int64_t cus = num_cus();
+    s.splits = 1;
+    s.ksteps = (int)((K + DBK - 1) / DBK);
+    s.mt = 1;
+    s.pieces = false;
+    if (la == OP_KC && lb == OP_KC && M <= SLAB_ROWS) {
+        s.kind = M <= THIN_ROWS && epi != EPI_GATE8 ? THIN : SLAB;
         s.nt = (N + 127) / 128;
+        if (s.kind == SLAB) set_splits(s, K, cus / s.nt, 4);
+        s.pieces = s.kind == SLAB;
+        return s;
     }
+    const int64_t wide_n = gate ? 128 : 256;
+    const int64_t wide_tiles = (M + 255) / 256 * ((cols + wide_n - 1) / wide_n);
+    if (wide_tiles * 4 >= cus * 3) {
+        s.kind = WIDE;
+        s.mt = (M + 255) / 256;
+        s.nt = (cols + wide_n - 1) / wide_n;
+        return s;
+    }
+    const int64_t small = (M + 63) / 64 * ((N + 63) / 64);
+    // 64 x 64 tiles read the operands twice as often as 128 x 128 ones, which long sums
+    // pay for: 2000 x 2000 over 1000 takes 22.8 us (27.0 on 128 x 128 tiles), 8192 x 256
+    // over 7168 takes 49 us (43.8)
+    if (small <= cus || (small <= 4 * cus && K <= 1024)) {
+        s.kind = SMALL;
+        s.mt = (M + 63) / 64;
+        s.nt = (N + 63) / 64;  // (32 columns each of G and U for EPI_GATE)
+        // the 8-bit save takes whole blocks, in the sum of the pieces
+        set_splits(s, K, 2 * cus / small, 16);
+        s.pieces = s.splits > 1 || epi == EPI_GATE8;
+        return s;
+    }
+    s.kind = TILES;
+    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
+    set_splits(s, K, 2 * cus / tiles, 8);
+    s.pieces = s.splits > 1;
+    const int64_t bm = gate && s.splits == 1 ? 64 : 128;
+    s.mt = (M + bm - 1) / bm;
+    s.nt = ((s.splits > 1 ? N : cols) + 127) / 128;
     return s;
 }
 template <int WM, int WN, int LA, int LB, int EPI>
@@ -581,6 +747,18 @@ int launch_one(const DenseArgs& g, int splits, hipStream_t stream) {
     return MOE_OK;
 }
 template <int LA, int LB, int EPI>
+int launch_small_one(const DenseArgs& g, int splits, hipStream_t stream) {
+    dense_small_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt * splits)), dim3(256), 0, stream>>>(g);
+    MOE_LAUNCH_CHECK("dense_small_kernel");
+    return MOE_OK;
+}
+template <int EPI>
+int launch_small(const DenseArgs& g, int la, int lb, int splits, hipStream_t stream) {
+    if (la == OP_KC && lb == OP_KC) return launch_small_one<OP_KC, OP_KC, EPI>(g, splits, stream);
+    if (la == OP_KC) return launch_small_one<OP_KC, OP_KS, EPI>(g, splits, stream);
+    return launch_small_one<OP_KS, OP_KS, EPI>(g, splits, stream);
+}
+template <int LA, int LB, int EPI>
 int launch_wide(const DenseArgs& g, hipStream_t stream) {
     dense_wide_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt)), dim3(512), 0, stream>>>(g);
     MOE_LAUNCH_CHECK("dense_wide_kernel");
@@ -589,8 +767,8 @@ int launch_wide(const DenseArgs& g, hipStream_t stream) {
 template <int EPI>
 int launch_sum(const DenseArgs& g, int splits, hipStream_t stream) {
     const int64_t cols = EPI == EPI_GATE ? g.f : g.part_ld;
-    const int64_t blocks = ((int64_t)g.M * (cols / 4) + 255) / 256;
-    dense_sum_kernel<EPI><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(g, splits);
+    const int64_t blocks = ((int64_t)g.M * (cols / 4) + 127) / 128;
+    dense_sum_kernel<EPI><<<dim3((unsigned)blocks), dim3(128), 0, stream>>>(g, splits);
     MOE_LAUNCH_CHECK("dense_sum_kernel");
     return MOE_OK;
 }
@@ -602,26 +780,31 @@ int launch_layout(const DenseArgs& g, int la, int lb, int splits, hipStream_t st
 }
 }  // namespace
 
-size_t dense_ws(int64_t M, int64_t N, int64_t K, int epi) {
+size_t dense_ws(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
     if (M <= 0 || N <= 0 || K <= 0) return 0;  // T = 0
-    const Shape s = dense_shape(M, N, K, epi);
-    return s.splits > 1 ? (size_t)s.splits * M * round_up(N, 4) * 4 : 0;
+    const Shape s = dense_shape(M, N, K, la, lb, epi);
+    return s.pieces ? (size_t)s.splits * M * round_up(N, 4) * 4 : 0;
 }
 
 int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes, hipStream_t stream) {
-    const Shape s = dense_shape(g.M, g.N, g.K, epi);
+    if (epi == EPI_GATE && g.save == MOE_SAVE_INT8) epi = EPI_GATE8;
+    const Shape s = dense_shape(g.M, g.N, g.K, la, lb, epi);
+    if (epi == EPI_GATE8) epi = EPI_GATE;
     if (epi == EPI_DGATE && g.save == MOE_SAVE_INT8) epi = EPI_DGATE8;
     if (epi == EPI_LINEAR && g.vec && !g.out_f32 && !g.pre && g.act == MOE_ACT_NONE) epi = EPI_PLAIN;
-    if (la == OP_KC && lb == OP_KC && dense_is_thin(g.M, epi, g.save)) return dense_thin_launch(g, epi, stream);
     MOE_REQUIRE(s.mt * s.nt * s.splits < (1ll << 31), MOE_ERR_SHAPE, "product of %d x %d has too many tiles", g.M, g.N);
     g.mt = (int)s.mt;
     g.nt = (int)s.nt;
     g.ksteps = s.ksteps;
-    if (s.splits > 1) {
-        MOE_REQUIRE(ws && ws_bytes >= dense_ws(g.M, g.N, g.K, epi), MOE_ERR_WORKSPACE, "workspace too small");
+    if (s.kind == THIN) return dense_thin_launch(g, epi, stream);
+    if (s.pieces) {
+        MOE_REQUIRE(ws && aligned16(ws) && ws_bytes >= (size_t)s.splits * g.M * round_up(g.N, 4) * 4, MOE_ERR_WORKSPACE,
+                    "workspace too small");
         g.part = (float*)ws;
         g.part_ld = round_up(g.N, 4);
-        const int rc = launch_layout<EPI_PART>(g, la, lb, s.splits, stream);
+        const int rc = s.kind == SLAB    ? dense_slab_launch(g, s.splits, stream)
+                       : s.kind == SMALL ? launch_small<EPI_PART>(g, la, lb, s.splits, stream)
+                                         : launch_layout<EPI_PART>(g, la, lb, s.splits, stream);
         if (rc != MOE_OK) return rc;
         if (epi == EPI_GATE) return launch_sum<EPI_GATE>(g, s.splits, stream);
         if (epi == EPI_DGATE) return launch_sum<EPI_DGATE>(g, s.splits, stream);
@@ -629,7 +812,14 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         if (epi == EPI_PLAIN) return launch_sum<EPI_PLAIN>(g, s.splits, stream);
         return launch_sum<EPI_LINEAR>(g, s.splits, stream);
     }
-    if (s.wide) {
+    if (s.kind == SMALL) {
+        if (epi == EPI_GATE) return launch_small_one<OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
+        if (epi == EPI_DGATE) return launch_small_one<OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);
+        if (epi == EPI_DGATE8) return launch_small_one<OP_KC, OP_KS, EPI_DGATE8>(g, 1, stream);
+        if (epi == EPI_LINEAR) return launch_small_one<OP_KC, OP_KC, EPI_LINEAR>(g, 1, stream);
+        return launch_small<EPI_PLAIN>(g, la, lb, 1, stream);
+    }
+    if (s.kind == WIDE) {
         if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, stream);
         if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, stream);
         if (epi == EPI_DGATE8) return launch_wide<OP_KC, OP_KS, EPI_DGATE8>(g, stream);

@@ -19,8 +19,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int DBK = 64;  // K step: 128 bytes of a KC row, 64 rows of a KS matrix
 
 // EPI_PLAIN: EPI_LINEAR's common form (bf16 out = C + bias + residual, vec);
-// EPI_DGATE8: EPI_DGATE from the 8-bit [G, U]
-enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3, EPI_PLAIN = 4, EPI_DGATE8 = 5 };
+// EPI_DGATE8: EPI_DGATE from the 8-bit [G, U]; EPI_GATE8: EPI_GATE with the 8-bit
+// save, which needs whole 128-column blocks (the kernels read `save`: EPI_GATE)
+enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3, EPI_PLAIN = 4, EPI_DGATE8 = 5, EPI_GATE8 = 6 };
 constexpr bool is_dgate(int epi) { return epi == EPI_DGATE || epi == EPI_DGATE8; }
 
 struct DenseArgs {
@@ -213,6 +214,15 @@ __device__ __forceinline__ uint32_t ks_frag(int lane, int c16) {
     const uint32_t l15 = (uint32_t)lane & 15;
     const uint32_t k = ((uint32_t)lane >> 4) * 8 + (l15 >> 2);
     return k * 256 + (((uint32_t)c16 ^ ks_f(k)) << 5) + (l15 & 3) * 8;
+}
+
+// The same in images of 64 columns: K row k at 128 k, its eight chunks c at
+// c ^ 2 f64(k); + 512 the next four K values, + 4096 per s.
+__device__ __forceinline__ uint32_t ks_f64(uint32_t k) { return (k >> 1 & 1) | ((k >> 3 & 1) << 1); }
+__device__ __forceinline__ uint32_t ks_frag64(int lane, int c16) {
+    const uint32_t l15 = (uint32_t)lane & 15;
+    const uint32_t k = ((uint32_t)lane >> 4) * 8 + (l15 >> 2);
+    return k * 128 + (((uint32_t)c16 ^ ks_f64(k)) << 5) + (l15 & 3) * 8;
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -410,17 +420,36 @@ __device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v
     }
 }
 
+// EPI_GATE without the 8-bit save for G, U[m, n] and [m, n + 1] (m < M, n < f)
+__device__ __forceinline__ void epi_gate2(const DenseArgs& g, int64_t m, int n, v4f G, v4f U) {
+    if (g.bias) {
+        G.x += bf16_to_f32(g.bias[n]);
+        G.y += bf16_to_f32(g.bias[n + 1]);
+        U.x += bf16_to_f32(g.bias[g.f + n]);
+        U.y += bf16_to_f32(g.bias[g.f + n + 1]);
+    }
+    const float z[4] = {G.x, G.y, 0.f, 0.f};
+    float h[4];
+    act_value4(g.act, z, h);
+    *reinterpret_cast<uint32_t*>(g.h + m * g.f + n) = cvt_bf16x2(h[0] * U.x, h[1] * U.y);
+    if (g.save == MOE_SAVE_BF16) {
+        uint16_t* p = (uint16_t*)g.gu + m * (2 * (int64_t)g.f) + n;
+        *reinterpret_cast<uint32_t*>(p) = cvt_bf16x2(G.x, G.y);
+        *reinterpret_cast<uint32_t*>(p + g.f) = cvt_bf16x2(U.x, U.y);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 // A product: fills in tiles, splits and workspace use and launches it (and, for
 // a split K, the sum of the pieces with the epilogue).
 enum { OP_KC = 0, OP_KS = 1 };
 int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes, hipStream_t stream);
 // dense_thin.hip: products of few rows with both operands K-contiguous
-constexpr int THIN_ROWS = 64;
-bool dense_is_thin(int64_t M, int epi, int save);
 int dense_thin_launch(const DenseArgs& g, int epi, hipStream_t stream);
+constexpr int THIN_ROWS = 4, SLAB_ROWS = 128;
+int dense_slab_launch(const DenseArgs& g, int splits, hipStream_t stream);
 // fp32 workspace of a product with M x N results and K summands
-size_t dense_ws(int64_t M, int64_t N, int64_t K, int epi);
+size_t dense_ws(int64_t M, int64_t N, int64_t K, int la, int lb, int epi);
 
 // column sums of src [T, N] bf16 (row stride ld, N % 4 == 0) as bf16; part: fp32
 // workspace of colsum_ws bytes

@@ -39,8 +39,8 @@ BackwardWs backward_ws(int64_t T, int64_t d, int64_t f) {
     const size_t c1 = colsum_ws(T, 2 * f), c2 = colsum_ws(T, d);
     w.gemm = w.part + (size_t)round_up((int64_t)(c1 > c2 ? c1 : c2), 256);
     size_t g = 0;
-    for (const size_t s : {dense_ws(T, f, d, EPI_DGATE), dense_ws(T, d, 2 * f, EPI_LINEAR),
-                           dense_ws(2 * f, d, T, EPI_LINEAR), dense_ws(d, f, T, EPI_LINEAR)})
+    for (const size_t s : {dense_ws(T, f, d, OP_KC, OP_KS, EPI_DGATE), dense_ws(T, d, 2 * f, OP_KC, OP_KS, EPI_LINEAR),
+                           dense_ws(2 * f, d, T, OP_KS, OP_KS, EPI_LINEAR), dense_ws(d, f, T, OP_KS, OP_KS, EPI_LINEAR)})
         if (s > g) g = s;
     w.total = w.gemm + g;
     return w;
@@ -55,8 +55,10 @@ extern "C" int moe_gated_ffn_workspace(int64_t T, int64_t d, int64_t f, size_t* 
     clear_error();
     MOE_REQUIRE(bytes, MOE_ERR_NULL, "bytes is NULL");
     if (const int rc = check_sizes(T, d, f)) return rc;
-    const size_t a = dense_ws(T, 2 * f, d, EPI_GATE), b = dense_ws(T, d, f, EPI_LINEAR);
-    *bytes = a > b ? a : b;
+    *bytes = 0;
+    for (const size_t s : {dense_ws(T, 2 * f, d, OP_KC, OP_KC, EPI_GATE), dense_ws(T, 2 * f, d, OP_KC, OP_KC, EPI_GATE8),
+                           dense_ws(T, d, f, OP_KC, OP_KC, EPI_LINEAR)})
+        if (s > *bytes) *bytes = s;
     return MOE_OK;
 }
 

@@ -31,8 +31,8 @@ BackwardWs backward_ws(int64_t T, int64_t N, int64_t K) {
     w.dz = 0;
     w.part = (size_t)round_up(T * ldz * 2, 256);
     w.gemm = w.part + (size_t)round_up((int64_t)colsum_ws(T, ldz), 256);
-    size_t g = dense_ws(T, K, N, EPI_LINEAR);
-    const size_t g2 = dense_ws(N, K, T, EPI_LINEAR);
+    size_t g = dense_ws(T, K, N, OP_KC, OP_KS, EPI_LINEAR);
+    const size_t g2 = dense_ws(N, K, T, OP_KS, OP_KS, EPI_LINEAR);
     if (g2 > g) g = g2;
     w.total = w.gemm + g;
     return w;
@@ -47,7 +47,7 @@ extern "C" int moe_linear_workspace(int64_t T, int64_t N, int64_t K, size_t* byt
     clear_error();
     MOE_REQUIRE(bytes, MOE_ERR_NULL, "bytes is NULL");
     if (const int rc = check_sizes(T, N, K)) return rc;
-    *bytes = dense_is_thin(T, EPI_LINEAR, MOE_SAVE_NONE) ? 0 : dense_ws(T, N, K, EPI_LINEAR);
+    *bytes = dense_ws(T, N, K, OP_KC, OP_KC, EPI_LINEAR);
     return MOE_OK;
 }
 

@@ -42,9 +42,9 @@ def test_linear_refusals(kw, want):
 
 
 def test_linear_refuses_a_small_workspace():
-    # a few tiles of 7168 summands are split along K; up to 64 rows need no workspace
+    # a few tiles of 7168 summands are split along K; up to 4 rows need no workspace
     n = ops.workspace_bytes("moe_linear_workspace", 100, 256, 7168)
-    assert n > 0 and ops.workspace_bytes("moe_linear_workspace", 64, 256, 7168) == 0
+    assert n > 0 and ops.workspace_bytes("moe_linear_workspace", 4, 256, 7168) == 0
     kw = dict(T=100, N=256, K=7168, ldx=7168, ldw=7168, ldo=256)
     assert rc("moe_linear", LIN, wsb=n - 1, **kw) == -4
     assert rc("moe_linear", LIN, ws=None, **kw) == -4
