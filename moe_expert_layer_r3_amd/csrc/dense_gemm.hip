@@ -686,20 +686,28 @@ void set_splits(Shape& s, int64_t K, int64_t sp, int64_t least) {
     s.ksteps = (int)((steps + sp - 1) / sp);
     s.splits = (int)((steps + s.ksteps - 1) / s.ksteps);
 }
-// The kernel for an M x N product over K:
+// The kernel for an M x N product over K, by the number of tiles it would have:
 //   THIN   up to 4 rows, one launch
 //   SLAB   up to 128 rows, K in pieces
-//   SMALL  64 x 64 tiles
-//   WIDE   256 x 256 tiles where they fill three quarters of the compute units
-//   TILES  64 x 64 wave tiles; with fewer tiles than two per compute unit K is
-//          split, pieces of at least 8 steps on 128 x 128 tiles
+//   WIDE   256 x 256 tiles, where they fill three quarters of the compute units, or
+//          where K split in as many pieces as fill them pays for the pieces' extra
+//          traffic (about 130 MB, 15 us): from 2e10 multiplications on (2048 x 4096
+//          over 7168: 105 us, 118 on 128 x 128 tiles; 16384 x 256 over 7168: 77 and
+//          95 us), or where an operand is far larger than the caches, since these
+//          tiles read it half as often (8192 x 256 over 7168: 51 and 57 us)
+//   SMALL  64 x 64 tiles for short sums (1237 x 1032 over 688: 10.0 us, 15.6 on
+//          128 x 128 tiles); they read the operands twice as often, which long sums
+//          of many tiles pay for (1000 x 600 over 12000: 44 us, 35 on 128 x 128)
+//   TILES  128 x 128 tiles, K split where they are fewer than the compute units
+//          (2048 x 2048 over 2048 has exactly as many: 28 us, 31 split in two)
 Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
     Shape s;
     const bool gate = epi == EPI_GATE || epi == EPI_GATE8;
     const int64_t cols = gate ? N / 2 : N;
     const int64_t cus = num_cus();
+    const int64_t steps = (K + DBK - 1) / DBK;
     s.splits = 1;
-    s.ksteps = (int)((K + DBK - 1) / DBK);
+    s.ksteps = (int)steps;
     s.mt = 1;
     s.pieces = false;
     if (la == OP_KC && lb == OP_KC && M <= SLAB_ROWS) {
@@ -709,34 +717,40 @@ Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
         s.pieces = s.kind == SLAB;
         return s;
     }
-    const int64_t wide_n = gate ? 128 : 256;
-    const int64_t wide_tiles = (M + 255) / 256 * ((cols + wide_n - 1) / wide_n);
-    if (wide_tiles * 4 >= cus * 3) {
+    const int64_t wide_m = (M + 255) / 256, wide_n = gate ? (cols + 127) / 128 : (N + 255) / 256;
+    if (wide_m * wide_n * 4 >= cus * 3) {
         s.kind = WIDE;
-        s.mt = (M + 255) / 256;
-        s.nt = (cols + wide_n - 1) / wide_n;
+        s.mt = wide_m;
+        s.nt = wide_n;
+        return s;
+    }
+    const int64_t plain = wide_m * ((N + 255) / 256), sp = cus / plain;  // pieces use plain tiles
+    if (sp >= 2 && steps / sp >= 8 &&
+        ((double)M * N * K >= 2e10 || (sp <= 8 && (M > N ? M : N) * K * 2 >= (64 << 20)))) {
+        s.kind = WIDE;
+        s.mt = wide_m;
+        s.nt = (N + 255) / 256;
+        set_splits(s, K, sp, 8);
+        s.pieces = true;
         return s;
     }
     const int64_t small = (M + 63) / 64 * ((N + 63) / 64);
-    // 64 x 64 tiles read the operands twice as often as 128 x 128 ones, which long sums
-    // pay for: 2000 x 2000 over 1000 takes 22.8 us (27.0 on 128 x 128 tiles), 8192 x 256
-    // over 7168 takes 49 us (43.8)
-    if (small <= cus || (small <= 4 * cus && K <= 1024)) {
+    if (small <= cus / 2 || (small <= cus && K <= 4096) || (small <= 4 * cus && K <= 1024)) {
         s.kind = SMALL;
         s.mt = (M + 63) / 64;
         s.nt = (N + 63) / 64;  // (32 columns each of G and U for EPI_GATE)
-        // the 8-bit save takes whole blocks, in the sum of the pieces
         set_splits(s, K, 2 * cus / small, 16);
+        // the 8-bit save takes whole blocks, in the sum of the pieces
         s.pieces = s.splits > 1 || epi == EPI_GATE8;
         return s;
     }
     s.kind = TILES;
     const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
-    set_splits(s, K, 2 * cus / tiles, 8);
+    if (tiles < cus) set_splits(s, K, 2 * cus / tiles, 8);
     s.pieces = s.splits > 1;
-    const int64_t bm = gate && s.splits == 1 ? 64 : 128;
+    const int64_t bm = gate && !s.pieces ? 64 : 128;
     s.mt = (M + bm - 1) / bm;
-    s.nt = ((s.splits > 1 ? N : cols) + 127) / 128;
+    s.nt = ((s.pieces ? N : cols) + 127) / 128;
     return s;
 }
 template <int WM, int WN, int LA, int LB, int EPI>
@@ -759,10 +773,16 @@ int launch_small(const DenseArgs& g, int la, int lb, int splits, hipStream_t str
     return launch_small_one<OP_KS, OP_KS, EPI>(g, splits, stream);
 }
 template <int LA, int LB, int EPI>
-int launch_wide(const DenseArgs& g, hipStream_t stream) {
-    dense_wide_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt)), dim3(512), 0, stream>>>(g);
+int launch_wide(const DenseArgs& g, int splits, hipStream_t stream) {
+    dense_wide_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt * splits)), dim3(512), 0, stream>>>(g);
     MOE_LAUNCH_CHECK("dense_wide_kernel");
     return MOE_OK;
+}
+template <int EPI>
+int launch_wide_any(const DenseArgs& g, int la, int lb, int splits, hipStream_t stream) {
+    if (la == OP_KC && lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI>(g, splits, stream);
+    if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI>(g, splits, stream);
+    return launch_wide<OP_KS, OP_KS, EPI>(g, splits, stream);
 }
 template <int EPI>
 int launch_sum(const DenseArgs& g, int splits, hipStream_t stream) {
@@ -804,6 +824,7 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         g.part_ld = round_up(g.N, 4);
         const int rc = s.kind == SLAB    ? dense_slab_launch(g, s.splits, stream)
                        : s.kind == SMALL ? launch_small<EPI_PART>(g, la, lb, s.splits, stream)
+                       : s.kind == WIDE  ? launch_wide_any<EPI_PART>(g, la, lb, s.splits, stream)
                                          : launch_layout<EPI_PART>(g, la, lb, s.splits, stream);
         if (rc != MOE_OK) return rc;
         if (epi == EPI_GATE) return launch_sum<EPI_GATE>(g, s.splits, stream);
@@ -820,14 +841,12 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         return launch_small<EPI_PLAIN>(g, la, lb, 1, stream);
     }
     if (s.kind == WIDE) {
-        if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, stream);
-        if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, stream);
-        if (epi == EPI_DGATE8) return launch_wide<OP_KC, OP_KS, EPI_DGATE8>(g, stream);
+        if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
+        if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);
+        if (epi == EPI_DGATE8) return launch_wide<OP_KC, OP_KS, EPI_DGATE8>(g, 1, stream);
+        if (epi == EPI_LINEAR) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, 1, stream);
         // (data and weight gradients are always EPI_PLAIN)
-        if (epi == EPI_LINEAR) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, stream);
-        if (lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI_PLAIN>(g, stream);
-        if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI_PLAIN>(g, stream);
-        return launch_wide<OP_KS, OP_KS, EPI_PLAIN>(g, stream);
+        return launch_wide_any<EPI_PLAIN>(g, la, lb, 1, stream);
     }
     if (epi == EPI_GATE) return launch_one<1, 4, OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
     if (epi == EPI_DGATE) return launch_one<2, 2, OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);

@@ -514,13 +514,18 @@ class _Device:
         self.guard.__exit__(*a)
 
 
+# handle of the current stream of a device, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def launch(name, dev, *args):
     """One C-ABI call on ``dev``'s current stream; pointers are plain integers (0
     or None: NULL).  The device is switched only if another one is current."""
     if torch.cuda.current_device() != dev.index:
         with _Device(dev):
             return launch(name, dev, *args)
-    rc = getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream)
+    rc = getattr(lib(), name)(*args, _raw_stream(dev.index))
     if rc != 0:
         raise MoeError(name, rc, last_error())
 
@@ -547,8 +552,7 @@ def act_save(x, out=None):
     dev = x.device
     nb = (cols + 127) // 128
     if out is None:
-        out = (torch.empty((rows, cols), dtype=torch.int8, device=dev),
-               torch.empty((nb, rows), dtype=torch.float32, device=dev))
+        out = x.new_empty((rows, cols), dtype=torch.int8), x.new_empty((nb, rows), dtype=torch.float32)
     else:
         _dense(out[0], (rows, cols), torch.int8, "q", dev)
         _dense(out[1], (nb, rows), torch.float32, "s", dev)
@@ -564,7 +568,7 @@ def act_restore(q, s, out=None):
     _dense(q, (rows, cols), torch.int8, "q", dev)
     _dense(s, ((cols + 127) // 128, rows), torch.float32, "s", dev)
     if out is None:
-        x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        x = q.new_empty((rows, cols), dtype=torch.bfloat16)
     else:
         x = _dense(out, (rows, cols), torch.bfloat16, "out", dev)
     launch("moe_act_restore", dev, q.data_ptr(), s.data_ptr(), rows, cols, x.data_ptr())
