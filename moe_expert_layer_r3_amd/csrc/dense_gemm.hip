@@ -39,12 +39,14 @@ struct TileEpilogue {
     static constexpr int BATCH = EPI == EPI_PLAIN && STEPS % 8 == 0 ? 8 : STEPS < 4 ? STEPS : 4;
     static_assert(STEPS % BATCH == 0, "whole batches");
     EpiIn<EPI> in[READS ? BATCH : 1];
+    EpiBias<EPI> bias;
     // this thread's first row; where a wave takes one row, a scalar
     static __device__ __forceinline__ int first_row() {
         const int r = threadIdx.x / PER_ROW;
         return PER_ROW % 64 == 0 ? __builtin_amdgcn_readfirstlane(r) : r;
     }
     __device__ __forceinline__ void load(const DenseArgs& g, int64_t m0, int n0, int s = 0) {
+        if (s == 0) bias.load(g, n0 + threadIdx.x % PER_ROW * 4);
         if constexpr (READS) {
             const int c = threadIdx.x % PER_ROW, r0 = first_row();
 #pragma unroll
@@ -59,11 +61,11 @@ struct TileEpilogue {
         const v4f v = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c));
         if constexpr (EPI == EPI_GATE) {
             const v4f u = *reinterpret_cast<const v4f*>(sm + stage_at(COLS, r, c + PER_ROW));
-            epi_gate(g, m, n, v, u, m < g.M && n < g.f);
+            epi_gate(g, m, n, v, u, bias, m < g.M && n < g.f);
         } else if constexpr (EPI == EPI_LINEAR) {
-            if (m < g.M && n < g.N) epi_linear(g, m, n, v, in);
+            if (m < g.M && n < g.N) epi_linear(g, m, n, v, in, bias);
         } else if constexpr (EPI == EPI_PLAIN) {
-            if (m < g.M && n < g.N) epi_plain(g, m, n, v, in);
+            if (m < g.M && n < g.N) epi_plain(g, m, n, v, in, bias);
         } else if constexpr (is_dgate(EPI)) {
             if (m < g.M && n < g.f) epi_dgate(g, m, n, v, in);
         } else {
@@ -75,6 +77,7 @@ struct TileEpilogue {
 #pragma unroll 1
         for (int s = 0; s < STEPS; s += BATCH) {
             TileEpilogue next;
+            next.bias = bias;
             if (READS && s + BATCH < STEPS) next.load(g, m0, n0, s + BATCH);
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) step(g, sm, m0, n0, split, s + i, in[READS ? i : 0]);
@@ -651,9 +654,11 @@ __global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits)
         }
         return s;
     };
+    EpiBias<EPI> bias;
+    bias.load(g, n);
     if constexpr (EPI == EPI_GATE) {
         const v4f G = sum(n), U = sum(g.f + n);
-        epi_gate(g, m, n, G, U, on);
+        epi_gate(g, m, n, G, U, bias, on);
     } else {
         if (!on) return;
         EpiIn<EPI> in;
@@ -662,9 +667,9 @@ __global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits)
         if constexpr (is_dgate(EPI))
             epi_dgate(g, m, n, s, in);
         else if constexpr (EPI == EPI_PLAIN)
-            epi_plain(g, m, n, s, in);
+            epi_plain(g, m, n, s, in, bias);
         else
-            epi_linear(g, m, n, s, in);
+            epi_linear(g, m, n, s, in, bias);
     }
 }
 
@@ -861,7 +866,7 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
 // flight: a wave takes 256 columns and CS_ROWS / 4 rows of a chunk, all loaded
 // before the first is added.
 namespace {
-constexpr int CS_ROWS = 32;  // rows of a chunk that are loaded at a time
+constexpr int CS_ROWS = 8;  // rows of a chunk that are loaded at a time
 struct Chunks {
     int n;
     int64_t rows;
@@ -894,13 +899,31 @@ __device__ __forceinline__ v4f load4(const void* src, int f32, int64_t at, int64
 // dz = dy * act'(pre) of moe_linear_backward: bf16 rows of stride ldz (columns
 // past N zero) if dz is given, and fp32 column sums over chunks of rows (before
 // the rounding) if part is given.  One thread per four columns of a row.
+struct DzArgs {
+    const void* dy;
+    int dy_f32;
+    int64_t ld;
+    const uint16_t* pre;  // [T, N]
+    int64_t N, ldz;
+    uint16_t* dz;   // [T, ldz]
+    float* part;    // [chunks, ldz]
+    uint16_t* out;  // [N]
+    int blocks;     // of 256 columns
+};
 template <bool ACT>
-__global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act,
-                                                 int64_t T, int64_t N, int64_t ldz, int64_t rows, uint16_t* dz,
-                                                 float* part) {
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs d0, DzArgs d1, int act, int64_t T, int64_t rows) {
     __shared__ float sm[4][256];
+    const bool second = (int)blockIdx.x >= d0.blocks;
+    const DzArgs& d = second ? d1 : d0;
+    const int bx = blockIdx.x - (second ? d0.blocks : 0);
+    const void* dy = d.dy;
+    const int dy_f32 = d.dy_f32;
+    const int64_t ld = d.ld, N = d.N, ldz = d.ldz;
+    const uint16_t* pre = d.pre;
+    uint16_t* dz = d.dz;
+    float* part = d.part;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t n = (int64_t)blockIdx.x * 256 + lane * 4;
+    const int64_t n = (int64_t)bx * 256 + lane * 4;
     const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = min(t0 + rows, T);
     const bool vec = (N & 3) == 0;
     constexpr int R = CS_ROWS / 4;
@@ -933,18 +956,22 @@ __global__ __launch_bounds__(256) void dz_kernel(const void* dy, int dy_f32, int
 #pragma unroll
     for (int i = 0; i < 4; ++i) sm[w][lane * 4 + i] = s[i];
     __syncthreads();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t c = (int64_t)bx * 256 + threadIdx.x;
     if (c < ldz)
         part[blockIdx.y * ldz + c] =
             (sm[0][threadIdx.x] + sm[1][threadIdx.x]) + (sm[2][threadIdx.x] + sm[3][threadIdx.x]);
 }
 
 // out[n] = bf16 of the chunks' sums: 16 columns per block, 16 threads to a column
-__global__ __launch_bounds__(256) void colsum_finish_kernel(const float* part, int chunks, int64_t ld, int64_t N,
-                                                            uint16_t* out) {
+__global__ __launch_bounds__(256) void colsum_finish_kernel(DzArgs d0, DzArgs d1, int chunks) {
     __shared__ float sm[16][17];
+    const int first = (int)((d0.N + 15) / 16);
+    const bool second = (int)blockIdx.x >= first;
+    const float* part = second ? d1.part : d0.part;
+    uint16_t* out = second ? d1.out : d0.out;
+    const int64_t ld = second ? d1.ldz : d0.ldz, N = second ? d1.N : d0.N;
     const int c = threadIdx.x & 15, q = threadIdx.x >> 4;
-    const int64_t n = (int64_t)blockIdx.x * 16 + c;
+    const int64_t n = (int64_t)(blockIdx.x - (second ? first : 0)) * 16 + c;
     float s = 0.f;
     if (n < N) {
 #pragma unroll 8
@@ -965,25 +992,38 @@ __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
 
 size_t colsum_ws(int64_t T, int64_t N) { return (size_t)colsum_chunks(T).n * N * 4; }
 
-int dz_launch(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz,
-              uint16_t* dz, float* part, uint16_t* dbias, hipStream_t stream) {
+namespace {
+int dz_both(DzArgs d0, DzArgs d1, int act, int64_t T, hipStream_t stream) {
     const Chunks c = colsum_chunks(T);
-    const dim3 grid((unsigned)((ldz + 255) / 256), c.n);
-    float* p = dbias ? part : nullptr;
+    d0.blocks = (int)((d0.ldz + 255) / 256);
+    d1.blocks = (int)((d1.ldz + 255) / 256);
+    const dim3 grid((unsigned)(d0.blocks + d1.blocks), c.n);
     if (act != MOE_ACT_NONE)
-        dz_kernel<true><<<grid, dim3(256), 0, stream>>>(dy, dy_f32, ld, pre, act, T, N, ldz, c.rows, dz, p);
+        dz_kernel<true><<<grid, dim3(256), 0, stream>>>(d0, d1, act, T, c.rows);
     else
-        dz_kernel<false><<<grid, dim3(256), 0, stream>>>(dy, dy_f32, ld, nullptr, act, T, N, ldz, c.rows, dz, p);
+        dz_kernel<false><<<grid, dim3(256), 0, stream>>>(d0, d1, act, T, c.rows);
     MOE_LAUNCH_CHECK("dz_kernel");
-    if (!dbias) return MOE_OK;
-    colsum_finish_kernel<<<dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream>>>(part, c.n, ldz, N, dbias);
+    if (!d0.out) return MOE_OK;
+    const int64_t blocks = (d0.N + 15) / 16 + (d1.N + 15) / 16;
+    colsum_finish_kernel<<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(d0, d1, c.n);
     MOE_LAUNCH_CHECK("colsum_finish_kernel");
     return MOE_OK;
 }
+}  // namespace
 
-int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_t* out, float* part,
-                  hipStream_t stream) {
-    return dz_launch(src, 0, ld, nullptr, MOE_ACT_NONE, T, N, N, nullptr, part, out, stream);
+int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
+              float* part, uint16_t* dbias, hipStream_t stream) {
+    const DzArgs d = {dy, dy_f32, N, pre, N, ldz, dz, dbias ? part : nullptr, dbias, 0};
+    return dz_both(d, DzArgs{}, act, T, stream);
+}
+
+int colsum_launch(const uint16_t* a, int64_t Na, uint16_t* out_a, const uint16_t* b, int64_t Nb, uint16_t* out_b,
+                  int64_t T, float* part, hipStream_t stream) {
+    DzArgs d[2] = {};
+    int n = 0;
+    if (out_a) d[n++] = DzArgs{a, 0, Na, nullptr, Na, Na, nullptr, part, out_a, 0};
+    if (out_b) d[n++] = DzArgs{b, 0, Nb, nullptr, Nb, Nb, nullptr, part + (out_a ? colsum_ws(T, Na) / 4 : 0), out_b, 0};
+    return n ? dz_both(d[0], d[1], MOE_ACT_NONE, T, stream) : MOE_OK;
 }
 
 int zero16_launch(uint16_t* p, int64_t n, hipStream_t stream) {

@@ -272,6 +272,31 @@ struct EpiIn {
         }
     }
 };
+// The biases of columns n .. n + 3 (a thread's columns are the same for all its rows)
+template <int EPI>
+struct EpiBias {
+    v4f a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};  // EPI_GATE: of G and U
+    __device__ __forceinline__ void load(const DenseArgs& g, int n) {
+        if constexpr (EPI == EPI_LINEAR || EPI == EPI_PLAIN || EPI == EPI_GATE) {
+            if (!g.bias) return;
+            float t[4];
+            if constexpr (EPI == EPI_GATE) {
+                if (n >= g.f) return;
+                load_bf16x4(g.bias + n, t);
+                a = v4f{t[0], t[1], t[2], t[3]};
+                load_bf16x4(g.bias + g.f + n, t);
+                b = v4f{t[0], t[1], t[2], t[3]};
+            } else if (EPI == EPI_PLAIN || g.vec) {
+                if (n >= g.N) return;
+                load_bf16x4(g.bias + n, t);
+                a = v4f{t[0], t[1], t[2], t[3]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = bf16_to_f32(g.bias[min(n + i, g.N - 1)]);
+            }
+        }
+    }
+};
 __device__ __forceinline__ void unpack_bf16x4(v2u w, float* v) {
     v[0] = bf16_lo(w.x);
     v[1] = bf16_hi(w.x);
@@ -280,20 +305,11 @@ __device__ __forceinline__ void unpack_bf16x4(v2u w, float* v) {
 }
 
 // EPI_LINEAR for C[m, n .. n + 3], m < M, n < N
-__device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_LINEAR>& in) {
+__device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_LINEAR>& in,
+                                           const EpiBias<EPI_LINEAR>& bias) {
     const int left = g.N - n;
+    c += bias.a;
     float v[4] = {c.x, c.y, c.z, c.w}, t[4];
-    if (g.bias) {
-        if (g.vec) {
-            load_bf16x4(g.bias + n, t);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += t[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left) v[i] += bf16_to_f32(g.bias[n + i]);
-        }
-    }
     if (g.pre) {
         uint16_t* p = g.pre + m * g.N + n;
         const v2u w = pack_bf16x4(v[0], v[1], v[2], v[3]);
@@ -336,12 +352,10 @@ __device__ __forceinline__ void epi_linear(const DenseArgs& g, int64_t m, int n,
 }
 
 // EPI_PLAIN for C[m, n .. n + 3], m < M, n < N
-__device__ __forceinline__ void epi_plain(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_PLAIN>& in) {
+__device__ __forceinline__ void epi_plain(const DenseArgs& g, int64_t m, int n, v4f c, const EpiIn<EPI_PLAIN>& in,
+                                          const EpiBias<EPI_PLAIN>& bias) {
     float t[4];
-    if (g.bias) {
-        load_bf16x4(g.bias + n, t);
-        c += v4f{t[0], t[1], t[2], t[3]};
-    }
+    c += bias.a;
     if (g.res) {
         unpack_bf16x4(in.a, t);
         c += v4f{t[0], t[1], t[2], t[3]};
@@ -382,14 +396,10 @@ __device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, 
 // EPI_GATE for the sums G, U[m, n .. n + 3]; `on`: m < M and n < f.  With the 8-bit
 // save (f % 128 == 0) 32 adjacent lanes hold one 128-column block of a row, and
 // every lane of a wave calls.
-__device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v4f G, v4f U, bool on) {
-    if (on && g.bias) {
-        float t[4];
-        load_bf16x4(g.bias + n, t);
-        G += v4f{t[0], t[1], t[2], t[3]};
-        load_bf16x4(g.bias + g.f + n, t);
-        U += v4f{t[0], t[1], t[2], t[3]};
-    }
+__device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v4f G, v4f U,
+                                         const EpiBias<EPI_GATE>& bias, bool on) {
+    G += bias.a;
+    U += bias.b;
     if (g.save == MOE_SAVE_INT8) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
@@ -451,15 +461,16 @@ int dense_slab_launch(const DenseArgs& g, int splits, hipStream_t stream);
 // fp32 workspace of a product with M x N results and K summands
 size_t dense_ws(int64_t M, int64_t N, int64_t K, int la, int lb, int epi);
 
-// column sums of src [T, N] bf16 (row stride ld, N % 4 == 0) as bf16; part: fp32
-// workspace of colsum_ws bytes
+// column sums of a [T, Na] and b [T, Nb] (bf16, dense, Na, Nb % 4 == 0) as bf16,
+// each skipped if its output is NULL; part: fp32 workspace of colsum_ws bytes for
+// each of the two
 size_t colsum_ws(int64_t T, int64_t N);
-int colsum_launch(const uint16_t* src, int64_t ld, int64_t T, int64_t N, uint16_t* out, float* part,
-                  hipStream_t stream);
+int colsum_launch(const uint16_t* a, int64_t Na, uint16_t* out_a, const uint16_t* b, int64_t Nb, uint16_t* out_b,
+                  int64_t T, float* part, hipStream_t stream);
 // dz = dy * act'(pre) [T, ldz] bf16 (dz may be NULL) and its column sums (dbias
-// may be NULL; part then unused); ldz = N rounded up to 8
-int dz_launch(const void* dy, int dy_f32, int64_t ld, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz,
-              uint16_t* dz, float* part, uint16_t* dbias, hipStream_t stream);
+// may be NULL; part then unused); dy [T, N] dense, ldz = N rounded up to 8
+int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
+              float* part, uint16_t* dbias, hipStream_t stream);
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }

@@ -8,11 +8,13 @@ template <int EPI>
 __device__ __forceinline__ void finish(const DenseArgs& g, int m, int n, v4f v) {
     if (n >= g.N) return;
     EpiIn<EPI> in;
+    EpiBias<EPI> bias;
     in.load(g, m, n);
+    bias.load(g, n);
     if constexpr (EPI == EPI_PLAIN)
-        epi_plain(g, m, n, v, in);
+        epi_plain(g, m, n, v, in, bias);
     else
-        epi_linear(g, m, n, v, in);
+        epi_linear(g, m, n, v, in, bias);
 }
 
 // dense_thin_kernel (up to 4 rows): a workgroup owns R rows of W and its NW waves
@@ -109,7 +111,9 @@ __global__ __launch_bounds__(NW * 64) void dense_thin_kernel(DenseArgs g) {
         const int n4 = n0 + (lane >> 4) * 4;
         if constexpr (GATE) {
             const v4f G = sum(lane), U4 = sum(lane + 32);  // G rows 0-7, U rows 8-15
-            epi_gate(g, l15, n4, G, U4, n4 < g.f);
+            EpiBias<EPI_GATE> bias;
+            bias.load(g, n4);
+            epi_gate(g, l15, n4, G, U4, bias, n4 < g.f);
         } else {
             finish<EPI>(g, l15, n4, sum(lane));
         }

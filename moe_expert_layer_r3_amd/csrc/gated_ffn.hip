@@ -36,8 +36,7 @@ BackwardWs backward_ws(int64_t T, int64_t d, int64_t f) {
     w.dgu = 0;
     w.h = (size_t)round_up(T * 2 * f * 2, 256);
     w.part = w.h + (size_t)round_up(T * f * 2, 256);
-    const size_t c1 = colsum_ws(T, 2 * f), c2 = colsum_ws(T, d);
-    w.gemm = w.part + (size_t)round_up((int64_t)(c1 > c2 ? c1 : c2), 256);
+    w.gemm = w.part + (size_t)round_up((int64_t)(colsum_ws(T, 2 * f) + colsum_ws(T, d)), 256);
     size_t g = 0;
     for (const size_t s : {dense_ws(T, f, d, OP_KC, OP_KS, EPI_DGATE), dense_ws(T, d, 2 * f, OP_KC, OP_KS, EPI_LINEAR),
                            dense_ws(2 * f, d, T, OP_KS, OP_KS, EPI_LINEAR), dense_ws(d, f, T, OP_KS, OP_KS, EPI_LINEAR)})
@@ -223,9 +222,5 @@ extern "C" int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int
         g.ldo = f;
         if (const int rc = dense_launch(g, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
     }
-    if (db13)
-        if (const int rc = colsum_launch(dgu, 2 * f, T, 2 * f, db13, part, stream)) return rc;
-    if (db2)
-        if (const int rc = colsum_launch(dy, d, T, d, db2, part, stream)) return rc;
-    return MOE_OK;
+    return colsum_launch(dgu, 2 * f, db13, dy, d, db2, T, part, stream);
 }

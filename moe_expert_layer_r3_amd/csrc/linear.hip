@@ -133,7 +133,7 @@ extern "C" int moe_linear_backward(const void* dy, int32_t dy_type, const uint16
     const bool own = needs_dz(dy_type, N, act);
     if (own || dbias) {
         const int64_t ldp = round_up(N, 8);
-        if (const int rc = dz_launch(dy, dy_type == MOE_SRC_F32, N, act == MOE_ACT_NONE ? nullptr : pre, act, T, N, ldp,
+        if (const int rc = dz_launch(dy, dy_type == MOE_SRC_F32, act == MOE_ACT_NONE ? nullptr : pre, act, T, N, ldp,
                                      own && (dx || dW) ? (uint16_t*)(wp + w.dz) : nullptr, (float*)(wp + w.part), dbias,
                                      stream))
             return rc;

@@ -97,7 +97,7 @@ def test_gated_ffn_backward_refusals(kw, want):
 @pytest.mark.parametrize("kw, want", [
     (dict(rows=-1), -2), (dict(cols=12), -2), (dict(cols=0), -2), (dict(src=None), -1), (dict(q=None), -1),
     (dict(s=None), -1), (dict(ld=120), -2), (dict(ld=132), -2), (dict(src=ODD), -2), (dict(q=ODD), -2),
-    (dict(rows=1 << 30, cols=1 << 20, ld=1 << 20), -2), (dict(rows=0, src=None), 0),
+    (dict(rows=1 << 30, cols=1 << 20, ld=1 << 20), -2), (dict(s=ODD), -2), (dict(rows=0, src=None), 0),
 ])
 def test_act_save_refusals(kw, want):
     assert rc("moe_act_save", dict(src=A, ld=128, rows=4, cols=128, q=A, s=A, st=None), **kw) == want
