@@ -1,6 +1,7 @@
 """The dense products around the routed experts, as plans of C-ABI calls on
 preallocated device buffers (no allocation per step): the router's projection
-and a shared expert's gated feed-forward block, forward and backward.
+and a shared expert's gated feed-forward block, forward and backward, and a
+layer's training step that joins them to the routed experts.
 
 Operands are bf16; x (and LinearPlan's W) may be a column slice of a wider
 buffer.  A plan's outputs are its own buffers, valid until its next call."""
@@ -8,7 +9,7 @@ buffer.  A plan's outputs are its own buffers, valid until its next call."""
 import torch
 
 from . import ops
-from .layer import capture_graph
+from .layer import TrainPlan, capture_graph
 from .ops import _dense, _Device, launch, rows_of, workspace_bytes
 
 BF16 = torch.bfloat16
@@ -160,3 +161,51 @@ class GatedFFNPlan:
     def capture(self, x, W13, W2, b13=None, b2=None, residual=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
         return capture_graph(lambda: self.forward(x, W13, W2, b13=b13, b2=b2, residual=residual), warmup)
+
+
+class MoELayerPlan:
+    """One MoE layer's training step with what surrounds the routed experts:
+
+        logits = x Wr^T + br                     (router, fp32)
+        y      = routed experts(x, logits) + shared expert(x)
+
+    on preallocated buffers: a LinearPlan, a TrainPlan and a GatedFFNPlan whose
+    sums ride in the products' epilogues (the shared expert adds the routed
+    experts' y, the data gradients add up in turn).  act8: what the backward needs
+    of the shared expert, x and [G, U], is kept in 8 bits (fs % 128 == 0).
+    Needs every expert on this GPU (L == E): under expert parallelism d_logits
+    has to be summed over the GPUs between the parts."""
+
+    def __init__(self, T, d, f, E, k, fs, act="silu", act8=False, router_bias=False, device="cuda"):
+        self.T, self.d = T, d
+        self.router = LinearPlan(T, d, E, out_dtype=torch.float32, train=True, bias=router_bias, device=device)
+        dv = self.router.device
+        self.routed = TrainPlan(T, d, f, E, E, k, device=dv)
+        self.shared = GatedFFNPlan(T, d, fs, act=act, save="int8" if act8 else "bf16", device=dv)
+        self.x8 = self.xr = None
+        if act8:
+            self.x8 = (torch.empty((T, d), dtype=torch.int8, device=dv),
+                       torch.empty(((d + 127) // 128, T), dtype=torch.float32, device=dv))
+            self.xr = torch.empty((T, d), dtype=BF16, device=dv)
+
+    def forward(self, x, Wr, wts, W13s, W2s, br=None):
+        """y [T, d]; wts from quantize_weights (with its transposed copies where
+        ``self.routed.transpose_weights``)."""
+        with _Device(self.router.device):
+            if self.x8 is not None:
+                ops.act_save(x, out=self.x8)
+            logits = self.router.forward(x, Wr, bias=br)
+            y = self.routed.forward(x, logits, wts)
+            return self.shared.forward(x, W13s, W2s, residual=y)
+
+    def backward(self, dy, x, Wr, wts, W13s, W2s):
+        """Gradients of the last forward: dict of dx, dWr, dbr (None without
+        router_bias), dW13 and dW2 (routed experts), dW13s and dW2s.  With act8,
+        x is not read (None will do)."""
+        with _Device(self.router.device):
+            if self.x8 is not None:
+                x = ops.act_restore(*self.x8, out=self.xr)
+            dx, dW13, dW2, d_logits = self.routed.backward(x, dy, wts)
+            dx, dWr, dbr = self.router.backward(d_logits, x, Wr, dx_add=dx)
+            dx, dW13s, dW2s, _, _ = self.shared.backward(dy, x, W13s, W2s, dx_add=dx)
+        return dict(dx=dx, dWr=dWr, dbr=dbr, dW13=dW13, dW2=dW2, dW13s=dW13s, dW2s=dW2s)
