@@ -7,9 +7,9 @@ namespace moe {
 // Tile index of a workgroup: XCD x runs a contiguous eighth of the tiles, which
 // go m fastest inside groups of 8 m-tiles, so that the tiles an XCD runs side by
 // side share few A and B tiles in its L2.
-__device__ __forceinline__ void dense_tile(const DenseArgs& g, int& mt, int& nt, int& split) {
+__device__ __forceinline__ void dense_tile(const DenseArgs& g, int bid, int tiles, int& mt, int& nt, int& split) {
     const int per = g.mt * g.nt;
-    const int t0 = (int)xcd_tile(blockIdx.x, gridDim.x);
+    const int t0 = (int)xcd_tile(bid, tiles);
     split = t0 / per;
     const int t = t0 - split * per;
     constexpr int GM = 8;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     int mt, nt, split;
-    dense_tile(g, mt, nt, split);
+    dense_tile(g, blockIdx.x, gridDim.x, mt, nt, split);
     const int64_t m0 = (int64_t)mt * BM;
     const int n0 = nt * (EPI == EPI_GATE ? 128 : BN);
     const int ks0 = split * g.ksteps;
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int mt, nt, split;
-    dense_tile(g, mt, nt, split);
+    dense_tile(g, blockIdx.x, gridDim.x, mt, nt, split);
     const int64_t m0 = (int64_t)mt * 64;
     const int n0 = nt * (EPI == EPI_GATE ? 32 : 64);
     const int ks0 = split * g.ksteps;
@@ -402,66 +402,111 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
 // refill is awaited (vmcnt(8): those of the last two phases stay in flight) one
 // phase before it is read, ahead of a barrier.  Steps past the end fill zeros
 // without reading memory, so the counts hold to the last step.
-template <int LA, int LB, int EPI>
-__global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
+//
+// Workgroups are persistent (one per compute unit).  At the end of a tile the DMA of
+// the next one's first steps goes out before the results leave, straight from the
+// accumulators (DIRECT): lanes trade 16-column pieces (permlane16_swap) so that
+// each holds 8 adjacent columns.  The general
+// epilogues, too long to be written out for every register, go through LDS.
+//
+// act: the activation of the gated epilogues at compile time (-1: at run time).
+constexpr bool is_direct(int epi, int act) {
+    return epi == EPI_PLAIN || epi == EPI_PART || ((epi == EPI_GATE || is_dgate(epi)) && act >= 0);
+}
+
+// A lane's results after the swap: 8 adjacent columns from n
+__device__ __forceinline__ void swap_cols(v4f& a, v4f& b) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        uint32_t x = __float_as_uint(a[r]), y = __float_as_uint(b[r]);
+        swap16(x, y);
+        a[r] = __uint_as_float(x);
+        b[r] = __uint_as_float(y);
+    }
+}
+__device__ __forceinline__ u32x4 pack_bf16x8(const v4f& a, const v4f& b) {
+    return u32x4{cvt_bf16x2(a.x, a.y), cvt_bf16x2(a.z, a.w), cvt_bf16x2(b.x, b.y), cvt_bf16x2(b.z, b.w)};
+}
+__device__ __forceinline__ void unpack_bf16x8(const u32x4& w, v4f& a, v4f& b) {
+    a = v4f{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+    b = v4f{bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
+}
+
+template <int LA, int LB, int EPI, int ACT>
+__global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int tiles) {
     constexpr int HALF = 16384, STAGE = 4 * HALF;
-    static_assert(EPI != EPI_GATE || LB == OP_KC, "gated tiles pair 128 G with 128 U rows of W13");
+    constexpr bool GATE = EPI == EPI_GATE, DIRECT = is_direct(EPI, ACT);
+    static_assert(!GATE || LB == OP_KC, "gated tiles pair 128 G with 128 U rows of W13");
+    // A wave's 32 columns of half b of B begin at wn WSTEP + b HSTEP: 64 adjacent
+    // columns for KC operands, whose rows may be dealt at will; a KS operand's 128
+    // columns of a half stay adjacent (64-byte pieces of its rows cost 5%)
+    constexpr int WSTEP = LB == OP_KC && !GATE ? 64 : 32, HSTEP = LB == OP_KC && !GATE ? 32 : 128;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+    // EPI_GATE with the 8-bit save: row maxima [wave column][G, U][row]
+    __shared__ uint32_t rowmax[GATE && DIRECT ? 4 : 1][2][256];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    int mt, nt, split;
-    dense_tile(g, mt, nt, split);
-    const int64_t m0 = (int64_t)mt * 256;
-    const int n0 = nt * (EPI == EPI_GATE ? 128 : 256);
-    const int ks0 = split * g.ksteps;
-    const int ks1 = min(ks0 + g.ksteps, (g.K + DBK - 1) / DBK);
-    const int kend = min(g.K, ks1 * DBK);
+    const int l15 = lane & 15, g4 = lane >> 4;
     const uint32_t sbase = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+    const int64_t step_a = LA == OP_KC ? 128 : (int64_t)DBK * g.lda * 2;
+    const int64_t step_b = LB == OP_KC ? 128 : (int64_t)DBK * g.ldb * 2;
 
-    // DMA: wave w moves segments 2w, 2w + 1 of every half: KC rows 16w .. + 15
-    // (one K chunk per lane), KS K rows 8w .. + 7
+    // ---- the current tile
+    int64_t m0 = 0;
+    int n0 = 0, split = 0, ks0 = 0, ks1 = 0, kend = 0;
+    // DMA: wave w moves segments 2w, 2w + 1 of every half: KC rows 16w .. + 15 (one
+    // K chunk per lane), KS K rows 8w .. + 7
     uint32_t va[2][2], vb[2][2];
     const uint8_t *pa[2], *pb[2];
     const KcLane la(lane, g.lda), lb(lane, g.ldb);
     const uint32_t kseg = wave * 8 + (lane >> 4);  // KS: K row of segment 0, + 4 of segment 1
+    auto setup = [&](int t) {
+        int mt, nt;
+        dense_tile(g, t, tiles, mt, nt, split);
+        m0 = (int64_t)mt * 256;
+        n0 = nt * (GATE ? 128 : 256);
+        ks0 = split * g.ksteps;
+        ks1 = min(ks0 + g.ksteps, (g.K + DBK - 1) / DBK);
+        kend = min(g.K, ks1 * DBK);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if constexpr (LA == OP_KC) {
-            const int64_t r0 = m0 + h * 128 + wave * 16;
-            pa[h] = (const uint8_t*)(g.a + r0 * g.lda);
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (LA == OP_KC) {
+                const int64_t r0 = m0 + h * 128 + wave * 16;
+                pa[h] = (const uint8_t*)(g.a + r0 * g.lda);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                va[h][i] = r0 + 8 * i + la.row < g.M ? la.off + (uint32_t)(8 * i * g.lda * 2) : OOB;
-        } else {
-            const int64_t c0 = m0 + h * 128;
-            pa[h] = (const uint8_t*)(g.a + c0);
+                for (int i = 0; i < 2; ++i)
+                    va[h][i] = r0 + 8 * i + la.row < g.M ? la.off + (uint32_t)(8 * i * g.lda * 2) : OOB;
+            } else {
+                const int64_t c0 = m0 + h * 128;
+                pa[h] = (const uint8_t*)(g.a + c0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
-                va[h][i] = c0 + c * 8 < g.a_cols ? k * (uint32_t)(g.lda * 2) + c * 16 : OOB;
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
+                    va[h][i] = c0 + c * 8 < g.a_cols ? k * (uint32_t)(g.lda * 2) + c * 16 : OOB;
+                }
+            }
+            // (EPI_GATE: half 0 is G, half 1 U)
+            if constexpr (LB == OP_KC) {
+                const int64_t r0 = GATE ? (int64_t)h * g.f + n0 + wave * 16
+                                        : n0 + (wave >> 1) * WSTEP + h * HSTEP + (wave & 1) * 16;
+                const int64_t lim = GATE ? (int64_t)(h + 1) * g.f : g.N;
+                pb[h] = (const uint8_t*)(g.b + r0 * g.ldb);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    vb[h][i] = r0 + 8 * i + lb.row < lim ? lb.off + (uint32_t)(8 * i * g.ldb * 2) : OOB;
+            } else {
+                const int64_t c0 = n0 + h * 128;
+                pb[h] = (const uint8_t*)(g.b + c0);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
+                    vb[h][i] = c0 + c * 8 < g.b_cols ? k * (uint32_t)(g.ldb * 2) + c * 16 : OOB;
+                }
             }
         }
-        if constexpr (LB == OP_KC) {
-            const int64_t r0 = (EPI == EPI_GATE ? (int64_t)h * g.f + n0 : n0 + (int64_t)h * 128) + wave * 16;
-            const int64_t lim = EPI == EPI_GATE ? (int64_t)(h + 1) * g.f : g.N;
-            pb[h] = (const uint8_t*)(g.b + r0 * g.ldb);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                vb[h][i] = r0 + 8 * i + lb.row < lim ? lb.off + (uint32_t)(8 * i * g.ldb * 2) : OOB;
-        } else {
-            const int64_t c0 = n0 + h * 128;
-            pb[h] = (const uint8_t*)(g.b + c0);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t k = kseg + 4 * i, c = (lane & 15) ^ (2 * ks_f(k));
-                vb[h][i] = c0 + c * 8 < g.b_cols ? k * (uint32_t)(g.ldb * 2) + c * 16 : OOB;
-            }
-        }
-    }
-    const int64_t step_a = LA == OP_KC ? 128 : (int64_t)DBK * g.lda * 2;
-    const int64_t step_b = LB == OP_KC ? 128 : (int64_t)DBK * g.ldb * 2;
+    };
     // half h of A (B) of K step ks into stage st
     auto issue_a = [&](int st, int h, int ks) {
         const int left = kend - ks * DBK;
@@ -532,15 +577,6 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     };
 
     v4f acc[2][2][4][2];
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
     auto multiply = [&](auto ac, auto st_c) {
         constexpr int a = decltype(ac)::value, st = decltype(st_c)::value;
         wait_lgkm0();
@@ -562,7 +598,8 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
     constexpr std::integral_constant<int, 1> c1;
     constexpr std::integral_constant<int, 2> c2;
     constexpr std::integral_constant<int, HALF> half1;
-    auto kstep = [&](auto st_c, int ks) {
+    // `wait`: not in a tile's first step, whose operands have landed before it begins
+    auto kstep = [&](auto st_c, int ks, bool wait) {
         constexpr int st = decltype(st_c)::value;
         constexpr std::integral_constant<int, st ^ 1> other;
         uint32_t base = sbase + st * STAGE, next = sbase + (st ^ 1) * STAGE;
@@ -571,7 +608,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
         read_b(half1, c2, base);
         issue_b(st, 0, ks + 2);
         issue_a(st ^ 1, 1, ks + 1);
-        wait_vmcnt<8>();  // A1 of this step, B0 of the next
+        if (wait) wait_vmcnt<8>();  // A1 of this step, B0 of the next
         multiply(c0, st_c);
         pin(base);
         pin(next);
@@ -579,53 +616,299 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g) {
         read_b(c0, other, next);
         issue_a(st, 0, ks + 2);
         issue_b(st, 1, ks + 2);
-        wait_vmcnt<8>();  // A0, B1 of the next step
+        if (wait) wait_vmcnt<8>();  // A0, B1 of the next step
         multiply(c1, st_c);
     };
 
-    issue_b(0, 0, ks0);
-    issue_a(0, 0, ks0);
-    issue_b(0, 1, ks0);
-    issue_b(1, 0, ks0 + 1);
-    issue_a(0, 1, ks0);
-    issue_a(1, 0, ks0 + 1);
-    issue_b(1, 1, ks0 + 1);
-    wait_vmcnt<8>();
-    phase_barrier();
-    {
-        uint32_t base = sbase;
-        pin(base);
-        read_b(c0, c0, base);
-        wait_lgkm0();
-        phase_barrier();
-    }
-    if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
-    for (int ks = ks0; ks < ks1; ks += 2) {
-        kstep(c0, ks);
-        if (ks + 1 < ks1) kstep(c1, ks + 1);
-    }
-    if (wm == 0) phase_barrier();
-    wait_vmcnt<0>();  // the fills past the end have landed: LDS may be reused or given up
-    phase_barrier();
+    // ---- results straight from the accumulators.  Every store comes after
+    // wait_vmcnt<0>: the next tile's first steps, issued before, have then landed, and
+    // no wait of its first step has to wait for the stores.
+    auto leave = [&](int64_t m0, int n0, int split) {
+        const int coff = ((g4 & 1) << 4) | ((g4 & 2) << 2);  // a lane's 8 columns after swap_cols
+        auto row = [&](int u) { return m0 + (u >> 2) * 128 + wm * 64 + (u & 3) * 16 + l15; };  // u: 4 a + i
+        if constexpr (EPI == EPI_PART) {
+            wait_vmcnt<0>();
+            static_for<0, 8>([&](auto uc) {
+                constexpr int u = decltype(uc)::value;
+                const int64_t m = row(u);
+                float* p = g.part + ((int64_t)split * g.M + m) * g.part_ld;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int n = n0 + wn * WSTEP + b * HSTEP + j * 16 + g4 * 4;
+                        if (m < g.M && n < g.part_ld) *reinterpret_cast<v4f*>(p + n) = acc[u >> 2][b][u & 3][j];
+                    }
+            });
+        } else if constexpr (EPI == EPI_PLAIN) {
+            u32x4 r[8][2];
+            const int n = n0 + wn * WSTEP + coff;
+            const bool on[2] = {n < g.N, n + HSTEP < g.N};
+            if (g.res) {
+                static_for<0, 8>([&](auto uc) {
+                    constexpr int u = decltype(uc)::value;
+                    const int64_t m = min(row(u), (int64_t)g.M - 1);
+                    const uint16_t* p = g.res + m * g.ldr;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) r[u][b] = *reinterpret_cast<const u32x4*>(p + (on[b] ? n + b * HSTEP : 0));
+                });
+            }
+            wait_vmcnt<0>();
+            static_for<0, 8>([&](auto uc) {
+                constexpr int u = decltype(uc)::value;
+                const int64_t m = row(u);
+                uint16_t* p = (uint16_t*)g.out + m * g.ldo;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    v4f v0 = acc[u >> 2][b][u & 3][0], v1 = acc[u >> 2][b][u & 3][1];
+                    swap_cols(v0, v1);
+                    if (g.bias) {
+                        v4f t0, t1;
+                        unpack_bf16x8(*reinterpret_cast<const u32x4*>(g.bias + (on[b] ? n + b * HSTEP : 0)), t0, t1);
+                        v0 += t0;
+                        v1 += t1;
+                    }
+                    if (g.res) {
+                        v4f t0, t1;
+                        unpack_bf16x8(r[u][b], t0, t1);
+                        v0 += t0;
+                        v1 += t1;
+                    }
+                    if (m < g.M && on[b]) *reinterpret_cast<u32x4*>(p + n + b * HSTEP) = pack_bf16x8(v0, v1);
+                }
+            });
+        } else if constexpr (EPI == EPI_GATE) {
+            const int nj = n0 + wn * 32 + g4 * 4, n = n0 + wn * 32 + coff;
+            if (g.bias) {
+                EpiBias<EPI_GATE> bias[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) bias[j].load(g, nj + j * 16);
+                static_for<0, 8>([&](auto uc) {
+                    constexpr int u = decltype(uc)::value;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        acc[u >> 2][0][u & 3][j] += bias[j].a;
+                        acc[u >> 2][1][u & 3][j] += bias[j].b;
+                    }
+                });
+            }
+            if (g.save == MOE_SAVE_INT8) {
+                static_for<0, 8>([&](auto uc) {
+                    constexpr int u = decltype(uc)::value;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) mx = umax(mx, abs_bits(acc[u >> 2][w][u & 3][j][q]));
+                        mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 16));
+                        mx = umax(mx, (uint32_t)__shfl_xor((int)mx, 32));
+                        if (lane < 16) rowmax[wn][w][(u >> 2) * 128 + wm * 64 + (u & 3) * 16 + l15] = mx;
+                    }
+                });
+                wait_lgkm0();
+                phase_barrier();
+            }
+            wait_vmcnt<0>();
+            const bool on = n < g.f;
+            static_for<0, 8>([&](auto uc) {
+                constexpr int u = decltype(uc)::value;
+                const int64_t m = row(u);
+                const bool mine = on && m < g.M;
+                const v4f G[2] = {acc[u >> 2][0][u & 3][0], acc[u >> 2][0][u & 3][1]};
+                const v4f U[2] = {acc[u >> 2][1][u & 3][0], acc[u >> 2][1][u & 3][1]};
+                if (g.save == MOE_SAVE_INT8) {
+                    const int r = (u >> 2) * 128 + wm * 64 + (u & 3) * 16 + l15;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        uint32_t mx = rowmax[0][w][r];
+#pragma unroll
+                        for (int v = 1; v < 4; ++v) mx = umax(mx, rowmax[v][w][r]);
+                        const Keep8 k = keep8_scale(mx);
+                        if (wn == 0 && lane < 16 && m < g.M)
+                            g.gu_s[((int64_t)(w * (g.f >> 7)) + (n0 >> 7)) * g.M + m] = k.s;
+                        uint32_t q[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const v4f v = w ? U[j] : G[j];
+                            q[j] = pack_s8x4(keep8_code(v.x, k.inv), keep8_code(v.y, k.inv), keep8_code(v.z, k.inv),
+                                             keep8_code(v.w, k.inv));
+                        }
+                        swap16(q[0], q[1]);
+                        if (mine)
+                            *reinterpret_cast<v2u*>((int8_t*)g.gu + m * (2 * (int64_t)g.f) + (int64_t)w * g.f + n) =
+                                v2u{q[0], q[1]};
+                    }
+                }
+                auto put = [&](uint16_t* p, const v4f& a, const v4f& b) {
+                    v2u x = pack_bf16x4(a.x, a.y, a.z, a.w), y = pack_bf16x4(b.x, b.y, b.z, b.w);
+                    uint32_t x0 = x.x, x1 = x.y, y0 = y.x, y1 = y.y;
+                    swap16(x0, y0);
+                    swap16(x1, y1);
+                    if (mine) *reinterpret_cast<u32x4*>(p) = u32x4{x0, x1, y0, y1};
+                };
+                if (g.save == MOE_SAVE_BF16) {
+                    uint16_t* p = (uint16_t*)g.gu + m * (2 * (int64_t)g.f) + n;
+                    put(p, G[0], G[1]);
+                    put(p + g.f, U[0], U[1]);
+                }
+                v4f h[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float z[4] = {G[j].x, G[j].y, G[j].z, G[j].w};
+                    float v[4];
+                    act_value4(ACT, z, v);
+                    h[j] = v4f{v[0], v[1], v[2], v[3]} * U[j];
+                }
+                put(g.h + m * (int64_t)g.f + n, h[0], h[1]);
+            });
+        } else {  // EPI_DGATE, EPI_DGATE8: four 16-row subtiles' loads in flight
+            const int n = n0 + wn * WSTEP + coff;
+            const bool on[2] = {n < g.f, n + HSTEP < g.f};
+            constexpr bool I8 = EPI == EPI_DGATE8;
+            u32x4 q[4][2][I8 ? 1 : 2];
+            float sc[I8 ? 4 : 1][2][2];
+            auto load = [&](auto uc) {
+                constexpr int u = decltype(uc)::value, at = u & 3;
+                const int64_t m = min(row(u), (int64_t)g.M - 1);
+                const int64_t o = m * (2 * (int64_t)g.f);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int c = on[b] ? n + b * HSTEP : 0;
+                    if constexpr (I8) {
+                        const v2u x = *reinterpret_cast<const v2u*>((const int8_t*)g.gu + o + c);
+                        const v2u y = *reinterpret_cast<const v2u*>((const int8_t*)g.gu + o + g.f + c);
+                        q[at][b][0] = u32x4{x.x, x.y, y.x, y.y};
+                        sc[at][b][0] = g.gu_s[(int64_t)(c >> 7) * g.M + m];
+                        sc[at][b][1] = g.gu_s[(int64_t)((g.f >> 7) + (c >> 7)) * g.M + m];
+                    } else {
+                        q[at][b][0] = *reinterpret_cast<const u32x4*>((const uint16_t*)g.gu + o + c);
+                        q[at][b][1] = *reinterpret_cast<const u32x4*>((const uint16_t*)g.gu + o + g.f + c);
+                    }
+                }
+            };
+            static_for<0, 4>([&](auto uc) { load(uc); });
+            wait_vmcnt<0>();
+            static_for<0, 8>([&](auto uc) {
+                constexpr int u = decltype(uc)::value, at = u & 3;
+                const int64_t m = row(u);
+                uint16_t* p = g.dgu + m * (2 * (int64_t)g.f) + n;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    v4f dh[2] = {acc[u >> 2][b][u & 3][0], acc[u >> 2][b][u & 3][1]};
+                    swap_cols(dh[0], dh[1]);
+                    v4f G[2], U[2], dG[2], dU[2], h[2];
+                    if constexpr (I8) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                G[j][e] = s8_of(q[at][b][0][j], e) * sc[at][b][0];
+                                U[j][e] = s8_of(q[at][b][0][2 + j], e) * sc[at][b][1];
+                            }
+                    } else {
+                        unpack_bf16x8(q[at][b][0], G[0], G[1]);
+                        unpack_bf16x8(q[at][b][1], U[0], U[1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float z[4] = {G[j].x, G[j].y, G[j].z, G[j].w};
+                        float v[4], sl[4];
+                        act_both4(ACT, z, v, sl);
+                        const v4f vv = {v[0], v[1], v[2], v[3]}, ss = {sl[0], sl[1], sl[2], sl[3]};
+                        dG[j] = dh[j] * U[j] * ss;
+                        dU[j] = dh[j] * vv;
+                        h[j] = vv * U[j];
+                    }
+                    if (m < g.M && on[b]) {
+                        *reinterpret_cast<u32x4*>(p + b * HSTEP) = pack_bf16x8(dG[0], dG[1]);
+                        *reinterpret_cast<u32x4*>(p + g.f + b * HSTEP) = pack_bf16x8(dU[0], dU[1]);
+                        if (g.h)
+                            *reinterpret_cast<u32x4*>(g.h + m * (int64_t)g.f + n + b * HSTEP) = pack_bf16x8(h[0], h[1]);
+                    }
+                }
+                if constexpr (u < 4) load(std::integral_constant<int, u + 4>{});
+            });
+        }
+    };
+    // ---- or through LDS, a 128-row half at a time
+    auto leave_staged = [&](int64_t m0, int n0, int split) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            TileEpilogue<EPI, 128, 256, 512> epi;
+            epi.load(g, m0 + a * 128, n0);
+            if (a) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = (wn * WSTEP + b * HSTEP + j * 16) / 4;
+                        *reinterpret_cast<v4f*>(smem + stage_at(256, wm * 64 + i * 16 + l15, c + g4)) = acc[a][b][i][j];
+                    }
+            __syncthreads();
+            epi.run(g, smem, m0 + a * 128, n0, split);
+        }
+        __syncthreads();
+    };
 
-    // ---- epilogue, a 128-row half at a time
-    const int l15 = lane & 15, g4 = lane >> 4;
+    bool have = false;  // acc holds a tile's results
+    int64_t pm0 = 0;
+    int pn0 = 0, psplit = 0;
+    for (int t = blockIdx.x;; t += gridDim.x) {
+        const bool more = t < tiles;
+        if constexpr (!DIRECT) {
+            if (have) leave_staged(pm0, pn0, psplit);
+        }
+        if (more) {
+            setup(t);
+            issue_b(0, 0, ks0);
+            issue_a(0, 0, ks0);
+            issue_b(0, 1, ks0);
+            issue_b(1, 0, ks0 + 1);
+            issue_a(0, 1, ks0);
+            issue_a(1, 0, ks0 + 1);
+            issue_b(1, 1, ks0 + 1);
+        }
+        if constexpr (DIRECT) {
+            if (have) leave(pm0, pn0, psplit);
+        }
+        if (!more) break;
+        if (!DIRECT || !have) wait_vmcnt<0>();
+        phase_barrier();
+        {
+            uint32_t base = sbase;
+            pin(base);
+            read_b(c0, c0, base);
+            wait_lgkm0();
+            phase_barrier();
+        }
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-        TileEpilogue<EPI, 128, 256, 512> epi;
-        epi.load(g, m0 + a * 128, n0);
-        if (a) __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    *reinterpret_cast<v4f*>(smem + stage_at(256, wm * 64 + i * 16 + l15, b * 32 + wn * 8 + j * 4 + g4)) =
-                        acc[a][b][i][j];
-        __syncthreads();
-        epi.run(g, smem, m0 + a * 128, n0, split);
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
+        for (int ks = ks0; ks < ks1; ks += 2) {
+            kstep(c0, ks, ks > ks0);
+            if (ks + 1 < ks1) kstep(c1, ks + 1, true);
+        }
+        if (wm == 0) phase_barrier();
+        // every wave has read the last step, and this wave's fills past the end (into
+        // places only it refills) have landed: LDS may be refilled, or reused
+        wait_vmcnt<0>();
+        if constexpr (!DIRECT) phase_barrier();
+        have = true;
+        pm0 = m0;
+        pn0 = n0;
+        psplit = split;
     }
+    wait_vmcnt<0>();
 }
 
 // ---------------------------------------------------------------- split K: sum and epilogue
@@ -777,9 +1060,11 @@ int launch_small(const DenseArgs& g, int la, int lb, int splits, hipStream_t str
     if (la == OP_KC) return launch_small_one<OP_KC, OP_KS, EPI>(g, splits, stream);
     return launch_small_one<OP_KS, OP_KS, EPI>(g, splits, stream);
 }
-template <int LA, int LB, int EPI>
+template <int LA, int LB, int EPI, int ACT = -1>
 int launch_wide(const DenseArgs& g, int splits, hipStream_t stream) {
-    dense_wide_kernel<LA, LB, EPI><<<dim3((unsigned)(g.mt * g.nt * splits)), dim3(512), 0, stream>>>(g);
+    const int tiles = g.mt * g.nt * splits, cus = num_cus() & ~7;
+    const int grid = tiles < cus ? tiles : cus;
+    dense_wide_kernel<LA, LB, EPI, ACT><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(g, tiles);
     MOE_LAUNCH_CHECK("dense_wide_kernel");
     return MOE_OK;
 }
@@ -788,6 +1073,12 @@ int launch_wide_any(const DenseArgs& g, int la, int lb, int splits, hipStream_t 
     if (la == OP_KC && lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI>(g, splits, stream);
     if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI>(g, splits, stream);
     return launch_wide<OP_KS, OP_KS, EPI>(g, splits, stream);
+}
+// the gated epilogues: silu, the usual activation, is compiled in
+template <int LB, int EPI>
+int launch_wide_act(const DenseArgs& g, hipStream_t stream) {
+    if (g.act == MOE_ACT_SILU) return launch_wide<OP_KC, LB, EPI, MOE_ACT_SILU>(g, 1, stream);
+    return launch_wide<OP_KC, LB, EPI>(g, 1, stream);
 }
 template <int EPI>
 int launch_sum(const DenseArgs& g, int splits, hipStream_t stream) {
@@ -816,7 +1107,9 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
     const Shape s = dense_shape(g.M, g.N, g.K, la, lb, epi);
     if (epi == EPI_GATE8) epi = EPI_GATE;
     if (epi == EPI_DGATE && g.save == MOE_SAVE_INT8) epi = EPI_DGATE8;
-    if (epi == EPI_LINEAR && g.vec && !g.out_f32 && !g.pre && g.act == MOE_ACT_NONE) epi = EPI_PLAIN;
+    if (epi == EPI_LINEAR && g.vec && !g.out_f32 && !g.pre && g.act == MOE_ACT_NONE && g.N % 8 == 0 && g.ldo % 8 == 0 &&
+        (!g.res || g.ldr % 8 == 0))
+        epi = EPI_PLAIN;
     MOE_REQUIRE(s.mt * s.nt * s.splits < (1ll << 31), MOE_ERR_SHAPE, "product of %d x %d has too many tiles", g.M, g.N);
     g.mt = (int)s.mt;
     g.nt = (int)s.nt;
@@ -846,9 +1139,9 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         return launch_small<EPI_PLAIN>(g, la, lb, 1, stream);
     }
     if (s.kind == WIDE) {
-        if (epi == EPI_GATE) return launch_wide<OP_KC, OP_KC, EPI_GATE>(g, 1, stream);
-        if (epi == EPI_DGATE) return launch_wide<OP_KC, OP_KS, EPI_DGATE>(g, 1, stream);
-        if (epi == EPI_DGATE8) return launch_wide<OP_KC, OP_KS, EPI_DGATE8>(g, 1, stream);
+        if (epi == EPI_GATE) return launch_wide_act<OP_KC, EPI_GATE>(g, stream);
+        if (epi == EPI_DGATE) return launch_wide_act<OP_KS, EPI_DGATE>(g, stream);
+        if (epi == EPI_DGATE8) return launch_wide_act<OP_KS, EPI_DGATE8>(g, stream);
         if (epi == EPI_LINEAR) return launch_wide<OP_KC, OP_KC, EPI_LINEAR>(g, 1, stream);
         // (data and weight gradients are always EPI_PLAIN)
         return launch_wide_any<EPI_PLAIN>(g, la, lb, 1, stream);

@@ -18,7 +18,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int DBK = 64;  // K step: 128 bytes of a KC row, 64 rows of a KS matrix
 
-// EPI_PLAIN: EPI_LINEAR's common form (bf16 out = C + bias + residual, vec);
+// EPI_PLAIN: EPI_LINEAR's common form (bf16 out = C + bias + residual; N and the
+// strides multiples of 8);
 // EPI_DGATE8: EPI_DGATE from the 8-bit [G, U]; EPI_GATE8: EPI_GATE with the 8-bit
 // save, which needs whole 128-column blocks (the kernels read `save`: EPI_GATE)
 enum { EPI_LINEAR = 0, EPI_PART = 1, EPI_GATE = 2, EPI_DGATE = 3, EPI_PLAIN = 4, EPI_DGATE8 = 5, EPI_GATE8 = 6 };

@@ -325,10 +325,22 @@ def test_linear_wide(on_gpu, T, K, N):
     check_linear(T, K, N, "none", True, False, False, True)
 
 
+@pytest.mark.parametrize("T, K, N", [(8192, 7168, 256), (1500, 7168, 3000)])
+def test_linear_wide_pieces(on_gpu, T, K, N):
+    """256 x 256 tiles with K in pieces, forward and weight gradient."""
+    check_linear(T, K, N, "none", True, True, False, True)
+
+
+@pytest.mark.parametrize("save", ["bf16", "int8"])
+def test_ffn_wide_pieces(on_gpu, save):
+    check_ffn(1100, 7168, 2048, "silu", save, True, True)
+
+
 @pytest.mark.parametrize("T, d, f, save", [(3300, 72, 2104, "bf16"), (3300, 200, 4200, "bf16"), (3300, 136, 2176, "int8"),
                                            (3300, 64, 4224, "int8"), (6000, 1000, 1032, "none")])
 def test_ffn_wide(on_gpu, T, d, f, save):
     check_ffn(T, d, f, "silu", save, save == "bf16", True)
+    check_ffn(T, d, f, "gelu", save, False, False)
 
 
 # ---------------------------------------------------------------- 8-bit activations
