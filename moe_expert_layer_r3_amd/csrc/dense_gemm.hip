@@ -349,21 +349,25 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
         wait_vmcnt<(RING - 2) * 4>();  // this step has landed; the next three are in flight
         wait_lgkm0();
         phase_barrier();  // for every wave, which has also read the previous step
-        issue(slot == 0 ? RING - 1 : slot - 1, ks + RING - 1);
         uint32_t base = sbase + slot * STAGE;
         pin(base);
+        u32x4 fa[2][2], fb[2][2];
         static_for<0, 2>([&](auto sc) {
-            u32x4 fa[2], fb[2];
+            constexpr int s = decltype(sc)::value;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                fa[i] = frag(std::integral_constant<int, LA>{}, base + ra[i], sc);
-                fb[i] = frag(std::integral_constant<int, LB>{}, base + rb[i], sc);
+                fa[i][s] = frag(std::integral_constant<int, LA>{}, base + ra[i], sc);
+                fb[i][s] = frag(std::integral_constant<int, LB>{}, base + rb[i], sc);
             }
+        });
+        // the DMA goes out while the fragments are on their way
+        issue(slot == 0 ? RING - 1 : slot - 1, ks + RING - 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
-        });
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(fb[j][s], fa[i][s], acc[i][j]);
         slot = slot == RING - 1 ? 0 : slot + 1;
     }
     wait_lgkm0();
