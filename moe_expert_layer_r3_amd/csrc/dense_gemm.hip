@@ -413,6 +413,10 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
 // each holds 8 adjacent columns.  The general
 // epilogues, too long to be written out for every register, go through LDS.
 //
+// HM = 1: 128 x 256 tiles, for products with too few 256 x 256 ones.  A K step is
+// then one phase (16 fragments read, 32 MFMAs, 6 DMA instructions) and LDS holds
+// three stages of 48 KB, so the DMA still runs two steps ahead.
+//
 // act: the activation of the gated epilogues at compile time (-1: at run time).
 constexpr bool is_direct(int epi, int act) {
     return epi == EPI_PLAIN || epi == EPI_PART || ((epi == EPI_GATE || is_dgate(epi)) && act >= 0);
@@ -436,18 +440,18 @@ __device__ __forceinline__ void unpack_bf16x8(const u32x4& w, v4f& a, v4f& b) {
     b = v4f{bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
 }
 
-template <int LA, int LB, int EPI, int ACT>
+template <int HM, int LA, int LB, int EPI, int ACT>
 __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int tiles) {
-    constexpr int HALF = 16384, STAGE = 4 * HALF;
+    constexpr int HALF = 16384, STAGE = (HM + 2) * HALF, BOFF = HM * HALF, STAGES = HM == 2 ? 2 : 3;
     constexpr bool GATE = EPI == EPI_GATE, DIRECT = is_direct(EPI, ACT);
     static_assert(!GATE || LB == OP_KC, "gated tiles pair 128 G with 128 U rows of W13");
     // A wave's 32 columns of half b of B begin at wn WSTEP + b HSTEP: 64 adjacent
     // columns for KC operands, whose rows may be dealt at will; a KS operand's 128
     // columns of a half stay adjacent (64-byte pieces of its rows cost 5%)
     constexpr int WSTEP = LB == OP_KC && !GATE ? 64 : 32, HSTEP = LB == OP_KC && !GATE ? 32 : 128;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
     // EPI_GATE with the 8-bit save: row maxima [wave column][G, U][row]
-    __shared__ uint32_t rowmax[GATE && DIRECT ? 4 : 1][2][256];
+    __shared__ uint32_t rowmax[GATE && DIRECT ? 4 : 1][2][HM * 128];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -462,20 +466,20 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
     int n0 = 0, split = 0, ks0 = 0, ks1 = 0, kend = 0;
     // DMA: wave w moves segments 2w, 2w + 1 of every half: KC rows 16w .. + 15 (one
     // K chunk per lane), KS K rows 8w .. + 7
-    uint32_t va[2][2], vb[2][2];
-    const uint8_t *pa[2], *pb[2];
+    uint32_t va[HM][2], vb[2][2];
+    const uint8_t *pa[HM], *pb[2];
     const KcLane la(lane, g.lda), lb(lane, g.ldb);
     const uint32_t kseg = wave * 8 + (lane >> 4);  // KS: K row of segment 0, + 4 of segment 1
     auto setup = [&](int t) {
         int mt, nt;
         dense_tile(g, t, tiles, mt, nt, split);
-        m0 = (int64_t)mt * 256;
+        m0 = (int64_t)mt * (HM * 128);
         n0 = nt * (GATE ? 128 : 256);
         ks0 = split * g.ksteps;
         ks1 = min(ks0 + g.ksteps, (g.K + DBK - 1) / DBK);
         kend = min(g.K, ks1 * DBK);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < HM; ++h) {
             if constexpr (LA == OP_KC) {
                 const int64_t r0 = m0 + h * 128 + wave * 16;
                 pa[h] = (const uint8_t*)(g.a + r0 * g.lda);
@@ -491,6 +495,9 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                     va[h][i] = c0 + c * 8 < g.a_cols ? k * (uint32_t)(g.lda * 2) + c * 16 : OOB;
                 }
             }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             // (EPI_GATE: half 0 is G, half 1 U)
             if constexpr (LB == OP_KC) {
                 const int64_t r0 = GATE ? (int64_t)h * g.f + n0 + wave * 16
@@ -522,7 +529,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
     auto issue_b = [&](int st, int h, int ks) {
         const int left = kend - ks * DBK;
         const u32x4 d = buf_desc(pb[h] + ks * step_b);
-        const uint32_t s = sbase + st * STAGE + (2 + h) * HALF + wave * 2048;
+        const uint32_t s = sbase + st * STAGE + BOFF + h * HALF + wave * 2048;
         const int k0 = LB == OP_KC ? (int)lb.k : (int)kseg, k1 = LB == OP_KC ? (int)lb.k : (int)kseg + 4;
         dma16b2(d, k0 < left ? vb[h][0] : OOB, k1 < left ? vb[h][1] : OOB, s);
     };
@@ -539,13 +546,13 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         for (int i = 0; i < 4; ++i) ra[i] = ks_frag(lane, wm * 4 + i);
     }
     if constexpr (LB == OP_KC) {
-        rb[0] = 2 * HALF + kc_frag(lane, wn * 32);
+        rb[0] = BOFF + kc_frag(lane, wn * 32);
         rb[1] = rb[0] ^ 64;
     } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) rb[j] = 2 * HALF + ks_frag(lane, wn * 2 + j);
+        for (int j = 0; j < 2; ++j) rb[j] = BOFF + ks_frag(lane, wn * 2 + j);
     }
-    // [subtile][K half]; B: half 0 of even and odd steps, half 1
+    // [subtile][K half]; B: half 0 of even and odd steps (HM = 1: of the step), half 1
     u32x4 fa[4][2], fb[3][2][2];
     auto read_a = [&](auto off_c, uint32_t base) {
         constexpr int OFF = decltype(off_c)::value;
@@ -580,7 +587,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         });
     };
 
-    v4f acc[2][2][4][2];
+    v4f acc[HM][2][4][2];
     auto multiply = [&](auto ac, auto st_c) {
         constexpr int a = decltype(ac)::value, st = decltype(st_c)::value;
         wait_lgkm0();
@@ -603,7 +610,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
     constexpr std::integral_constant<int, 2> c2;
     constexpr std::integral_constant<int, HALF> half1;
     // `wait`: not in a tile's first step, whose operands have landed before it begins
-    auto kstep = [&](auto st_c, int ks, bool wait) {
+    [[maybe_unused]] auto kstep = [&](auto st_c, int ks, bool wait) {
         constexpr int st = decltype(st_c)::value;
         constexpr std::integral_constant<int, st ^ 1> other;
         uint32_t base = sbase + st * STAGE, next = sbase + (st ^ 1) * STAGE;
@@ -611,7 +618,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         read_a(c0, base);
         read_b(half1, c2, base);
         issue_b(st, 0, ks + 2);
-        issue_a(st ^ 1, 1, ks + 1);
+        issue_a(st ^ 1, HM - 1, ks + 1);
         if (wait) wait_vmcnt<8>();  // A1 of this step, B0 of the next
         multiply(c0, st_c);
         pin(base);
@@ -621,7 +628,21 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         issue_a(st, 0, ks + 2);
         issue_b(st, 1, ks + 2);
         if (wait) wait_vmcnt<8>();  // A0, B1 of the next step
-        multiply(c1, st_c);
+        multiply(std::integral_constant<int, HM - 1>{}, st_c);
+    };
+    // HM = 1: step ks from stage st, refilling the stage of the step before
+    auto kstep1 = [&](int st, int ks, bool wait) {
+        uint32_t base = sbase + st * STAGE;
+        pin(base);
+        read_a(c0, base);
+        read_b(c0, c0, base);
+        read_b(half1, c2, base);
+        const int refill = st == 0 ? 2 : st - 1;
+        issue_a(refill, 0, ks + 2);
+        issue_b(refill, 0, ks + 2);
+        issue_b(refill, 1, ks + 2);
+        if (wait) wait_vmcnt<6>();  // the next step
+        multiply(c0, c0);
     };
 
     // ---- results straight from the accumulators.  Every store comes after
@@ -632,7 +653,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         auto row = [&](int u) { return m0 + (u >> 2) * 128 + wm * 64 + (u & 3) * 16 + l15; };  // u: 4 a + i
         if constexpr (EPI == EPI_PART) {
             wait_vmcnt<0>();
-            static_for<0, 8>([&](auto uc) {
+            static_for<0, HM * 4>([&](auto uc) {
                 constexpr int u = decltype(uc)::value;
                 const int64_t m = row(u);
                 float* p = g.part + ((int64_t)split * g.M + m) * g.part_ld;
@@ -645,11 +666,11 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                     }
             });
         } else if constexpr (EPI == EPI_PLAIN) {
-            u32x4 r[8][2];
+            u32x4 r[HM * 4][2];
             const int n = n0 + wn * WSTEP + coff;
             const bool on[2] = {n < g.N, n + HSTEP < g.N};
             if (g.res) {
-                static_for<0, 8>([&](auto uc) {
+                static_for<0, HM * 4>([&](auto uc) {
                     constexpr int u = decltype(uc)::value;
                     const int64_t m = min(row(u), (int64_t)g.M - 1);
                     const uint16_t* p = g.res + m * g.ldr;
@@ -658,7 +679,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                 });
             }
             wait_vmcnt<0>();
-            static_for<0, 8>([&](auto uc) {
+            static_for<0, HM * 4>([&](auto uc) {
                 constexpr int u = decltype(uc)::value;
                 const int64_t m = row(u);
                 uint16_t* p = (uint16_t*)g.out + m * g.ldo;
@@ -687,7 +708,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                 EpiBias<EPI_GATE> bias[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) bias[j].load(g, nj + j * 16);
-                static_for<0, 8>([&](auto uc) {
+                static_for<0, HM * 4>([&](auto uc) {
                     constexpr int u = decltype(uc)::value;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -697,7 +718,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                 });
             }
             if (g.save == MOE_SAVE_INT8) {
-                static_for<0, 8>([&](auto uc) {
+                static_for<0, HM * 4>([&](auto uc) {
                     constexpr int u = decltype(uc)::value;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
@@ -716,7 +737,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
             }
             wait_vmcnt<0>();
             const bool on = n < g.f;
-            static_for<0, 8>([&](auto uc) {
+            static_for<0, HM * 4>([&](auto uc) {
                 constexpr int u = decltype(uc)::value;
                 const int64_t m = row(u);
                 const bool mine = on && m < g.M;
@@ -794,7 +815,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
             };
             static_for<0, 4>([&](auto uc) { load(uc); });
             wait_vmcnt<0>();
-            static_for<0, 8>([&](auto uc) {
+            static_for<0, HM * 4>([&](auto uc) {
                 constexpr int u = decltype(uc)::value, at = u & 3;
                 const int64_t m = row(u);
                 uint16_t* p = g.dgu + m * (2 * (int64_t)g.f) + n;
@@ -832,14 +853,14 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
                             *reinterpret_cast<u32x4*>(g.h + m * (int64_t)g.f + n + b * HSTEP) = pack_bf16x8(h[0], h[1]);
                     }
                 }
-                if constexpr (u < 4) load(std::integral_constant<int, u + 4>{});
+                if constexpr (u + 4 < HM * 4) load(std::integral_constant<int, u + 4>{});
             });
         }
     };
     // ---- or through LDS, a 128-row half at a time
     auto leave_staged = [&](int64_t m0, int n0, int split) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
+        for (int a = 0; a < HM; ++a) {
             TileEpilogue<EPI, 128, 256, 512> epi;
             epi.load(g, m0 + a * 128, n0);
             if (a) __syncthreads();
@@ -872,7 +893,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
             issue_a(0, 0, ks0);
             issue_b(0, 1, ks0);
             issue_b(1, 0, ks0 + 1);
-            issue_a(0, 1, ks0);
+            if constexpr (HM == 2) issue_a(0, 1, ks0);
             issue_a(1, 0, ks0 + 1);
             issue_b(1, 1, ks0 + 1);
         }
@@ -882,7 +903,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
         if (!more) break;
         if (!DIRECT || !have) wait_vmcnt<0>();
         phase_barrier();
-        {
+        if constexpr (HM == 2) {
             uint32_t base = sbase;
             pin(base);
             read_b(c0, c0, base);
@@ -890,7 +911,7 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
             phase_barrier();
         }
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < HM; ++a)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -898,9 +919,17 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
 #pragma unroll
                     for (int j = 0; j < 2; ++j) acc[a][b][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
         if (wm == 1) phase_barrier();  // the second wave of each SIMD runs half a phase behind
-        for (int ks = ks0; ks < ks1; ks += 2) {
-            kstep(c0, ks, ks > ks0);
-            if (ks + 1 < ks1) kstep(c1, ks + 1, true);
+        if constexpr (HM == 2) {
+            for (int ks = ks0; ks < ks1; ks += 2) {
+                kstep(c0, ks, ks > ks0);
+                if (ks + 1 < ks1) kstep(c1, ks + 1, true);
+            }
+        } else {
+            int st = 0;
+            for (int ks = ks0; ks < ks1; ++ks) {
+                kstep1(st, ks, ks > ks0);
+                st = st == 2 ? 0 : st + 1;
+            }
         }
         if (wm == 0) phase_barrier();
         // every wave has read the last step, and this wave's fills past the end (into
@@ -962,7 +991,7 @@ __global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits)
 
 // ---------------------------------------------------------------- host side
 namespace {
-enum Kind { THIN, SLAB, SMALL, TILES, WIDE };
+enum Kind { THIN, SLAB, SMALL, TILES, HALF, WIDE };
 struct Shape {
     Kind kind;
     int64_t mt, nt;
@@ -978,28 +1007,37 @@ void set_splits(Shape& s, int64_t K, int64_t sp, int64_t least) {
     s.ksteps = (int)((steps + sp - 1) / sp);
     s.splits = (int)((steps + s.ksteps - 1) / s.ksteps);
 }
-// The kernel for an M x N product over K, by the number of tiles it would have:
-//   THIN   up to 4 rows, one launch
-//   SLAB   up to 128 rows, K in pieces
-//   WIDE   256 x 256 tiles, where they fill three quarters of the compute units, or
-//          where K split in as many pieces as fill them pays for the pieces' extra
-//          traffic (about 130 MB, 15 us): from 2e10 multiplications on (2048 x 4096
-//          over 7168: 105 us, 118 on 128 x 128 tiles; 16384 x 256 over 7168: 77 and
-//          95 us), or where an operand is far larger than the caches, since these
-//          tiles read it half as often (8192 x 256 over 7168: 51 and 57 us)
-//   SMALL  64 x 64 tiles for short sums (1237 x 1032 over 688: 10.0 us, 15.6 on
-//          128 x 128 tiles); they read the operands twice as often, which long sums
-//          of many tiles pay for (1000 x 600 over 12000: 44 us, 35 on 128 x 128)
-//   TILES  128 x 128 tiles, K split where they are fewer than the compute units
-//          (2048 x 2048 over 2048 has exactly as many: 28 us, 31 split in two)
+// The kernel for an M x N product over K.  THIN (up to 4 rows) and SLAB (up to 128
+// rows, K in pieces) go by the rows.  Of the tiled ones, each with K whole or in as
+// many pieces as fill the compute units, the one with the least estimated time is
+// taken:
+//     rounds of tiles x K steps x time of a step + fixed
+//         + the pieces' second launch (4 us) and traffic (8 bytes per result, 10 TB/s)
+// with the steps' times measured on operands of 16 to 120 MB:
+//   WIDE   256 x 256 tiles   1.45 us a step   2048 x 7168 over 4096: 96 us (HALF 123)
+//   HALF   128 x 256         0.87             1024 x 7168 over 2048: 32 us (TILES 40)
+//   TILES  128 x 128         1.05 (two of them on a compute unit; 0.75 alone)
+//                                             12000 x 600 over 1200: 29 us (HALF 39)
+//   SMALL  64 x 64           0.38 (two; 0.22 alone)
+//                                             256 x 4096 over 7168: 29 us (TILES 31)
+// The estimates are within 15% of the times over 50 shapes, and the choice within
+// 10% of the best kernel's.
+struct Tiling {
+    Kind kind;
+    int bm, bn, per_cu;      // tile, workgroups that share a compute unit
+    double alone, shared, fixed;  // us per step (one, per_cu of them on a unit), us
+    int least;               // K steps of a piece at least
+};
+constexpr Tiling TILINGS[] = {{WIDE, 256, 256, 1, 1.45, 1.45, 10., 8},
+                              {HALF, 128, 256, 1, 0.87, 0.87, 7., 8},
+                              {TILES, 128, 128, 2, 0.75, 1.05, 6., 8},
+                              {SMALL, 64, 64, 2, 0.22, 0.38, 5., 8}};
 Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
     Shape s;
     const bool gate = epi == EPI_GATE || epi == EPI_GATE8;
-    const int64_t cols = gate ? N / 2 : N;
     const int64_t cus = num_cus();
-    const int64_t steps = (K + DBK - 1) / DBK;
     s.splits = 1;
-    s.ksteps = (int)steps;
+    s.ksteps = (int)((K + DBK - 1) / DBK);
     s.mt = 1;
     s.pieces = false;
     if (la == OP_KC && lb == OP_KC && M <= SLAB_ROWS) {
@@ -1009,41 +1047,40 @@ Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
         s.pieces = s.kind == SLAB;
         return s;
     }
-    const int64_t wide_m = (M + 255) / 256, wide_n = gate ? (cols + 127) / 128 : (N + 255) / 256;
-    if (wide_m * wide_n * 4 >= cus * 3) {
-        s.kind = WIDE;
-        s.mt = wide_m;
-        s.nt = wide_n;
-        return s;
+    Shape best = s;
+    double least = 1e30;
+    for (const Tiling& t : TILINGS) {
+        for (int64_t share = 0; share <= t.per_cu; ++share) {  // 0: K whole
+            Shape c = s;
+            c.kind = t.kind;
+            // gated tiles hold half as many h columns (on TILES: 64 x 256 tiles of B rows)
+            const bool paired = gate && share == 0;
+            int64_t bm = t.bm, bn = paired ? t.bn / 2 : t.bn;
+            if (paired && t.kind == TILES) bm = 64, bn = 128;
+            c.mt = (M + bm - 1) / bm;
+            c.nt = ((paired ? N / 2 : N) + bn - 1) / bn;
+            const int64_t tiles = c.mt * c.nt;
+            if (share) {
+                set_splits(c, K, share * cus / tiles, t.least);
+                if (c.splits < 2) continue;
+                c.pieces = true;
+            }
+            // the 8-bit save takes whole 128-column blocks: in the sum of the pieces
+            if (epi == EPI_GATE8 && t.kind == SMALL && !share) {
+                c.nt = (N + 63) / 64;
+                c.pieces = true;
+            }
+            const int64_t n = tiles * c.splits;
+            const double rounds = (double)((n + t.per_cu * cus - 1) / (t.per_cu * cus));
+            double us = rounds * c.ksteps * (n <= cus ? t.alone : t.shared) + t.fixed;
+            if (c.pieces) us += 4. + (double)c.splits * M * N * 8 / 1e7;
+            if (us < least) {
+                least = us;
+                best = c;
+            }
+        }
     }
-    const int64_t plain = wide_m * ((N + 255) / 256), sp = cus / plain;  // pieces use plain tiles
-    if (sp >= 2 && steps / sp >= 8 &&
-        ((double)M * N * K >= 2e10 || (sp <= 8 && (M > N ? M : N) * K * 2 >= (64 << 20)))) {
-        s.kind = WIDE;
-        s.mt = wide_m;
-        s.nt = (N + 255) / 256;
-        set_splits(s, K, sp, 8);
-        s.pieces = true;
-        return s;
-    }
-    const int64_t small = (M + 63) / 64 * ((N + 63) / 64);
-    if (small <= cus / 2 || (small <= cus && K <= 4096) || (small <= 4 * cus && K <= 1024)) {
-        s.kind = SMALL;
-        s.mt = (M + 63) / 64;
-        s.nt = (N + 63) / 64;  // (32 columns each of G and U for EPI_GATE)
-        set_splits(s, K, 2 * cus / small, 16);
-        // the 8-bit save takes whole blocks, in the sum of the pieces
-        s.pieces = s.splits > 1 || epi == EPI_GATE8;
-        return s;
-    }
-    s.kind = TILES;
-    const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
-    if (tiles < cus) set_splits(s, K, 2 * cus / tiles, 8);
-    s.pieces = s.splits > 1;
-    const int64_t bm = gate && !s.pieces ? 64 : 128;
-    s.mt = (M + bm - 1) / bm;
-    s.nt = ((s.pieces ? N : cols) + 127) / 128;
-    return s;
+    return best;
 }
 template <int WM, int WN, int LA, int LB, int EPI>
 int launch_one(const DenseArgs& g, int splits, hipStream_t stream) {
@@ -1064,25 +1101,25 @@ int launch_small(const DenseArgs& g, int la, int lb, int splits, hipStream_t str
     if (la == OP_KC) return launch_small_one<OP_KC, OP_KS, EPI>(g, splits, stream);
     return launch_small_one<OP_KS, OP_KS, EPI>(g, splits, stream);
 }
-template <int LA, int LB, int EPI, int ACT = -1>
+template <int LA, int LB, int EPI, int ACT = -1, int HM = 2>
 int launch_wide(const DenseArgs& g, int splits, hipStream_t stream) {
     const int tiles = g.mt * g.nt * splits, cus = num_cus() & ~7;
     const int grid = tiles < cus ? tiles : cus;
-    dense_wide_kernel<LA, LB, EPI, ACT><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(g, tiles);
+    dense_wide_kernel<HM, LA, LB, EPI, ACT><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(g, tiles);
     MOE_LAUNCH_CHECK("dense_wide_kernel");
     return MOE_OK;
 }
-template <int EPI>
+template <int EPI, int HM = 2>
 int launch_wide_any(const DenseArgs& g, int la, int lb, int splits, hipStream_t stream) {
-    if (la == OP_KC && lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI>(g, splits, stream);
-    if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI>(g, splits, stream);
-    return launch_wide<OP_KS, OP_KS, EPI>(g, splits, stream);
+    if (la == OP_KC && lb == OP_KC) return launch_wide<OP_KC, OP_KC, EPI, -1, HM>(g, splits, stream);
+    if (la == OP_KC) return launch_wide<OP_KC, OP_KS, EPI, -1, HM>(g, splits, stream);
+    return launch_wide<OP_KS, OP_KS, EPI, -1, HM>(g, splits, stream);
 }
 // the gated epilogues: silu, the usual activation, is compiled in
-template <int LB, int EPI>
+template <int LB, int EPI, int HM = 2>
 int launch_wide_act(const DenseArgs& g, hipStream_t stream) {
-    if (g.act == MOE_ACT_SILU) return launch_wide<OP_KC, LB, EPI, MOE_ACT_SILU>(g, 1, stream);
-    return launch_wide<OP_KC, LB, EPI>(g, 1, stream);
+    if (g.act == MOE_ACT_SILU) return launch_wide<OP_KC, LB, EPI, MOE_ACT_SILU, HM>(g, 1, stream);
+    return launch_wide<OP_KC, LB, EPI, -1, HM>(g, 1, stream);
 }
 template <int EPI>
 int launch_sum(const DenseArgs& g, int splits, hipStream_t stream) {
@@ -1126,6 +1163,7 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         g.part_ld = round_up(g.N, 4);
         const int rc = s.kind == SLAB    ? dense_slab_launch(g, s.splits, stream)
                        : s.kind == SMALL ? launch_small<EPI_PART>(g, la, lb, s.splits, stream)
+                       : s.kind == HALF  ? launch_wide_any<EPI_PART, 1>(g, la, lb, s.splits, stream)
                        : s.kind == WIDE  ? launch_wide_any<EPI_PART>(g, la, lb, s.splits, stream)
                                          : launch_layout<EPI_PART>(g, la, lb, s.splits, stream);
         if (rc != MOE_OK) return rc;
@@ -1141,6 +1179,13 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
         if (epi == EPI_DGATE8) return launch_small_one<OP_KC, OP_KS, EPI_DGATE8>(g, 1, stream);
         if (epi == EPI_LINEAR) return launch_small_one<OP_KC, OP_KC, EPI_LINEAR>(g, 1, stream);
         return launch_small<EPI_PLAIN>(g, la, lb, 1, stream);
+    }
+    if (s.kind == HALF) {
+        if (epi == EPI_GATE) return launch_wide_act<OP_KC, EPI_GATE, 1>(g, stream);
+        if (epi == EPI_DGATE) return launch_wide_act<OP_KS, EPI_DGATE, 1>(g, stream);
+        if (epi == EPI_DGATE8) return launch_wide_act<OP_KS, EPI_DGATE8, 1>(g, stream);
+        if (epi == EPI_LINEAR) return launch_wide<OP_KC, OP_KC, EPI_LINEAR, -1, 1>(g, 1, stream);
+        return launch_wide_any<EPI_PLAIN, 1>(g, la, lb, 1, stream);
     }
     if (s.kind == WIDE) {
         if (epi == EPI_GATE) return launch_wide_act<OP_KC, EPI_GATE>(g, stream);
