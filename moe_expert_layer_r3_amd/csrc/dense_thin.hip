@@ -23,11 +23,10 @@ __device__ __forceinline__ void finish(const DenseArgs& g, int m, int n, v4f v) 
 // waves' fp32 sums are added in order through LDS and the epilogue runs on them.
 // An MFMA takes 16 rows of W.  With R = 4 they are 4 rows x 4 chunks of K, and
 // likewise the 16 rows of x: of the products only those of equal chunks count.  A W
-// of few rows is then spread over 4 times as many compute units (one CU alone
-// streams about 20 GB/s): 256 rows of 7168 take 4.2 us, 10.7 us
-// with R = 16.  Where
-// R = 16 fills the chip its fewer workgroups are ahead (7168 rows of 2048: 7.7 against
-// 15.7 us).
+// of few rows is then spread over 4 times as many compute units (one alone streams
+// about 20 GB/s): 256 rows of 7168 take 4.2 us, 10.7 us with R = 16.  Where R = 16
+// fills the chip its fewer workgroups are ahead (7168 rows of 2048: 7.7 us, 3.8 TB/s,
+// against 15.7 us; 4096 rows of 7168: 11.8 us, 5.0 TB/s).
 template <int R, int NW, int EPI>
 __global__ __launch_bounds__(NW * 64) void dense_thin_kernel(DenseArgs g) {
     static_assert(R == 4 || R == 16, "rows of W per workgroup");
@@ -125,8 +124,9 @@ __global__ __launch_bounds__(NW * 64) void dense_thin_kernel(DenseArgs g) {
 // then every wave streams its W rows into MFMA operands without synchronisation.  The
 // fp32 sums of the K ranges go to the workspace (EPI_PART) and dense_sum_kernel
 // adds them in order.  Against the kernel above, x passes through the texture path
-// once per 128 W rows instead of once per 16: from 17 rows on its re-reads cost
-// more than the second launch.
+// once per 128 W rows instead of once per 16, whose re-reads cost more than the
+// second launch from 5 rows on (48 rows of x, 4096 rows of 7168: 16.4 us and 34.8 us;
+// 16 rows of x: 14.5 and 16.0 us).
 template <int MT>
 __global__ __launch_bounds__(512) void dense_slab_kernel(DenseArgs g) {
     constexpr int U = 4;  // K steps of 64 in flight per wave (two loads each)
@@ -170,7 +170,9 @@ __global__ __launch_bounds__(512) void dense_slab_kernel(DenseArgs g) {
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) load(u, min(u, n - 1));
-        // loads complete in order: the 2 U younger ones may stay in flight
+        // loads complete in order: the 2 U younger ones may stay in flight (none of them
+        // may be scheduled behind the wait)
+        __builtin_amdgcn_sched_barrier(0);
         wait_vmcnt<U * 2>();
         phase_barrier();
         uint32_t base = sbase;
@@ -202,6 +204,9 @@ __global__ __launch_bounds__(512) void dense_slab_kernel(DenseArgs g) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (s + u < n) mul(u, s + u);
+        // (also tells the compiler that the next slab's registers are free: it would
+        // wait for the x slab before the first W loads otherwise)
+        wait_vmcnt<0>();
         if (ks0 + SLAB_STEPS < end) {  // every wave has read the slab: the next one may overwrite it
             wait_lgkm0();
             phase_barrier();
