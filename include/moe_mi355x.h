@@ -4,7 +4,9 @@
  * One Mixture-of-Experts layer on one GPU's share of experts: top-k routing or
  * Router Replay of recorded expert ids, the expert-grouped token permutation,
  * block-scaled FP8 e4m3 quantisation, an MFMA FP8 grouped GEMM with a fused
- * SwiGLU epilogue, the weighted combine, and the training backward.
+ * SwiGLU epilogue, the weighted combine, and the training backward.  Around the
+ * routed experts: bf16 products with fused epilogues (the router's projection, a
+ * shared expert) with their gradients, and activations kept in 8 bits.
  *
  * Sources (cited by page and section):
  *   [R3]  "RL at 1T scale: a deep dive into prime-rl performance", section
@@ -36,7 +38,8 @@
  *     bounds on such input.
  *   - Calls are deterministic: the same inputs give bitwise-equal outputs.
  *
- * Supported shapes: hidden size d and expert FFN size f multiples of 128;
+ * Supported shapes (the dense products have rules of their own, below): hidden
+ * size d and expert FFN size f multiples of 128;
  * 1 <= top_k <= 16; 1 <= E <= 1024; local experts [e0, e0+L) inside [0, E).
  */
 #ifndef MOE_MI355X_H
