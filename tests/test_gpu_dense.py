@@ -343,6 +343,96 @@ def test_ffn_wide(on_gpu, T, d, f, save):
     check_ffn(T, d, f, "gelu", save, False, False)
 
 
+# ---------------------------------------------------------------- what must stay untouched, offsets past 32 bits
+
+class Guarded:
+    """Output buffers with 4096 poisoned elements in front and behind."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, shape, dtype=BF):
+        n = 1
+        for v in shape:
+            n *= v
+        n16 = (n + 7) // 8 * 8
+        b = torch.full((n16 + 8192,), 77, dtype=dtype, device=DEV)
+        self.bufs.append((b, n))
+        return b[4096:4096 + n]
+
+    def check(self):
+        for b, n in self.bufs:
+            assert (b[:4096] == 77).all() and (b[4096 + n:] == 77).all()
+
+
+@pytest.mark.parametrize("T, d, f", [(3, 72, 136), (37, 136, 128), (131, 200, 136), (700, 1032, 520), (3300, 72, 2184),
+                                     (3300, 2056, 4104)])
+@pytest.mark.parametrize("save", ["bf16", "int8"])
+def test_nothing_past_the_outputs(T, d, f, save):
+    if save == "int8":
+        f = f // 128 * 128
+    g = Guarded()
+    p = lambda t: t.data_ptr()
+    x, W13, W2, dy = normal((T, d), 1), normal((2 * f, d), 2, 0.1), normal((d, f), 3, 0.1), normal((T, d), 4)
+    h, y, dx, dW13, dW2, db13, db2 = g((T, f)), g((T, d)), g((T, d)), g((2 * f, d)), g((d, f)), g((2 * f,)), g((d,))
+    gu = g((T, 2 * f), BF if save == "bf16" else torch.int8)
+    gs = g((2 * f // 128, T), torch.float32) if save == "int8" else None
+    nb = max(ops.workspace_bytes("moe_gated_ffn_workspace", T, d, f),
+             ops.workspace_bytes("moe_gated_ffn_backward_workspace", T, d, f))
+    ws = g((nb,), torch.uint8)
+    gp = None if gs is None else p(gs)
+    ops.launch("moe_gated_ffn", x.device, p(x), d, p(W13), None, p(W2), None, p(dy), T, d, f, 2, p(h), p(y),
+               ops.SAVES[save], p(gu), gp, p(ws), nb)
+    ops.launch("moe_gated_ffn_backward", x.device, p(dy), p(x), d, p(W13), p(W2), ops.SAVES[save], p(gu), gp, None, T, d, f,
+               2, p(dx), p(dW13), p(dW2), p(db13), p(db2), p(ws), nb)
+    # a linear layer with an odd number of columns on the same inputs
+    N = 2 * f - 3
+    out, pre, lx, lW, lb = g((T, N)), g((T, N)), g((T, d)), g((N, d)), g((N,))
+    nl = max(ops.workspace_bytes("moe_linear_workspace", T, N, d), ops.workspace_bytes("moe_linear_backward_workspace", T, N, d))
+    wl = g((nl,), torch.uint8)
+    ops.launch("moe_linear", x.device, p(x), d, p(W13), d, None, None, N, T, N, d, 3, p(out), 0, N, p(pre), p(wl), nl)
+    ops.launch("moe_linear_backward", x.device, p(out), 0, p(pre), p(x), d, p(W13), d, None, T, N, d, 3, p(lx), p(lW), p(lb),
+               p(wl), nl)
+    torch.cuda.synchronize()
+    g.check()
+
+
+def test_offsets_past_32_bits():
+    """x of 2.2e9 elements and an output of 2.2e9: rows at the far end against
+    the same rows alone, and the weight gradient against the sum of two halves."""
+    T, K, N = 307_203, 7168, 8
+    x = torch.randn((T, K), device=DEV, dtype=BF)
+    W, dy = normal((N, K), 2, 0.02), normal((T, N), 3)
+    p = LinearPlan(T, K, N, train=True, device=DEV)
+    out = p.forward(x, W)
+    X, Wd = x[-200:].double(), W.double()
+    ref = X @ Wd.t()
+    e = acc_err(K, X, Wd.t())
+    assert ((out[-200:].double() - ref).abs() <= e + U16 * (ref.abs() + e)).all()
+    dx, dW, _ = p.backward(dy, x, W)
+    D = dy[-200:].double()
+    ref = D @ Wd
+    e = acc_err(N, D, Wd)
+    assert ((dx[-200:].double() - ref).abs() <= e + U16 * (ref.abs() + e) + 1e-30).all()
+    ref = sum(dy[a:a + 50_000].double().t() @ x[a:a + 50_000].double() for a in range(0, T, 50_000))
+    mag = sum(dy[a:a + 50_000].double().abs().t() @ x[a:a + 50_000].double().abs() for a in range(0, T, 50_000))
+    e = (T + 8) * 2.0 ** -24 * mag
+    assert ((dW.double() - ref).abs() <= e + U16 * (ref.abs() + e)).all()
+    del p, out, dx
+    q, s = ops.act_save(x)
+    back = ops.act_restore(q, s)
+    q1, s1 = ops.act_save(x[-200:])
+    assert torch.equal(q[-200:], q1) and torch.equal(s[:, -200:], s1)
+    assert torch.equal(back[-200:], ops.act_restore(q1, s1))
+    del x, q, s, back
+    x, W = normal((T, 16), 4), normal((K, 16), 5)   # an output of 2.2e9 elements
+    out = LinearPlan(T, 16, K, device=DEV).forward(x, W)
+    X, Wd = x[-200:].double(), W.double()
+    ref = X @ Wd.t()
+    e = acc_err(16, X, Wd.t())
+    assert ((out[-200:].double() - ref).abs() <= e + U16 * (ref.abs() + e) + 1e-30).all()
+
+
 # ---------------------------------------------------------------- 8-bit activations
 
 @pytest.mark.parametrize("rows, cols, pad", [(1, 8, 0), (3, 128, 0), (5, 136, 24), (130, 1000, 0), (257, 384, 8),
