@@ -449,13 +449,14 @@ enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_INT8 = 2 };
  * MOE_ERR_SHAPE for sizes, strides and alignment, MOE_ERR_UNSUPPORTED for
  * unknown enum values, MOE_ERR_WORKSPACE for a workspace smaller than the
  * *_workspace function says (which depends on the sizes and the current
- * device's compute units).  Calls that share a workspace must not overlap.    */
+ * device's compute units).  Calls that share a workspace must not overlap.
+ * Outputs overlap no input, workspace or other output, but where it is said.  */
 
 /* out[t, n] = act(sum_k x[t, k] W[n, k] + bias[n]) + residual[t, n]
  *   x [T, K] bf16 (stride ldx), W [N, K] bf16 (ldw), bias [N] bf16 or NULL,
  *   residual [T, N] bf16 (ldr) or NULL, out [T, N] (ldo) bf16 (out_type
  *   MOE_SRC_BF16) or fp32 (MOE_SRC_F32). out may be the residual's memory
- *   (bf16, ldo == ldr); it overlaps no other input.
+ *   (bf16, ldo == ldr).
  *   pre: NULL, or [T, N] bf16 dense: the argument of act, rounded, which
  *   moe_linear_backward takes where act is not MOE_ACT_NONE.
  * T = 0 is a no-op.                                                           */

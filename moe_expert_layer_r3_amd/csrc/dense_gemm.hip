@@ -1071,6 +1071,8 @@ Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
                 c.pieces = true;
             }
             const int64_t n = tiles * c.splits;
+            // a launch takes less than 2^32 threads; HALF and WIDE are persistent
+            if (t.per_cu > 1 && n >= (1 << 23)) continue;
             const double rounds = (double)((n + t.per_cu * cus - 1) / (t.per_cu * cus));
             double us = rounds * c.ksteps * (n <= cus ? t.alone : t.shared) + t.fixed;
             if (c.pieces) us += 4. + (double)c.splits * M * N * 8 / 1e7;

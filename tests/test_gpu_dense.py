@@ -433,6 +433,43 @@ def test_offsets_past_32_bits():
     assert ((out[-200:].double() - ref).abs() <= e + U16 * (ref.abs() + e) + 1e-30).all()
 
 
+def test_most_rows():
+    """2^30 rows, the most there may be: blocks of rows repeat, and so do the results."""
+    T, R = 1 << 30, 1 << 20
+    b = normal((R, 8), 1)
+    x, W = b.repeat(T // R, 1), normal((8, 8), 2)
+    same = lambda t, ref: all(torch.equal(v, ref) for v in t.view(T // R, R, *t.shape[1:]))
+    p = LinearPlan(T, 8, 8, device=DEV)
+    out = p.forward(x, W)
+    assert torch.equal(out[:R], LinearPlan(R, 8, 8, device=DEV).forward(b, W)) and same(out, out[:R])
+    del p, out
+    p = GatedFFNPlan(T, 8, 8, device=DEV)
+    W13, W2 = normal((16, 8), 3), normal((8, 8), 4)
+    y = p.forward(x, W13, W2)
+    assert torch.equal(y[:R], GatedFFNPlan(R, 8, 8, device=DEV).forward(b, W13, W2)) and same(y, y[:R])
+    del p, y
+    q, s = ops.act_save(x)
+    q1, s1 = ops.act_save(b)
+    assert same(q, q1) and same(s[0], s1[0])
+    assert same(ops.act_restore(q, s), ops.act_restore(q1, s1))
+
+
+@pytest.mark.parametrize("T", [1, 3, 100, 700, 3300])
+def test_in_place(T):
+    """The addend's memory as the output's."""
+    d, f = 520, 264
+    x, W13, W2, W = normal((T, d), 1), normal((2 * f, d), 2, 0.1), normal((d, f), 3, 0.1), normal((d, d), 4, 0.1)
+    r, dy = normal((T, d), 5), normal((T, d), 6)
+    p, q = LinearPlan(T, d, d, train=True, device=DEV), GatedFFNPlan(T, d, f, save="bf16", device=DEV)
+    for plan, out, fwd, bwd in ((p, p.out, (x, W), (dy, x, W)), (q, q.y, (x, W13, W2), (dy, x, W13, W2))):
+        want = plan.forward(*fwd, residual=r).clone()
+        out.copy_(r)
+        assert torch.equal(plan.forward(*fwd, residual=out), want)
+        want = plan.backward(*bwd, dx_add=r)[0].clone()
+        plan.dx.copy_(r)
+        assert torch.equal(plan.backward(*bwd, dx_add=plan.dx)[0], want)
+
+
 # ---------------------------------------------------------------- 8-bit activations
 
 @pytest.mark.parametrize("rows, cols, pad", [(1, 8, 0), (3, 128, 0), (5, 136, 24), (130, 1000, 0), (257, 384, 8),
