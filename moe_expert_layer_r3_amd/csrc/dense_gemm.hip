@@ -22,6 +22,34 @@ __device__ __forceinline__ void dense_tile(const DenseArgs& g, int bid, int tile
     mt = __builtin_amdgcn_readfirstlane(grp * GM + in - nt * gm);
 }
 
+// v4f of four columns of a row of bf16 or fp32, zeros past its end; at: the first
+// one's index, left: the row's columns from there (it may be none); VEC: rows are of
+// whole fours.  What is past the end is read from the row's last columns and dropped:
+// branches would split a loop's loads (dz of 203 x 1001: 6.6 us with them, 4.6 without).
+template <bool F32, bool VEC>
+__device__ __forceinline__ v4f load4(const void* src, int64_t at, int left) {
+    float v[4];
+    if constexpr (VEC) {
+        const int64_t a = at + min(0, left - 4);
+        if constexpr (F32) {
+            const v4f w = *reinterpret_cast<const v4f*>((const float*)src + a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = w[i];
+        } else {
+            load_bf16x4((const uint16_t*)src + a, v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t a = at + min(i, left - 1);
+            v[i] = F32 ? ((const float*)src)[a] : bf16_to_f32(((const uint16_t*)src)[a]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? v[i] : 0.f;
+    return v4f{v[0], v[1], v[2], v[3]};
+}
+
 // Epilogue of ROWS x COLS fp32 results that the workgroup has put into LDS: rows
 // leave in order, 16 bytes of LDS (four columns) per thread and step, so that
 // global accesses are whole lines and the element-wise code exists once (written
@@ -88,7 +116,10 @@ struct TileEpilogue {
 
 // ---------------------------------------------------------------- 64 x 64 wave tiles
 // WM x WN waves of 64 x 64, K steps of 64 double-buffered in LDS: while a step is
-// multiplied the next one is on its way.
+// multiplied the next one is on its way.  Two workgroups per compute unit hide each
+// other's barriers: 12000 x 600 over 1200 in 29 us (0.60 PFLOP/s; 128 x 256 tiles 39 us,
+// whose last round is emptier).  Bound by the wait for the LDS DMA, which one step of
+// look-ahead does not cover.
 template <int WM, int WN, int LA, int LB, int EPI>
 __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
     constexpr int BM = WM * 64, BN = WN * 64, NW = WM * WN;
@@ -255,17 +286,18 @@ __global__ __launch_bounds__(WM * WN * 64) void dense_kernel(DenseArgs g) {
 // ---------------------------------------------------------------- 64 x 64 tiles
 // Small problems, where a K loop's time is its loads' latency: four waves of 32 x 32,
 // a ring of five K steps in LDS (80 KB, two workgroups per compute unit), four of
-// them in flight while one is multiplied, one barrier per step.
-constexpr int RING = 5;
+// them in flight while one is multiplied, one barrier per step.  1237 x 688 over 1032
+// takes 7.8 us (0.22 PFLOP/s): its 17 steps are 3.7 us, launch, first loads and
+// epilogue the rest.
+constexpr int RING = 5, SMALL_STAGE = 16384;  // A, B: 64 rows (columns) of a step
 template <int LA, int LB, int EPI>
-__global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
-    constexpr int HALF = 8192, STAGE = 2 * HALF;  // A, B: 64 rows (columns) of a step
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * STAGE];
+__device__ __forceinline__ void small_tile(const DenseArgs& g, int bid, int tiles, uint8_t* smem) {
+    constexpr int STAGE = SMALL_STAGE, HALF = STAGE / 2;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int mt, nt, split;
-    dense_tile(g, blockIdx.x, gridDim.x, mt, nt, split);
+    dense_tile(g, bid, tiles, mt, nt, split);
     const int64_t m0 = (int64_t)mt * 64;
     const int n0 = nt * (EPI == EPI_GATE ? 32 : 64);
     const int ks0 = split * g.ksteps;
@@ -387,6 +419,75 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
     __syncthreads();
     epi.run(g, smem, m0, n0, split);
 }
+template <int LA, int LB, int EPI>
+__global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * SMALL_STAGE];
+    small_tile<LA, LB, EPI>(g, blockIdx.x, gridDim.x, smem);
+}
+
+// Column sums of 32 columns over all rows, as bf16: 8 threads to a row (four columns
+// each), 32 rows at a time and eight such loads in flight, added in a fixed order.
+template <bool F32, bool VEC>
+__device__ __forceinline__ v4f colsum_rows(const ColSum& c, int64_t n, int q) {
+    constexpr int R = 8;
+    v4f s = {0.f, 0.f, 0.f, 0.f};
+    const int left = (int)(c.N - n);
+    if (left <= 0) return s;
+    for (int64_t t = q; t < c.rows; t += 32 * R) {
+        v4f v[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] = load4<F32, VEC>(c.src, min(t + 32 * i, c.rows - 1) * c.ld + n, left);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (t + 32 * i < c.rows) s += v[i];
+    }
+    return s;
+}
+__device__ __forceinline__ void colsum_block(const ColSum& c, int block, uint8_t* smem) {
+    float* sm = reinterpret_cast<float*>(smem);  // [32 rows][32 columns]
+    const int64_t n = (int64_t)block * 32 + (threadIdx.x & 7) * 4;
+    const int q = threadIdx.x >> 3;
+    const bool vec = (c.N & 3) == 0;
+    const v4f s = c.f32 ? (vec ? colsum_rows<true, true>(c, n, q) : colsum_rows<true, false>(c, n, q))
+                        : (vec ? colsum_rows<false, true>(c, n, q) : colsum_rows<false, false>(c, n, q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm[q * 32 + (threadIdx.x & 7) * 4 + i] = s[i];
+    __syncthreads();
+    const int64_t m = (int64_t)block * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && m < c.N) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v += sm[i * 32 + threadIdx.x];
+        c.out[m] = (uint16_t)cvt_bf16x2(v, 0.f);
+    }
+}
+
+// A small problem's gradients in one launch: up to two weight gradients, column
+// sums, the data gradient; the longest sums over K first.  None of them fills the
+// compute units by itself, and each launch has a few us of its own: the backward of
+// a 1032 -> 344 gated block takes 25.7 -> 15.6 us at 64 rows and 45.2 -> 30.0 at 1237
+// (5 launches -> 1 behind dG, dU), of a 1024 -> 256 linear layer 12.0 -> 8.5 at 1000
+// rows.  Bound by launch and load latency below 200 rows, by the LDS DMA of 64 x 64
+// tiles above.  A ring of three or four steps (three workgroups per unit) is no faster.
+__global__ __launch_bounds__(256) void dense_group_kernel(DenseGroup g) {
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * SMALL_STAGE];
+    int b = blockIdx.x;
+    if (b < g.tiles[1]) {
+        small_tile<OP_KS, OP_KS, EPI_PLAIN>(g.dw[0], b, g.tiles[1], smem);
+        return;
+    }
+    b -= g.tiles[1];
+    if (b < g.tiles[2]) {
+        small_tile<OP_KS, OP_KS, EPI_PLAIN>(g.dw[1], b, g.tiles[2], smem);
+        return;
+    }
+    b -= g.tiles[2];
+    if (b < g.sums[0].blocks) return colsum_block(g.sums[0], b, smem);
+    b -= g.sums[0].blocks;
+    if (b < g.sums[1].blocks) return colsum_block(g.sums[1], b, smem);
+    b -= g.sums[1].blocks;
+    small_tile<OP_KC, OP_KS, EPI_PLAIN>(g.dx, b, g.tiles[0], smem);
+}
 
 // ---------------------------------------------------------------- 256 x 256 tiles
 // Eight waves as 2 (M) x 4 (N); a wave owns, of each 128-row half of A and each
@@ -416,6 +517,11 @@ __global__ __launch_bounds__(256) void dense_small_kernel(DenseArgs g) {
 // HM = 1: 128 x 256 tiles, for products with too few 256 x 256 ones.  A K step is
 // then one phase (16 fragments read, 32 MFMAs, 6 DMA instructions) and LDS holds
 // three stages of 48 KB, so the DMA still runs two steps ahead.
+//
+// 16384 x 4096 over 7168 (gated, [G, U] saved) takes 654 us, 1.47 PFLOP/s; 16384 x 7168
+// over 2048 with a residual 408 us, as a data gradient over 4096 680 us (1.41), 4096 x
+// 7168 over 16384 as a weight gradient 699 us (1.38).  The clock is 1.77 GHz under
+// that load (power), the matrix cores are busy 62-68% of it; tiles' ends take the rest.
 //
 // act: the activation of the gated epilogues at compile time (-1: at run time).
 constexpr bool is_direct(int epi, int act) {
@@ -945,7 +1051,8 @@ __global__ __launch_bounds__(512, 1) void dense_wide_kernel(DenseArgs g, int til
 }
 
 // ---------------------------------------------------------------- split K: sum and epilogue
-// One thread per four columns; the pieces are added in order.
+// One thread per four columns; the pieces are added in order.  Bound by reading them
+// (from the LLC, just written): two of 16384 x 256 into fp32 take 12 us, 4.2 TB/s.
 template <int EPI>
 __global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits) {
     const int cols = EPI == EPI_GATE ? g.f : (int)g.part_ld;
@@ -997,6 +1104,7 @@ struct Shape {
     int64_t mt, nt;
     int splits, ksteps;
     bool pieces;  // results go through the workspace and dense_sum_kernel
+    double us;    // estimated
 };
 // K in at most `sp` pieces of at least `least` steps
 void set_splits(Shape& s, int64_t K, int64_t sp, int64_t least) {
@@ -1040,6 +1148,7 @@ Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
     s.ksteps = (int)((K + DBK - 1) / DBK);
     s.mt = 1;
     s.pieces = false;
+    s.us = 0.;
     if (la == OP_KC && lb == OP_KC && M <= SLAB_ROWS) {
         s.kind = M <= THIN_ROWS && epi != EPI_GATE8 ? THIN : SLAB;
         s.nt = (N + 127) / 128;
@@ -1079,6 +1188,7 @@ Shape dense_shape(int64_t M, int64_t N, int64_t K, int la, int lb, int epi) {
             if (us < least) {
                 least = us;
                 best = c;
+                best.us = us;
             }
         }
     }
@@ -1204,11 +1314,67 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
     return launch_layout<EPI_PLAIN>(g, la, lb, 1, stream);
 }
 
+// The group is taken where its estimated time is less than the single products' and
+// the column sums' two launches (4 us each).  A group's time: its longest sum over K,
+// or all steps dealt to two workgroups per compute unit and half a longest one.
+// Measured on 66 shapes: gated 2048 -> 512 at 2048 rows 54 us (alone 68), 4096 -> 512 at
+// 4096 rows 201 (170); linear 7168 -> 256 at 203 rows 11.0 (12.4), at 2048 43.5 (36.8);
+// the rule's choice is within 10% of the better one on 64 of them.
+bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, bool sums) {
+    const DenseArgs* p[3] = {dx, dw0, dw1};
+    const Tiling& t = TILINGS[3];
+    double alone = sums ? 8. : 0., steps = 0., longest = 0.;
+    int n = 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!p[i]) continue;
+        const DenseArgs& g = *p[i];
+        const int64_t c = ((g.M + 63ll) / 64) * ((g.N + 63ll) / 64), ks = (g.K + DBK - 1) / DBK;
+        alone += dense_shape(g.M, g.N, g.K, i == 0 ? OP_KC : OP_KS, OP_KS, EPI_PLAIN).us;
+        steps += (double)c * ks;
+        if (longest < ks) longest = (double)ks;
+        tiles += c;
+        ++n;
+    }
+    if (n + (sums ? 1 : 0) < 2 || n == 0 || tiles >= (1 << 22)) return false;
+    const int64_t cus = num_cus();
+    const double step = tiles <= cus ? t.alone : t.shared;
+    double us = steps / (t.per_cu * cus) * t.shared + longest * step / 2;
+    if (us < longest * step) us = longest * step;
+    return us + t.fixed < alone;
+}
+
+int dense_group_launch(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, const ColSum* sums, int nsums,
+                       hipStream_t stream) {
+    const DenseArgs* p[3] = {dx, dw0, dw1};
+    DenseGroup g = {};
+    DenseArgs* q[3] = {&g.dx, &g.dw[0], &g.dw[1]};
+    int64_t blocks = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!p[i]) continue;
+        *q[i] = *p[i];
+        q[i]->mt = (p[i]->M + 63) / 64;
+        q[i]->nt = (p[i]->N + 63) / 64;
+        q[i]->ksteps = (p[i]->K + DBK - 1) / DBK;
+        g.tiles[i] = q[i]->mt * q[i]->nt;
+        blocks += g.tiles[i];
+    }
+    for (int i = 0; i < nsums; ++i) {
+        g.sums[i] = sums[i];
+        g.sums[i].blocks = (int)((sums[i].N + 31) / 32);
+        blocks += g.sums[i].blocks;
+    }
+    dense_group_kernel<<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(g);
+    MOE_LAUNCH_CHECK("dense_group_kernel");
+    return MOE_OK;
+}
+
 // ---------------------------------------------------------------- column sums, zeros
 // Column sums in two launches: fp32 sums of chunks of rows, then the chunks'
 // sums in a fixed order.  Bound by the bytes read; what matters is loads in
 // flight: a wave takes 256 columns and CS_ROWS / 4 rows of a chunk, all loaded
-// before the first is added.
+// before the first is added.  dz and chunks of 16384 x 256 from fp32 take
+// 8.2 us (3.1 TB/s; too short to reach more), the chunks' sums 6 us.
 namespace {
 constexpr int CS_ROWS = 8;  // rows of a chunk that are loaded at a time
 struct Chunks {
@@ -1224,22 +1390,6 @@ Chunks colsum_chunks(int64_t T) {
 }
 }  // namespace
 
-// v4f of four columns n .. n + 3 of a row (fp32 or bf16), zeros past N; vec: N % 4 == 0
-__device__ __forceinline__ v4f load4(const void* src, int f32, int64_t at, int64_t n, int64_t N, bool vec) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-        if (n < N) {
-            if (f32) return *reinterpret_cast<const v4f*>((const float*)src + at);
-            load_bf16x4((const uint16_t*)src + at, v);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < N) v[i] = f32 ? ((const float*)src)[at + i] : bf16_to_f32(((const uint16_t*)src)[at + i]);
-    }
-    return v4f{v[0], v[1], v[2], v[3]};
-}
-
 // dz = dy * act'(pre) of moe_linear_backward: bf16 rows of stride ldz (columns
 // past N zero) if dz is given, and fp32 column sums over chunks of rows (before
 // the rounding) if part is given.  One thread per four columns of a row.
@@ -1254,14 +1404,13 @@ struct DzArgs {
     uint16_t* out;  // [N]
     int blocks;     // of 256 columns
 };
-template <bool ACT>
+template <bool ACT, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs d0, DzArgs d1, int act, int64_t T, int64_t rows) {
     __shared__ float sm[4][256];
     const bool second = (int)blockIdx.x >= d0.blocks;
     const DzArgs& d = second ? d1 : d0;
     const int bx = blockIdx.x - (second ? d0.blocks : 0);
     const void* dy = d.dy;
-    const int dy_f32 = d.dy_f32;
     const int64_t ld = d.ld, N = d.N, ldz = d.ldz;
     const uint16_t* pre = d.pre;
     uint16_t* dz = d.dz;
@@ -1269,7 +1418,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs d0, DzArgs d1, int act, 
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t n = (int64_t)bx * 256 + lane * 4;
     const int64_t t0 = (int64_t)blockIdx.y * rows, t1 = min(t0 + rows, T);
-    const bool vec = (N & 3) == 0;
+    const int left = (int)(N - n);
     constexpr int R = CS_ROWS / 4;
     v4f s = {0.f, 0.f, 0.f, 0.f};
     if (n < ldz) {
@@ -1278,8 +1427,8 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs d0, DzArgs d1, int act, 
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int64_t r = min(t + 4 * i, t1 - 1);
-                v[i] = load4(dy, dy_f32, r * ld + n, n, N, vec);
-                if (ACT) p[i] = load4(pre, 0, r * N + n, n, N, vec);
+                v[i] = load4<F32, VEC>(dy, r * ld + n, left);
+                if (ACT) p[i] = load4<false, VEC>(pre, r * N + n, left);
             }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -1334,18 +1483,25 @@ __global__ __launch_bounds__(256) void zero16_kernel(uint16_t* p, int64_t n) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
+int colsum_parts(int64_t T) { return colsum_chunks(T).n; }
 size_t colsum_ws(int64_t T, int64_t N) { return (size_t)colsum_chunks(T).n * N * 4; }
 
 namespace {
+using yes = std::true_type;
+using no = std::false_type;
 int dz_both(DzArgs d0, DzArgs d1, int act, int64_t T, hipStream_t stream) {
     const Chunks c = colsum_chunks(T);
     d0.blocks = (int)((d0.ldz + 255) / 256);
     d1.blocks = (int)((d1.ldz + 255) / 256);
     const dim3 grid((unsigned)(d0.blocks + d1.blocks), c.n);
-    if (act != MOE_ACT_NONE)
-        dz_kernel<true><<<grid, dim3(256), 0, stream>>>(d0, d1, act, T, c.rows);
-    else
-        dz_kernel<false><<<grid, dim3(256), 0, stream>>>(d0, d1, act, T, c.rows);
+    const bool vec = d0.N % 4 == 0;  // (d1: bf16 of a multiple of 8 columns, beside such a d0 without act)
+    auto go = [&](auto act_c, auto f32_c, auto vec_c) {
+        dz_kernel<decltype(act_c)::value, decltype(f32_c)::value, decltype(vec_c)::value>
+            <<<grid, dim3(256), 0, stream>>>(d0, d1, act, T, c.rows);
+    };
+    auto pick = [&](auto act_c, auto f32_c) { vec ? go(act_c, f32_c, yes{}) : go(act_c, f32_c, no{}); };
+    auto pick_f32 = [&](auto act_c) { d0.dy_f32 ? pick(act_c, yes{}) : pick(act_c, no{}); };
+    act != MOE_ACT_NONE ? pick_f32(yes{}) : pick_f32(no{});
     MOE_LAUNCH_CHECK("dz_kernel");
     if (!d0.out) return MOE_OK;
     const int64_t blocks = (d0.N + 15) / 16 + (d1.N + 15) / 16;
@@ -1357,7 +1513,7 @@ int dz_both(DzArgs d0, DzArgs d1, int act, int64_t T, hipStream_t stream) {
 
 int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
               float* part, uint16_t* dbias, hipStream_t stream) {
-    const DzArgs d = {dy, dy_f32, N, pre, N, ldz, dz, dbias ? part : nullptr, dbias, 0};
+    const DzArgs d = {dy, dy_f32, N, pre, N, ldz, dz, part, dbias, 0};
     return dz_both(d, DzArgs{}, act, T, stream);
 }
 

@@ -468,8 +468,28 @@ size_t dense_ws(int64_t M, int64_t N, int64_t K, int la, int lb, int epi);
 size_t colsum_ws(int64_t T, int64_t N);
 int colsum_launch(const uint16_t* a, int64_t Na, uint16_t* out_a, const uint16_t* b, int64_t Nb, uint16_t* out_b,
                   int64_t T, float* part, hipStream_t stream);
-// dz = dy * act'(pre) [T, ldz] bf16 (dz may be NULL) and its column sums (dbias
-// may be NULL; part then unused); dy [T, N] dense, ldz = N rounded up to 8
+// A small problem's gradients in one launch: a data gradient (KC, KS), weight
+// gradients (KS, KS), each NULL if not wanted, and column sums
+struct ColSum {
+    const void* src;  // [rows, ld], bf16 or fp32
+    int f32;
+    int64_t ld, rows, N;
+    uint16_t* out;  // [N]
+    int blocks;     // of 32 columns (filled in by the launch)
+};
+struct DenseGroup {
+    DenseArgs dx, dw[2];
+    ColSum sums[2];
+    int tiles[3];
+};
+bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, bool sums);
+int dense_group_launch(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, const ColSum* sums, int nsums,
+                       hipStream_t stream);
+
+// dz = dy * act'(pre) [T, ldz] bf16 (dz may be NULL) and its column sums: part
+// [colsum_parts(T), ldz] fp32 those of chunks of rows (may be NULL), dbias their
+// sums (may be NULL); dy [T, N] dense, ldz = N rounded up to 8
+int colsum_parts(int64_t T);
 int dz_launch(const void* dy, int dy_f32, const uint16_t* pre, int act, int64_t T, int64_t N, int64_t ldz, uint16_t* dz,
               float* part, uint16_t* dbias, hipStream_t stream);
 

@@ -176,51 +176,53 @@ extern "C" int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int
         g.h = dW2 ? h : nullptr;
         if (const int rc = dense_launch(g, OP_KC, OP_KS, EPI_DGATE, gw, gwb, stream)) return rc;
     }
-    DenseArgs g = {};
-    g.vec = 1;
-    if (dx) {  // [T, 2f] x [2f, d]
-        g.a = dgu;
-        g.lda = 2 * f;
-        g.b = W13;
-        g.ldb = d;
-        g.M = (int)T;
-        g.N = (int)d;
-        g.K = (int)(2 * f);
-        g.b_cols = (int)d;
-        g.res = dx_add;
-        g.ldr = d;
-        g.out = dx;
-        g.ldo = d;
-        if (const int rc = dense_launch(g, OP_KC, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
-        g.res = nullptr;
+    // dx [T, 2f] x [2f, d]
+    DenseArgs gx = {}, g13 = {}, g2 = {};
+    gx.vec = g13.vec = g2.vec = 1;
+    gx.a = dgu;
+    gx.lda = 2 * f;
+    gx.b = W13;
+    gx.ldb = d;
+    gx.M = (int)T;
+    gx.N = gx.b_cols = (int)d;
+    gx.K = (int)(2 * f);
+    gx.res = dx_add;
+    gx.ldr = d;
+    gx.out = dx;
+    gx.ldo = d;
+    // dW13 [T, 2f]^T x [T, d]
+    g13.a = dgu;
+    g13.lda = 2 * f;
+    g13.b = x;
+    g13.ldb = ldx;
+    g13.M = g13.a_cols = (int)(2 * f);
+    g13.N = g13.b_cols = (int)d;
+    g13.K = (int)T;
+    g13.out = dW13;
+    g13.ldo = d;
+    // dW2 [T, d]^T x [T, f]
+    g2.a = dy;
+    g2.lda = d;
+    g2.b = h;
+    g2.ldb = f;
+    g2.M = g2.a_cols = (int)d;
+    g2.N = g2.b_cols = (int)f;
+    g2.K = (int)T;
+    g2.out = dW2;
+    g2.ldo = f;
+    const DenseArgs *px = dx ? &gx : nullptr, *p13 = dW13 ? &g13 : nullptr, *p2 = dW2 ? &g2 : nullptr;
+    if (dense_group_pays(px, p13, p2, db13 || db2)) {
+        ColSum sums[2];
+        int n = 0;
+        if (db13) sums[n++] = ColSum{dgu, 0, 2 * f, T, 2 * f, db13, 0};
+        if (db2) sums[n++] = ColSum{dy, 0, d, T, d, db2, 0};
+        return dense_group_launch(px, p13, p2, sums, n, stream);
     }
-    if (dW13) {  // [T, 2f]^T x [T, d]
-        g.a = dgu;
-        g.lda = 2 * f;
-        g.b = x;
-        g.ldb = ldx;
-        g.M = (int)(2 * f);
-        g.N = (int)d;
-        g.K = (int)T;
-        g.a_cols = (int)(2 * f);
-        g.b_cols = (int)d;
-        g.out = dW13;
-        g.ldo = d;
-        if (const int rc = dense_launch(g, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
-    }
-    if (dW2) {  // [T, d]^T x [T, f]
-        g.a = dy;
-        g.lda = d;
-        g.b = h;
-        g.ldb = f;
-        g.M = (int)d;
-        g.N = (int)f;
-        g.K = (int)T;
-        g.a_cols = (int)d;
-        g.b_cols = (int)f;
-        g.out = dW2;
-        g.ldo = f;
-        if (const int rc = dense_launch(g, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
-    }
+    if (dx)
+        if (const int rc = dense_launch(gx, OP_KC, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
+    if (dW13)
+        if (const int rc = dense_launch(g13, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
+    if (dW2)
+        if (const int rc = dense_launch(g2, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
     return colsum_launch(dgu, 2 * f, db13, dy, d, db2, T, part, stream);
 }

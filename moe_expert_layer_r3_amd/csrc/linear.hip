@@ -125,53 +125,52 @@ extern "C" int moe_linear_backward(const void* dy, int32_t dy_type, const uint16
     MOE_REQUIRE((ws && aligned16(ws)) || !w.total, MOE_ERR_NULL, "ws is NULL or not 16-byte aligned");
     MOE_REQUIRE(ws_bytes >= w.total, MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, w.total);
     uint8_t* wp = (uint8_t*)ws;
-    void* gw = wp + w.gemm;
+    void* gws = wp + w.gemm;
     const size_t gwb = ws_bytes - w.gemm;
 
-    const uint16_t* dz = (const uint16_t*)dy;
-    int64_t ldz = N;
     const bool own = needs_dz(dy_type, N, act);
-    if (own || dbias) {
+    const int64_t ldz = own ? round_up(N, 8) : N;
+    const uint16_t* dz = own ? (const uint16_t*)(wp + w.dz) : (const uint16_t*)dy;
+    float* part = (float*)(wp + w.part);
+    DenseArgs gx = {}, gw = {};
+    gx.vec = gw.vec = 1;  // K % 8 == 0 and dense outputs
+    gx.ldo = gw.ldo = K;
+    gx.a = gw.a = dz;
+    gx.lda = gw.lda = ldz;
+    // [T, N] x [N, K]
+    gx.b = W;
+    gx.ldb = ldw;
+    gx.M = (int)T;
+    gx.N = gx.b_cols = (int)K;
+    gx.K = (int)N;
+    gx.res = dx_add;
+    gx.ldr = K;
+    gx.out = dx;
+    // [T, N]^T x [T, K]
+    gw.b = x;
+    gw.ldb = ldx;
+    gw.M = (int)N;
+    gw.N = gw.b_cols = (int)K;
+    gw.K = (int)T;
+    gw.a_cols = (int)ldz;
+    gw.out = dW;
+    const DenseArgs *px = dx ? &gx : nullptr, *pw = dW ? &gw : nullptr;
+
+    const bool group = dense_group_pays(px, pw, nullptr, dbias);
+    if (own || (dbias && !group)) {
         const int64_t ldp = round_up(N, 8);
         if (const int rc = dz_launch(dy, dy_type == MOE_SRC_F32, act == MOE_ACT_NONE ? nullptr : pre, act, T, N, ldp,
-                                     own && (dx || dW) ? (uint16_t*)(wp + w.dz) : nullptr, (float*)(wp + w.part), dbias,
-                                     stream))
+                                     own && (dx || dW) ? (uint16_t*)(wp + w.dz) : nullptr, dbias ? part : nullptr,
+                                     group ? nullptr : dbias, stream))
             return rc;
-        if (own) {
-            dz = (const uint16_t*)(wp + w.dz);
-            ldz = ldp;
-        }
     }
-    DenseArgs g = {};
-    g.vec = 1;  // K % 8 == 0 and dense outputs
-    g.ldo = K;
-    if (dx) {  // [T, N] x [N, K]
-        g.a = dz;
-        g.lda = ldz;
-        g.b = W;
-        g.ldb = ldw;
-        g.M = (int)T;
-        g.N = (int)K;
-        g.K = (int)N;
-        g.b_cols = (int)K;
-        g.res = dx_add;
-        g.ldr = K;
-        g.out = dx;
-        if (const int rc = dense_launch(g, OP_KC, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
+    if (group) {
+        const ColSum sum = own ? ColSum{part, 1, ldz, colsum_parts(T), N, dbias, 0} : ColSum{dy, 0, N, T, N, dbias, 0};
+        return dense_group_launch(px, pw, nullptr, &sum, dbias ? 1 : 0, stream);
     }
-    if (dW) {  // [T, N]^T x [T, K]
-        g.a = dz;
-        g.lda = ldz;
-        g.b = x;
-        g.ldb = ldx;
-        g.M = (int)N;
-        g.N = (int)K;
-        g.K = (int)T;
-        g.a_cols = (int)ldz;
-        g.b_cols = (int)K;
-        g.res = nullptr;
-        g.out = dW;
-        if (const int rc = dense_launch(g, OP_KS, OP_KS, EPI_LINEAR, gw, gwb, stream)) return rc;
-    }
+    if (dx)
+        if (const int rc = dense_launch(gx, OP_KC, OP_KS, EPI_LINEAR, gws, gwb, stream)) return rc;
+    if (dW)
+        if (const int rc = dense_launch(gw, OP_KS, OP_KS, EPI_LINEAR, gws, gwb, stream)) return rc;
     return MOE_OK;
 }

@@ -433,6 +433,39 @@ def test_offsets_past_32_bits():
     assert ((out[-200:].double() - ref).abs() <= e + U16 * (ref.abs() + e) + 1e-30).all()
 
 
+def ints(shape, seed):
+    """-1, 0 and 1: every sum of the tests that use them is exact in fp32, whatever its order."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-1, 2, shape, device=DEV, generator=g).to(BF)
+
+
+@pytest.mark.parametrize("T, d, f", [(2, 72, 40), (90, 72, 136), (700, 72, 136), (1237, 520, 264), (3300, 520, 264)])
+def test_gradients_one_by_one(T, d, f):
+    """Each gradient alone and without the others, against all at once."""
+    p = lambda t: None if t is None else t.data_ptr()
+    x, W13, W2, dy, W = ints((T, d), 1), ints((2 * f, d), 2), ints((d, f), 3), ints((T, d), 4), ints((f, d), 5)
+    plan = GatedFFNPlan(T, d, f, act="relu", save="bf16", bias=True, device=DEV)
+    plan.forward(x, W13, W2)
+    want = [t.clone() for t in plan.backward(dy, x, W13, W2)]
+    assert torch.equal(want[4], dy.double().sum(0).to(BF))
+    n = len(want)
+    for on in [{i} for i in range(n)] + [set(range(n)) - {i} for i in range(n)] + [{1, 2}, {3, 4}, {0, 4}]:
+        out = [torch.empty_like(t) if i in on else None for i, t in enumerate(want)]
+        ops.launch("moe_gated_ffn_backward", x.device, p(dy), p(x), d, p(W13), p(W2), 1, p(plan.gu), None, None, T, d, f, 1,
+                   *map(p, out), p(plan.ws), plan.ws_bytes)
+        assert all(t is None or torch.equal(t, w) for t, w in zip(out, want)), on
+    dz = ints((T, f), 6)
+    plan = LinearPlan(T, d, f, train=True, bias=True, device=DEV)
+    want = [t.clone() for t in plan.backward(dz, x, W)]
+    for a, b in zip(want, (dz.double() @ W.double(), dz.double().t() @ x.double(), dz.double().sum(0))):
+        assert torch.equal(a, b.to(BF))
+    for on in ({0}, {1}, {2}, {0, 1}, {0, 2}, {1, 2}):
+        out = [torch.empty_like(t) if i in on else None for i, t in enumerate(want)]
+        ops.launch("moe_linear_backward", x.device, p(dz), 0, None, p(x), d, p(W), d, None, T, f, d, 0, *map(p, out),
+                   p(plan.ws), plan.ws_bytes)
+        assert all(t is None or torch.equal(t, w) for t, w in zip(out, want)), on
+
+
 def test_most_rows():
     """2^30 rows, the most there may be: blocks of rows repeat, and so do the results."""
     T, R = 1 << 30, 1 << 20
