@@ -16,29 +16,26 @@ typedef const __attribute__((address_space(4))) float* cfloat_ptr;
 
 // 16- / 4-byte global -> LDS transfer (global_load_lds_dwordx4 / _dword): lane
 // l's bytes land at LDS byte address m0 + l*size (m0 = `lds`, wave-uniform).
+// The address is a wave-uniform 64-bit base in SGPRs and a 32-bit per-lane byte
+// offset: the base advances by scalar adds along K, so no per-lane 64-bit address
+// arithmetic is needed in the loop.
 // Written as inline assembly so that the compiler does not know these VMEM
 // instructions write LDS: it would otherwise wait for all of them (vmcnt(0))
 // before every LDS read, serialising the pipeline.  Completion is awaited with
 // explicit vmcnt waits followed by a barrier before a stage is read.
-__device__ __forceinline__ void dma16(const void* g, uint32_t lds) {
-    asm volatile("global_load_lds_dwordx4 %0, off" : : "v"(g), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void dma4(const void* g, uint32_t lds) {
-    asm volatile("global_load_lds_dword %0, off" : : "v"(g), "{m0}"(lds) : "memory");
-}
-
-// The same transfers with a wave-uniform 64-bit base in SGPRs and a 32-bit
-// per-lane byte offset: the base advances by scalar adds along K, so no
-// per-lane 64-bit address arithmetic is needed in the loop.
+// For the same reason the compiler inserts none of the wait states in front of
+// them, so s_nop 4 is part of the block: five states between a vector
+// instruction's write of a base SGPR (v_readlane, where a base was spilled) and
+// the load, one between a write of M0 and the load.
 __device__ __forceinline__ void dma16s(const void* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("global_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 // the same with the non-temporal hint, for operand bytes no other tile reads
 __device__ __forceinline__ void dma16s_nt(const void* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("global_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1 nt" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma4s(const void* sbase, uint32_t voff, uint32_t lds) {
-    asm volatile("global_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1" : : "v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 
 // s_waitcnt immediate waiting for vmcnt <= N only (gfx9 encoding: vmcnt[3:0],
