@@ -480,6 +480,11 @@ int moe_linear_backward(const void* dy, int32_t dy_type, const uint16_t* pre, co
                         int32_t act, uint16_t* dx, uint16_t* dW, uint16_t* dbias,
                         void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* Whether the gradients that are asked for (flags dx, dW, dbias) come from one
+ * launch, where that is estimated faster, or from one each.                    */
+int moe_linear_backward_grouped(int64_t T, int64_t N, int64_t K, int32_t dy_type, int32_t act, int32_t dx, int32_t dW,
+                                int32_t dbias, int32_t* yes);
+
 /* Gated feed-forward block (a shared expert). With W13 [2f, d] = [Wg; Wu] and
  * b13 [2f] = [bg; bu]:
  *     G = x Wg^T + bg,  U = x Wu^T + bu,  h = act(G) * U      (one kernel)
@@ -512,6 +517,10 @@ int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t ldx, c
                            const uint16_t* dx_add, int64_t T, int64_t d, int64_t f, int32_t act,
                            uint16_t* dx, uint16_t* dW13, uint16_t* dW2, uint16_t* db13, uint16_t* db2,
                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* As moe_linear_backward_grouped, for the gradients behind [dG, dU].           */
+int moe_gated_ffn_backward_grouped(int64_t T, int64_t d, int64_t f, int32_t dx, int32_t dW13, int32_t dW2, int32_t dbias,
+                                   int32_t* yes);
 
 /* ---- activations kept in 8 bits between forward and backward ---------------
  * Rows in blocks of 128 columns (the last one shorter if cols % 128 != 0), one

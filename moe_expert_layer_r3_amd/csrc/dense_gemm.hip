@@ -1338,14 +1338,16 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
 
 // The group is taken where its estimated time is less than the single products' and
 // the column sums' two launches (4 us each).  A group's time: its longest sum over K,
-// or all steps dealt to two workgroups per compute unit and half a longest one.
+// or all steps dealt to two workgroups per compute unit and half a longest one, or
+// its column sums' rounds of 256 rows (0.45 to 0.66 us each: dx and dbias of 64 -> 64 at
+// 16384 rows 31 us grouped and 13 alone, at 65536 171 and 19; a weight gradient is longer).
 // Measured on 66 shapes: gated 2048 -> 512 at 2048 rows 54 us (alone 68), 4096 -> 512 at
 // 4096 rows 201 (170); linear 7168 -> 256 at 203 rows 11.0 (12.4), at 2048 43.5 (36.8);
 // the rule's choice is within 10% of the better one on 64 of them.
-bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, bool sums) {
+bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, int64_t sum_rows) {
     const DenseArgs* p[3] = {dx, dw0, dw1};
     const Tiling& t = TILINGS[3];
-    double alone = sums ? 8. : 0., steps = 0., longest = 0.;
+    double alone = sum_rows ? 8. : 0., steps = 0., longest = 0.;
     int n = 0;
     int64_t tiles = 0;
     for (int i = 0; i < 3; ++i) {
@@ -1358,11 +1360,13 @@ bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs
         tiles += c;
         ++n;
     }
-    if (n + (sums ? 1 : 0) < 2 || n == 0 || tiles >= (1 << 22)) return false;
+    if (n + (sum_rows ? 1 : 0) < 2 || n == 0 || tiles >= (1 << 22)) return false;
     const int64_t cus = num_cus();
     const double step = tiles <= cus ? t.alone : t.shared;
     double us = steps / (t.per_cu * cus) * t.shared + longest * step / 2;
     if (us < longest * step) us = longest * step;
+    const double sum_us = (double)((sum_rows + 255) / 256) * 0.5;
+    if (us < sum_us) us = sum_us;
     return us + t.fixed < alone;
 }
 

@@ -483,7 +483,8 @@ struct DenseGroup {
     ColSum sums[2];
     int tiles[3];
 };
-bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, bool sums);
+// (looks at M, N, K only; sum_rows: rows of the column sums, 0 without them)
+bool dense_group_pays(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, int64_t sum_rows);
 int dense_group_launch(const DenseArgs* dx, const DenseArgs* dw0, const DenseArgs* dw1, const ColSum* sums, int nsums,
                        hipStream_t stream);
 

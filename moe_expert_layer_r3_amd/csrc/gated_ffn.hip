@@ -28,6 +28,16 @@ int check_kind(int32_t act, int32_t save, int64_t f) {
     return MOE_OK;
 }
 
+// one launch for the gradients behind [dG, dU] that are wanted
+bool grouped(int64_t T, int64_t d, int64_t f, bool dx, bool dW13, bool dW2, bool dbias) {
+    DenseArgs gx = {}, g13 = {}, g2 = {};
+    gx.M = g13.K = g2.K = (int)T;
+    gx.N = g13.N = g2.M = (int)d;
+    gx.K = g13.M = (int)(2 * f);
+    g2.N = (int)f;
+    return dense_group_pays(dx ? &gx : nullptr, dW13 ? &g13 : nullptr, dW2 ? &g2 : nullptr, dbias ? T : 0);
+}
+
 struct BackwardWs {
     size_t dgu, h, part, gemm, total;
 };
@@ -117,6 +127,15 @@ extern "C" int moe_gated_ffn_backward_workspace(int64_t T, int64_t d, int64_t f,
     MOE_REQUIRE(bytes, MOE_ERR_NULL, "bytes is NULL");
     if (const int rc = check_sizes(T, d, f)) return rc;
     *bytes = backward_ws(T, d, f).total;
+    return MOE_OK;
+}
+
+extern "C" int moe_gated_ffn_backward_grouped(int64_t T, int64_t d, int64_t f, int32_t dx, int32_t dW13, int32_t dW2,
+                                              int32_t dbias, int32_t* yes) {
+    clear_error();
+    MOE_REQUIRE(yes, MOE_ERR_NULL, "yes is NULL");
+    if (const int rc = check_sizes(T, d, f)) return rc;
+    *yes = T > 0 && grouped(T, d, f, dx, dW13, dW2, dbias);
     return MOE_OK;
 }
 
@@ -211,7 +230,7 @@ extern "C" int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int
     g2.out = dW2;
     g2.ldo = f;
     const DenseArgs *px = dx ? &gx : nullptr, *p13 = dW13 ? &g13 : nullptr, *p2 = dW2 ? &g2 : nullptr;
-    if (dense_group_pays(px, p13, p2, db13 || db2)) {
+    if (grouped(T, d, f, dx, dW13, dW2, db13 || db2)) {
         ColSum sums[2];
         int n = 0;
         if (db13) sums[n++] = ColSum{dgu, 0, 2 * f, T, 2 * f, db13, 0};

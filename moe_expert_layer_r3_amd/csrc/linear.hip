@@ -22,6 +22,15 @@ bool operand_ok(const void* p, int64_t ld, int64_t cols) {
     return aligned16(p) && ld >= cols && ld <= MAX_LD && ld % 8 == 0;
 }
 
+// one launch for the gradients that are wanted
+bool grouped(int64_t T, int64_t N, int64_t K, bool own, bool dx, bool dW, bool dbias) {
+    DenseArgs gx = {}, gw = {};
+    gx.M = gw.K = (int)T;
+    gx.N = gw.N = (int)K;
+    gx.K = gw.M = (int)N;
+    return dense_group_pays(dx ? &gx : nullptr, dW ? &gw : nullptr, nullptr, !dbias ? 0 : own ? colsum_parts(T) : T);
+}
+
 struct BackwardWs {
     size_t dz, part, gemm, total;
 };
@@ -97,6 +106,15 @@ extern "C" int moe_linear_backward_workspace(int64_t T, int64_t N, int64_t K, si
     return MOE_OK;
 }
 
+extern "C" int moe_linear_backward_grouped(int64_t T, int64_t N, int64_t K, int32_t dy_type, int32_t act, int32_t dx,
+                                           int32_t dW, int32_t dbias, int32_t* yes) {
+    clear_error();
+    MOE_REQUIRE(yes, MOE_ERR_NULL, "yes is NULL");
+    if (const int rc = check_sizes(T, N, K)) return rc;
+    *yes = T > 0 && grouped(T, N, K, needs_dz(dy_type, N, act), dx, dW, dbias);
+    return MOE_OK;
+}
+
 extern "C" int moe_linear_backward(const void* dy, int32_t dy_type, const uint16_t* pre, const uint16_t* x, int64_t ldx,
                                    const uint16_t* W, int64_t ldw, const uint16_t* dx_add, int64_t T, int64_t N,
                                    int64_t K, int32_t act, uint16_t* dx, uint16_t* dW, uint16_t* dbias, void* ws,
@@ -156,7 +174,7 @@ extern "C" int moe_linear_backward(const void* dy, int32_t dy_type, const uint16
     gw.out = dW;
     const DenseArgs *px = dx ? &gx : nullptr, *pw = dW ? &gw : nullptr;
 
-    const bool group = dense_group_pays(px, pw, nullptr, dbias);
+    const bool group = grouped(T, N, K, own, dx, dW, dbias);
     if (own || (dbias && !group)) {
         const int64_t ldp = round_up(N, 8);
         if (const int rc = dz_launch(dy, dy_type == MOE_SRC_F32, act == MOE_ACT_NONE ? nullptr : pre, act, T, N, ldp,

@@ -75,12 +75,16 @@ _SIGS = {
     "moe_linear_backward_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "moe_linear_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _P,
                                            _P, _SZ, _P]),
+    "moe_linear_backward_grouped": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32,
+                                                   ctypes.POINTER(_I32)]),
     "moe_gated_ffn_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "moe_gated_ffn": (ctypes.c_int, [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _P,
                                      _P, _SZ, _P]),
     "moe_gated_ffn_backward_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "moe_gated_ffn_backward": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I32, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P,
                                               _P, _P, _P, _P, _SZ, _P]),
+    "moe_gated_ffn_backward_grouped": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _I32, _I32,
+                                                      ctypes.POINTER(_I32)]),
     "moe_act_save": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "moe_act_restore": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
 }
