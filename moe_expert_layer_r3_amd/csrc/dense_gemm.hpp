@@ -56,7 +56,9 @@ struct DenseArgs {
 // ---------------------------------------------------------------- activations
 // act(z) and act'(z) of four values; `act` is uniform.  sigmoid from the hardware
 // exp2 and reciprocal (about 1 ulp each).
-__device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * (1.f + erff(z * 0.70710678118654752f)); }
+// Phi(z): the complementary function keeps its relative accuracy for z << 0, where
+// 1 + erf(z / sqrt 2) would cancel.
+__device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
 __device__ __forceinline__ float relu(float z) { return z > 0.f ? z : (z == z ? 0.f : z); }  // NaN stays NaN
 __device__ __forceinline__ void act_value4(int act, const float* z, float* v) {
     switch (act) {
@@ -109,8 +111,11 @@ __device__ __forceinline__ void act_both4(int act, const float* z, float* v, flo
         case MOE_ACT_SIGMOID:
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[i] = sigmoid_fast(z[i]);
-                slope[i] = v[i] * (1.f - v[i]);
+                // s(z) s(-z) from e = exp(-|z|), without 1 - s, which cancels for z >> 0
+                const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * __builtin_fabsf(z[i]));
+                const float r = __builtin_amdgcn_rcpf(1.f + e);
+                v[i] = z[i] < 0.f ? e * r : r;
+                slope[i] = e * r * r;
             }
             return;
         default:
