@@ -1285,10 +1285,6 @@ int dense_launch(DenseArgs g, int la, int lb, int epi, void* ws, size_t ws_bytes
     g.mt = (int)s.mt;
     g.nt = (int)s.nt;
     g.ksteps = s.ksteps;
-    // Results of 64 MB and more of a product that mostly writes pass the caches by, which
-    // keeps the operands of the next product there: 16384 x 7168 over 256 and the weight
-    // gradient behind it 214 -> 206 us, over 1024 425 -> 439, 4096 x 4096 over 256 39.6 -> 40.3.
-    g.past = g.K <= 256 && (int64_t)g.M * g.N >= 1 << 25;
     if (s.kind == THIN) return dense_thin_launch(g, epi, stream);
     if (s.pieces) {
         MOE_REQUIRE(ws && aligned16(ws) && ws_bytes >= (size_t)s.splits * g.M * round_up(g.N, 4) * 4, MOE_ERR_WORKSPACE,

@@ -41,7 +41,7 @@ struct DenseArgs {
     int64_t ldo;
     uint16_t* pre;         // [M, N] bf16
     int act, out_f32, vec;  // vec: N, strides and pointers allow four elements at a time
-    int past;               // 256-column tiles store past the caches
+    int past;               // 256-column tiles of EPI_PLAIN store past the caches
     // EPI_PART: part[split][m][part_ld]
     float* part;
     int64_t part_ld;
