@@ -171,8 +171,10 @@ class MoELayerPlan:
 
     on preallocated buffers: a LinearPlan, a TrainPlan and a GatedFFNPlan whose
     sums ride in the products' epilogues (the shared expert adds the routed
-    experts' y, the data gradients add up in turn).  act8: what the backward needs
-    of the shared expert, x and [G, U], is kept in 8 bits (fs % 128 == 0).
+    experts' y, the data gradients add up in turn).  act8: x and the shared expert's
+    [G, U] are kept in 8 bits for the backward (fs % 128 == 0), 1.03 bytes per
+    value.  The router's dWr and the shared expert's dW13s are then products with x
+    as restored from them (``xr``, valid after a backward until the next call).
     Needs every expert on this GPU (L == E): under expert parallelism d_logits
     has to be summed over the GPUs between the parts."""
 
@@ -186,7 +188,9 @@ class MoELayerPlan:
         if act8:
             self.x8 = (torch.empty((T, d), dtype=torch.int8, device=dv),
                        torch.empty(((d + 127) // 128, T), dtype=torch.float32, device=dv))
-            self.xr = torch.empty((T, d), dtype=BF16, device=dv)
+            # x is restored where the routed experts' backward, done by then, had the
+            # gradients of its rows (at least T): no memory of its own
+            self.xr = self.routed.dX[:T]
 
     def forward(self, x, Wr, wts, W13s, W2s, br=None):
         """y [T, d]; wts from quantize_weights (with its transposed copies where
@@ -203,9 +207,9 @@ class MoELayerPlan:
         router_bias), dW13 and dW2 (routed experts), dW13s and dW2s.  With act8,
         x is not read (None will do)."""
         with _Device(self.router.device):
+            dx, dW13, dW2, d_logits = self.routed.backward(x, dy, wts)  # (x is in its own 8-bit copies)
             if self.x8 is not None:
                 x = ops.act_restore(*self.x8, out=self.xr)
-            dx, dW13, dW2, d_logits = self.routed.backward(x, dy, wts)
             dx, dWr, dbr = self.router.backward(d_logits, x, Wr, dx_add=dx)
             dx, dW13s, dW2s, _, _ = self.shared.backward(dy, x, W13s, W2s, dx_add=dx)
         return dict(dx=dx, dWr=dWr, dbr=dbr, dW13=dW13, dW2=dW2, dW13s=dW13s, dW2s=dW2s)
