@@ -452,6 +452,16 @@ enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_INT8 = 2 };
  * device's compute units).  Calls that share a workspace must not overlap.
  * Outputs overlap no input, workspace or other output, but where it is said.  */
 
+/* The kernel that a product of M x N results over K takes on the current device
+ * (the choice is by estimated time), and in how many pieces K is summed by a second
+ * launch (0: none). FORWARD: moe_linear, and y of moe_gated_ffn; GATED: [G, U]
+ * (N = 2f); GRADIENT: dh, dx, dW (M x N = T x K or N x K), where they are not grouped.
+ * For tests and measurement.                                                  */
+enum { MOE_PRODUCT_FORWARD = 0, MOE_PRODUCT_GATED = 1, MOE_PRODUCT_GATED_INT8 = 2, MOE_PRODUCT_GRADIENT = 3 };
+enum { MOE_DENSE_THIN = 0, MOE_DENSE_SLAB = 1, MOE_DENSE_SMALL = 2, MOE_DENSE_TILES = 3, MOE_DENSE_HALF = 4,
+       MOE_DENSE_WIDE = 5 };
+int moe_dense_kernel(int64_t M, int64_t N, int64_t K, int32_t product, int32_t* kernel, int32_t* pieces);
+
 /* out[t, n] = act(sum_k x[t, k] W[n, k] + bias[n]) + residual[t, n]
  *   x [T, K] bf16 (stride ldx), W [N, K] bf16 (ldw), bias [N] bf16 or NULL,
  *   residual [T, N] bf16 (ldr) or NULL, out [T, N] (ldo) bf16 (out_type

@@ -1116,7 +1116,14 @@ __global__ __launch_bounds__(128) void dense_sum_kernel(DenseArgs g, int splits)
 
 // ---------------------------------------------------------------- host side
 namespace {
-enum Kind { THIN, SLAB, SMALL, TILES, HALF, WIDE };
+enum Kind {
+    THIN = MOE_DENSE_THIN,
+    SLAB = MOE_DENSE_SLAB,
+    SMALL = MOE_DENSE_SMALL,
+    TILES = MOE_DENSE_TILES,
+    HALF = MOE_DENSE_HALF,
+    WIDE = MOE_DENSE_WIDE
+};
 struct Shape {
     Kind kind;
     int64_t mt, nt;
@@ -1556,3 +1563,20 @@ int zero16_launch(uint16_t* p, int64_t n, hipStream_t stream) {
 }
 
 }  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_dense_kernel(int64_t M, int64_t N, int64_t K, int32_t product, int32_t* kernel, int32_t* pieces) {
+    clear_error();
+    MOE_REQUIRE(kernel && pieces, MOE_ERR_NULL, "kernel or pieces is NULL");
+    MOE_REQUIRE(product >= MOE_PRODUCT_FORWARD && product <= MOE_PRODUCT_GRADIENT, MOE_ERR_UNSUPPORTED,
+                "unknown product %d", product);
+    MOE_REQUIRE(M >= 1 && M <= (1 << 30) && N >= 1 && N <= (1 << 20) && K >= 1 && K <= (1 << 30), MOE_ERR_SHAPE,
+                "M=%lld, N=%lld, K=%lld: at least 1, at most 2^30, 2^20 and 2^30", (long long)M, (long long)N, (long long)K);
+    constexpr int EPIS[] = {EPI_LINEAR, EPI_GATE, EPI_GATE8, EPI_LINEAR};
+    const int side = product == MOE_PRODUCT_GRADIENT ? OP_KS : OP_KC;
+    const Shape s = dense_shape(M, N, K, OP_KC, side, EPIS[product]);
+    *kernel = s.kind;
+    *pieces = s.pieces ? s.splits : 0;
+    return MOE_OK;
+}

@@ -24,6 +24,8 @@ GEMM_THIN_SPLIT = 0x1000  # thin last 288-row m-tiles of a SwiGLU product split 
 SRC_BF16, SRC_F32 = 0, 1
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}  # MOE_ACT_*
 SAVES = {"none": 0, "bf16": 1, "int8": 2}  # MOE_SAVE_*
+DENSE_PRODUCTS = {"forward": 0, "gated": 1, "gated_int8": 2, "gradient": 3}  # MOE_PRODUCT_*
+DENSE_KERNELS = ("thin", "slab", "small", "tiles", "half", "wide")           # MOE_DENSE_*
 FLAG_BAD_ID, FLAG_DUP_ID, FLAG_ROW_CAP = 1, 2, 4
 ROW_ALIGN = 128
 
@@ -75,6 +77,7 @@ _SIGS = {
     "moe_linear_backward_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "moe_linear_backward": (ctypes.c_int, [_P, _I32, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _P, _P,
                                            _P, _SZ, _P]),
+    "moe_dense_kernel": (ctypes.c_int, [_I64, _I64, _I64, _I32, ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
     "moe_linear_backward_grouped": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _I32, _I32, _I32,
                                                    ctypes.POINTER(_I32)]),
     "moe_gated_ffn_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
@@ -532,6 +535,14 @@ def launch(name, dev, *args):
     rc = getattr(lib(), name)(*args, _raw_stream(dev.index))
     if rc != 0:
         raise MoeError(name, rc, last_error())
+
+
+def dense_kernel(M, N, K, product="forward"):
+    """(name of the kernel, pieces of K or 0) that a dense product of M x N
+    results over K takes on the current device."""
+    kind, pieces = _I32(0), _I32(0)
+    _call("moe_dense_kernel", M, N, K, DENSE_PRODUCTS[product], ctypes.byref(kind), ctypes.byref(pieces))
+    return DENSE_KERNELS[kind.value], pieces.value
 
 
 def rows_of(t, shape, dtype, name, dev=None):

@@ -47,3 +47,25 @@ def test_grouped_refusals():
     assert lib.moe_linear_backward_grouped(4, 64, 63, 0, 0, 1, 1, 1, ctypes.byref(v)) == -2
     assert lib.moe_gated_ffn_backward_grouped(4, 64, 64, 1, 1, 1, 1, None) == -1
     assert lib.moe_gated_ffn_backward_grouped(4, 60, 64, 1, 1, 1, 1, ctypes.byref(v)) == -2
+
+
+def test_dense_kernel_answers():
+    assert ops.dense_kernel(1, 256, 7168) == ("thin", 0)
+    assert ops.dense_kernel(48, 256, 7168)[0] == "slab"
+    assert ops.dense_kernel(4, 256, 64, "gated_int8")[0] == "slab"
+    for product in ("forward", "gated", "gradient"):
+        assert ops.dense_kernel(16384, 4096, 7168, product) == ("wide", 0)
+    # the pieces' workspace is what the choice says
+    for T, N, K in ((100, 256, 7168), (8192, 256, 7168), (203, 1001, 520), (1237, 776, 3080)):
+        n = ops.workspace_bytes("moe_linear_workspace", T, N, K)
+        assert n == ops.dense_kernel(T, N, K)[1] * T * ((N + 3) // 4 * 4) * 4
+
+
+def test_dense_kernel_refusals():
+    lib, a, b = ops.lib(), ctypes.c_int32(0), ctypes.c_int32(0)
+    f = lambda *s, k=ctypes.byref(a), p=ctypes.byref(b): lib.moe_dense_kernel(*s, k, p)
+    assert f(1, 1, 1, 0) == 0
+    assert f(1, 1, 1, 0, k=None) == -1 and f(1, 1, 1, 0, p=None) == -1
+    assert f(1, 1, 1, 4) == -3 and f(1, 1, 1, -1) == -3
+    for s in ((0, 1, 1), (1, 0, 1), (1, 1, 0), ((1 << 30) + 1, 1, 1), (1, (1 << 20) + 1, 1), (1, 1, (1 << 30) + 1)):
+        assert f(*s, 0) == -2

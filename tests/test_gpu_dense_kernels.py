@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import dense_ref
+import test_gpu_dense
 from dense_ref import U16, acc_err, close, d64
 from gpu_util import DEV, say
 from moe_expert_layer_r3_amd import ops
@@ -45,3 +46,105 @@ def test_large_data_gradient_with_and_without_the_weights(T, K, N):
     ref = D.t() @ X
     e = acc_err(T, D.t(), X)
     close(p.dW, ref, e + U16 * (ref.abs() + e), "dW")
+
+
+# ---------------------------------------------------------------- every kernel's every form
+# sizes with remainders along M, N and K whose products take the named kernel, K whole
+# or in pieces that a second launch adds up
+
+SIZES = [("small", False, 129, 8, 8), ("small", True, 129, 8, 2056), ("tiles", False, 1500, 4104, 136),
+         ("tiles", True, 7001, 264, 1544), ("half", False, 3081, 1288, 520), ("half", True, 1237, 776, 3080),
+         ("wide", False, 2049, 4104, 776), ("wide", True, 12003, 136, 3080)]
+
+
+def takes(kernel, pieces, M, N, K, product):
+    name, n = ops.dense_kernel(M, N, K, product)
+    assert (name, n > 0) == (kernel, pieces), (name, n)
+
+
+@pytest.mark.parametrize("kernel, pieces, M, N, K", SIZES)
+@pytest.mark.parametrize("form", ["plain", "vec", "odd"])
+def test_forward_forms(kernel, pieces, M, N, K, form):
+    """plain: bf16 of sum, bias and residual; vec: the same with an activation, its
+    argument saved, four columns at a time; odd: fp32 out of an odd number of columns."""
+    N = N - 3 if form == "odd" else N
+    takes(kernel, pieces, M, N, K, "forward")
+    name = "none" if form == "plain" else "gelu"
+    if form != "odd":
+        test_gpu_dense.check_linear(M, K, N, name, False, True, True, form == "vec", pad=8)
+    else:
+        test_gpu_dense.check_linear(M, K, N, name, True, True, True, False)
+        test_gpu_dense.check_linear(M, K, N, "none", True, False, False, False, pad=8)
+
+
+@pytest.mark.parametrize("kernel, pieces, M, N, K", SIZES)
+def test_gradient_forms(kernel, pieces, M, N, K):
+    """dx [M, N] = dy [M, K] W [K, N] and dW [M, N] = dy [K, M]^T x [K, N], each alone."""
+    takes(kernel, pieces, M, N, K, "gradient")
+    say(f"gradients {kernel} pieces={pieces} M={M} N={N} K={K}")
+    ptr = lambda t: None if t is None else t.data_ptr()
+
+    def run(T, cols, sums, dx, dW, dy, x, W, add):
+        n = ops.workspace_bytes("moe_linear_backward_workspace", T, sums, cols)
+        ws = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+        ops.launch("moe_linear_backward", dy.device, ptr(dy), 0, None, ptr(x), 0 if x is None else x.stride(0), ptr(W),
+                   0 if W is None else W.stride(0), ptr(add), T, sums, cols, 0, ptr(dx), ptr(dW), None, ptr(ws), ws.numel())
+
+    dy, W, add = normal((M, K), 1), normal((K, N), 2, 0.1, pad=8), normal((M, N), 3)
+    out = torch.full((M + 1, N), 5.0, dtype=BF, device=DEV)
+    run(M, N, K, out, None, dy, None, W, add)
+    D, Wd = d64(dy), d64(W)
+    ref = D @ Wd + d64(add)
+    e = acc_err(K, D, Wd) + (K + 8) * 2.0 ** -24 * d64(add).abs()
+    close(out[:M], ref, e + U16 * (ref.abs() + e) + 1e-30, "dx")
+    assert (out[M] == 5).all()
+
+    # (M odd: dy is copied to rows of whole 16 bytes first)
+    dy, x = normal((K, M), 4), normal((K, N), 5, pad=8)
+    out.fill_(5)
+    run(K, N, M, None, out, dy, x, None, None)
+    D, X = d64(dy).t(), d64(x)
+    ref = D @ X
+    e = acc_err(K, D, X)
+    close(out[:M], ref, e + U16 * (ref.abs() + e) + 1e-30, "dW")
+    assert (out[M] == 5).all()
+
+
+@pytest.mark.parametrize("kernel, pieces, T, f, d", [
+    ("small", False, 129, 8, 8), ("small", True, 129, 8, 2056), ("tiles", False, 1500, 2056, 136),
+    ("tiles", True, 1803, 648, 2056), ("half", False, 3081, 648, 520), ("half", True, 1237, 392, 3080),
+    ("wide", False, 2049, 2056, 776), ("wide", True, 12003, 72, 3080)])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_gated_forms(kernel, pieces, T, f, d, name):
+    """[G, U] of moe_gated_ffn, saved in bf16, with biases and without."""
+    takes(kernel, pieces, T, 2 * f, d, "gated")
+    test_gpu_dense.check_ffn(T, d, f, name, "bf16", name == "silu", True, pad=8)
+
+
+@pytest.mark.parametrize("kernel, pieces, T, f, d", [
+    ("small", True, 129, 128, 392), ("tiles", False, 129, 128, 8), ("tiles", True, 771, 640, 1544),
+    ("half", False, 1803, 1280, 392), ("half", True, 771, 1280, 1544), ("wide", False, 2049, 2176, 776),
+    ("wide", True, 129, 4224, 7176)])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_gated_int8_forms(kernel, pieces, T, f, d, name):
+    """The same saved in 8 bits."""
+    takes(kernel, pieces, T, 2 * f, d, "gated_int8")
+    test_gpu_dense.check_ffn(T, d, f, name, "int8", name == "gelu", True)
+
+
+@pytest.mark.parametrize("kernel, pieces, T, f, d", [
+    ("small", False, 129, 128, 8), ("small", True, 129, 128, 3080), ("tiles", False, 3081, 2176, 136),
+    ("tiles", True, 1237, 640, 7176), ("half", False, 2049, 2176, 520), ("half", True, 771, 1280, 3080),
+    ("wide", False, 2049, 4224, 776), ("wide", True, 2049, 2176, 3080)])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+@pytest.mark.parametrize("save", ["bf16", "int8"])
+def test_dgated_forms(kernel, pieces, T, f, d, name, save):
+    """dh with [dG, dU] and h formed on it, seen in all gradients."""
+    takes(kernel, pieces, T, f, d, "gradient")
+    test_gpu_dense.check_ffn(T, d, f, name, save, True, False)
+
+
+@pytest.mark.parametrize("M, N, K, product", [(1, 256, 7168, "forward"), (4, 64, 64, "gated")])
+def test_few_rows(M, N, K, product):
+    assert ops.dense_kernel(M, N, K, product) == ("thin", 0)
+    assert ops.dense_kernel(5, N, K, product)[0] == "slab" and ops.dense_kernel(128, N, K, product)[0] == "slab"
