@@ -440,9 +440,10 @@ enum { MOE_SAVE_NONE = 0, MOE_SAVE_BF16 = 1, MOE_SAVE_INT8 = 2 };
 
 /* Shared rules of the functions below.  Matrices are row-major; a row stride ld
  * (elements) is at least the row's length and at most 2^22, and a multiple of 8
- * where the matrix is an operand of a product; operand and gradient pointers are
+ * where the matrix is an operand of a product; operand and gradient pointers (and
+ * pre in moe_linear_backward, biases, residual, outputs and gu of moe_gated_ffn) are
  * 16-byte aligned (rows are moved in 16-byte pieces). K, d and f are multiples
- * of 8, N is any number >= 1, all at most 2^20; 0 <= T <= 2^30. Products
+ * of 8, N is any number >= 1, all at most 2^20 (f: 2^19); 0 <= T <= 2^30. Products
  * are bf16 x bf16 accumulated in fp32 (matrix instructions); a long K may be
  * summed in several fp32 pieces added in a fixed order. A NaN or infinity in a
  * row of x (or W) reaches that row (column) of the result only.
@@ -477,7 +478,8 @@ int moe_linear(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, c
                void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Gradients of moe_linear. With dz[t, n] = dy[t, n] * act'(pre[t, n]) (rounded
- * to bf16 for the products; dy itself is the residual's gradient):
+ * to bf16 for the products dx and dW, from an fp32 dy too; dbias sums it as it is
+ * before; dy itself is the residual's gradient):
  *     dx[t, k] = sum_n dz[t, n] W[n, k] + dx_add[t, k]
  *     dW[n, k] = sum_t dz[t, n] x[t, k]      dbias[n] = sum_t dz[t, n]
  *   dy [T, N] dense, bf16 or fp32 (dy_type); pre as saved (NULL for
@@ -516,6 +518,7 @@ int moe_gated_ffn(const uint16_t* x, int64_t ldx, const uint16_t* W13, const uin
  *     dh = dy W2,  dG = dh * U * act'(G),  dU = dh * act(G)   (one kernel; dh
  *                                      stays in fp32, [dG, dU] is rounded to bf16)
  *     dx = [dG, dU] W13 + dx_add       dW13 = [dG, dU]^T x     db13 = sum_t [dG, dU]
+ *                                      (all three of the rounded [dG, dU])
  *     dW2 = dy^T (act(G) * U)          db2 = sum_t dy
  *   dy [T, d], x [T, d] (ldx), dx_add as above; dx [T, d], dW13 [2f, d], dW2
  *   [d, f], db13 [2f], db2 [d] bf16 dense, each NULL to skip it; save, gu, gu_s

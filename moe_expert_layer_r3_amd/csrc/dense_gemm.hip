@@ -520,8 +520,9 @@ __global__ __launch_bounds__(256) void dense_group_kernel(DenseGroup g) {
 //
 // 16384 x 4096 over 7168 (gated, [G, U] saved) takes 654 us, 1.47 PFLOP/s; 16384 x 7168
 // over 2048 with a residual 408 us, as a data gradient over 4096 680 us (1.41), 4096 x
-// 7168 over 16384 as a weight gradient 699 us (1.38).  The clock is 1.77 GHz under
-// that load (power), the matrix cores are busy 62-68% of it; tiles' ends take the rest.
+// 7168 over 16384 as a weight gradient 699 us (1.38); another card is 7% slower on all.
+// The clock is 1.6 to 1.8 GHz under that load (power); the matrix cores are busy 76%
+// of the cycles in the first, 57, 67 and 61% in the others; tiles' ends take the rest.
 //
 // act: the activation of the gated epilogues at compile time (-1: at run time).
 constexpr bool is_direct(int epi, int act) {
@@ -1422,6 +1423,9 @@ Chunks colsum_chunks(int64_t T) {
 // dz = dy * act'(pre) of moe_linear_backward: bf16 rows of stride ldz (columns
 // past N zero) if dz is given, and fp32 column sums over chunks of rows (before
 // the rounding) if part is given.  One thread per four columns of a row.
+// dz is rounded, from fp32 dy too, since the products' operands are bf16: the rest as a
+// second bf16 term would double the products, for results that are rounded to bf16
+// themselves (they are about 1.4 times as far off as by that rounding alone).
 struct DzArgs {
     const void* dy;
     int dy_f32;

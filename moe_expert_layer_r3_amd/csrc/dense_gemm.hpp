@@ -372,7 +372,8 @@ __device__ __forceinline__ void epi_plain(const DenseArgs& g, int64_t m, int n, 
 }
 
 // EPI_DGATE for dh[m, n .. n + 3], m < M, n < f (f % 8 == 0): [dG, dU] and h from
-// the saved G, U
+// the saved G, U, rounded to bf16 as operands of the products behind (a second bf16
+// term of the rest would double those)
 template <int EPI>
 __device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, v4f dh, const EpiIn<EPI>& in) {
     float G[4], U[4];
@@ -402,7 +403,7 @@ __device__ __forceinline__ void epi_dgate(const DenseArgs& g, int64_t m, int n, 
 
 // EPI_GATE for the sums G, U[m, n .. n + 3]; `on`: m < M and n < f.  With the 8-bit
 // save (f % 128 == 0) 32 adjacent lanes hold one 128-column block of a row, and
-// every lane of a wave calls.
+// every lane of a wave calls.  h is rounded to bf16, the operand of y's product.
 __device__ __forceinline__ void epi_gate(const DenseArgs& g, int64_t m, int n, v4f G, v4f U,
                                          const EpiBias<EPI_GATE>& bias, bool on) {
     G += bias.a;

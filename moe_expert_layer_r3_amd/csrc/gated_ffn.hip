@@ -5,7 +5,10 @@
 //             columns in one wave, so that act, the product and the save of
 //             [G, U] run on the accumulators;  y = h W2^T + b2 + residual
 //   backward  dh = dy W2 with [dG, dU] and h formed on its accumulators (dh is
-//             never written);  dx, dW13, dW2 products;  bias column sums
+//             never written);  dx, dW13, dW2 products;  bias column sums, db13's
+//             over [dG, dU] as rounded for the products: fp32 values of them would
+//             have to be written and read again, 8 T f bytes more, for a sum whose
+//             terms' roundings (2^-9 of each on average) mostly cancel
 #include "dense_gemm.hpp"
 
 namespace moe {

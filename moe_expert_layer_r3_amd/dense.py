@@ -65,7 +65,8 @@ class LinearPlan:
 
     def backward(self, dy, x, W, dx_add=None):
         """(dx [T, K] + dx_add, dW [N, K], db [N] or None) of the last forward
-        for dy [T, N] of out's type (also the residual's gradient)."""
+        for dy [T, N] of out's type (also the residual's gradient).  dx and dW are
+        products of dy * act' rounded to bf16, from fp32 too."""
         if not self.train:
             raise ValueError("the plan was made without train=True")
         dv, T, K, N = self.device, self.T, self.K, self.N

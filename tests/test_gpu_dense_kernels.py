@@ -148,3 +148,32 @@ def test_dgated_forms(kernel, pieces, T, f, d, name, save):
 def test_few_rows(M, N, K, product):
     assert ops.dense_kernel(M, N, K, product) == ("thin", 0)
     assert ops.dense_kernel(5, N, K, product)[0] == "slab" and ops.dense_kernel(128, N, K, product)[0] == "slab"
+
+
+@pytest.mark.parametrize("T, K, N", [(1, 72, 30), (3, 136, 140), (4, 2056, 5000), (40, 136, 140), (128, 1032, 300),
+                                     (150, 136, 140), (1500, 136, 1032), (3081, 520, 1288), (2049, 776, 2056)])
+def test_nan_and_inf_stay_in_their_rows_and_columns(T, K, N):
+    """Each product of a linear layer with a NaN in one row of an operand and an
+    infinity in another: everything else has the bits it has without them."""
+    say(f"nan T={T} K={K} N={N}")
+    p = LinearPlan(T, K, N, train=True, device=DEV)
+    x, W, dy = normal((T, K), 1), normal((N, K), 2, 0.1), normal((T, N), 3)
+
+    def run():
+        return [t.clone() for t in (p.forward(x, W), *p.backward(dy, x, W)[:2])]
+
+    def others(t, dim, bad):
+        keep = torch.tensor([i for i in range(t.shape[dim]) if i not in bad], dtype=torch.long, device=DEV)
+        return t.index_select(dim, keep)
+
+    clean = run()
+    t0, n0, n1 = T - 1, N - 1, N // 2
+    x[t0, K - 1] = float("nan")      # out: row t0; dW: column K - 1
+    W[n0, 0] = float("nan")          # out: column n0; dx: column 0
+    dy[0, n1] = float("inf")         # dx: row 0; dW: row n1
+    out, dx, dW = run()
+    assert out[t0].isnan().all() and out[:, n0].isnan().all()
+    assert dx[:, 0].isnan().all() and not dx[0].isfinite().any()
+    assert dW[:, K - 1].isnan().all() and not dW[n1].isfinite().any()
+    for got, ref, rows, cols in ((out, clean[0], {t0}, {n0}), (dx, clean[1], {0}, {0}), (dW, clean[2], {n1}, {K - 1})):
+        assert torch.equal(others(others(got, 0, rows), 1, cols), others(others(ref, 0, rows), 1, cols))
