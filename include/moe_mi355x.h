@@ -64,6 +64,9 @@ typedef enum {
 
 enum { MOE_FLAG_BAD_ID = 1, MOE_FLAG_DUP_ID = 2, MOE_FLAG_ROW_CAP = 4 };
 
+/* Type of a matrix that comes in either. */
+enum { MOE_SRC_BF16 = 0, MOE_SRC_F32 = 1 };
+
 /* Rows of the expert-grouped layout are padded per expert to a multiple of this. */
 #define MOE_ROW_ALIGN 128
 
@@ -108,6 +111,82 @@ int moe_route_topk_capture(const float* logits, int64_t T, int32_t E, int32_t k,
 int moe_replay_load(const int32_t* rec, int32_t n_layers, int32_t k, int64_t seq_len,
                     int32_t layer, int64_t s0, int64_t T, const float* logits, int32_t E,
                     int32_t* ids, float* w, int32_t* dev_status, hipStream_t stream);
+
+/* ---- routing by scores ("RL at 1T scale", sections "Router Replay" and "Wide
+ * Expert Parallelism": the choice that is recorded and replayed, and the even
+ * load that experts spread over GPUs need) --------------------------------- */
+
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+/* Rules of the functions below.  logits [T, E] dense, fp32 (MOE_SRC_F32) or bf16
+ * (MOE_SRC_BF16). Scores of a token's logits l:
+ *     s_e = 1 / (1 + exp(-l_e))   or   exp(l_e) / sum over the row
+ * evaluated in 64 bits.  A logit of -inf or of its type's lowest value masks its
+ * expert: s_e = 0, and it counts in no sum.  A NaN or +inf makes its own sigmoid
+ * score NaN or 1, and every softmax score of its row NaN.
+ * Weights of the chosen experts id_j:
+ *     renorm != 0:  w_j = scale * s(id_j) / sum_i s(id_i), of the chosen logits
+ *                   alone (softmax scores: the softmax over them); 0 where
+ *                   all of them are masked or their scores are 0
+ *     renorm == 0:  w_j = scale * s(id_j)
+ * 0 <= T <= 2^30, 1 <= E <= 1024, 1 <= k <= min(16, E), scale finite.  T = 0 is
+ * a no-op.  logits and d_logits are 16-byte aligned.  MOE_ERR_SHAPE,
+ * MOE_ERR_UNSUPPORTED for unknown enum values.                                */
+
+/* Choice of k experts per token:
+ *     c_e = s_e (rounded to fp32) + bias_e        (fp32; bias NULL: c_e = s_e)
+ *           -inf for a masked expert; NaN comes after every number
+ *     groups > 1: the experts stand in `groups` groups of E / groups neighbours. A
+ *           group's value is the sum (fp32) of its group_top largest c above
+ *           -inf (fewer if it has no more; -inf if it has none).  The
+ *           top_groups groups of largest value stay, ties to the lower group.
+ *     ids[t, :] = the k largest c of the groups that stay, in descending order,
+ *           ties to the lower id
+ * and w [T, k] as above.  Only the choice sees the bias.
+ *   bias [E] fp32 or NULL; 1 <= groups <= 64, E % groups == 0,
+ *   1 <= top_groups <= groups, k <= top_groups * (E / groups), group_top 1 or 2.
+ *   load (NULL: none) int32 [E]: load[e] += the tokens that chose e.
+ *   rec (NULL: none): rec[layer, j, s0 + t] = ids[t, j] in the record
+ *   [n_layers, k, seq_len] int32 (0 <= layer < n_layers, s0 + T <= seq_len).   */
+int moe_route_scored(const void* logits, int32_t logits_type, int64_t T, int32_t E, int32_t k, int32_t score,
+                     const float* bias, int32_t groups, int32_t top_groups, int32_t group_top, int32_t renorm,
+                     float scale, int32_t* ids, float* w, int32_t* load, int32_t* rec, int32_t n_layers,
+                     int64_t seq_len, int32_t layer, int64_t s0, hipStream_t stream);
+
+/* Router Replay [R3] of such a choice: ids[t, j] = rec[layer, j, s0 + t] verbatim
+ * and w as above from this call's logits.  Ids outside [0, E) and repeated ids are
+ * treated and flagged as by moe_replay_load (dev_status may be NULL).          */
+int moe_replay_scored(const int32_t* rec, int32_t n_layers, int32_t k, int64_t seq_len, int32_t layer, int64_t s0,
+                      int64_t T, const void* logits, int32_t logits_type, int32_t E, int32_t score, int32_t renorm,
+                      float scale, int32_t* ids, float* w, int32_t* dev_status, hipStream_t stream);
+
+/* Gradient of the weights of moe_route_scored or moe_replay_scored (the choice
+ * itself has none):
+ *     sigmoid, renorm:    dl_j = w_j (1 - s_j) (d_w_j - sum_i d_w_i w_i / scale)
+ *     sigmoid:            dl_j = scale d_w_j s_j (1 - s_j)
+ *     softmax, renorm:    dl_j = w_j (d_w_j - sum_i d_w_i w_i / scale)
+ *     softmax:            dl_e = s_e (scale sum over {j: id_j = e} of d_w_j - sum_i d_w_i w_i)
+ * summed over the slots of an expert, 0 at the others.  A token with an id
+ * outside [0, E) gets 0.
+ *   d_w [T, k] fp32, logits as given to the forward, ids [T, k]; d_logits [T, E]
+ *   of logits' type.  scale = 0 counts as the limit (all gradients 0).          */
+int moe_route_scored_backward(const float* d_w, const void* logits, int32_t logits_type, const int32_t* ids, int64_t T,
+                              int32_t k, int32_t E, int32_t score, int32_t renorm, float scale, void* d_logits,
+                              hipStream_t stream);
+
+/* The same from the partials of moe_combine_backward_rows, as
+ * moe_gate_backward_parts takes them: d_gate [T, k] is written first.           */
+int moe_route_scored_backward_parts(const float* gate_part, const int32_t* pair_row, int64_t row_cap, int32_t d,
+                                    const void* logits, int32_t logits_type, const int32_t* ids, int64_t T, int32_t k,
+                                    int32_t E, int32_t score, int32_t renorm, float scale, float* d_gate,
+                                    void* d_logits, hipStream_t stream);
+
+/* Moves the choice's bias towards an even load:
+ *     bias_out[e] = bias[e] + step * sign(mean(load) - load[e])
+ * compared exactly (whole numbers); then load[e] = 0 if clear.  bias_out may be
+ * bias.  1 <= E <= 1024, step finite.                                          */
+int moe_balance_bias(int32_t* load, const float* bias, int32_t E, float step, int32_t clear, float* bias_out,
+                     hipStream_t stream);
 
 /* ---- dispatch (local permutation) [EP] ---------------------------------- */
 
@@ -167,7 +246,6 @@ int moe_permute_noalloc(const int32_t* ids, int64_t T, int32_t k, int32_t e0, in
 /* ---- block-scaled FP8 quantisation [FP8] -------------------------------- */
 
 enum { MOE_TILE_1x128 = 0, MOE_TILE_128x128 = 1 };
-enum { MOE_SRC_BF16 = 0, MOE_SRC_F32 = 1 };
 /* OR'ed into moe_quant_fp8's tile, moe_permute's quant_flags and
  * moe_grouped_gemm_fp8's epilogue: power-of-two (UE8M0) scales.  The scale of
  * a tile with a = max(max|v|, 2^-40) is s = 2^e, e the least integer with

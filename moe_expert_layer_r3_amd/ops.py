@@ -23,6 +23,7 @@ GEMM_B_KN = 0x800     # weights given as [L, K, N] (a dgrad product on the forwa
 GEMM_THIN_SPLIT = 0x1000  # thin last 288-row m-tiles of a SwiGLU product split along K (workspace in out3)
 SRC_BF16, SRC_F32 = 0, 1
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}  # MOE_ACT_*
+SCORES = {"softmax": 0, "sigmoid": 1}  # MOE_SCORE_*
 SAVES = {"none": 0, "bf16": 1, "int8": 2}  # MOE_SAVE_*
 DENSE_PRODUCTS = {"forward": 0, "gated": 1, "gated_int8": 2, "gradient": 3}  # MOE_PRODUCT_*
 DENSE_KERNELS = ("thin", "slab", "small", "tiles", "half", "wide")           # MOE_DENSE_*
@@ -42,6 +43,7 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_F32 = ctypes.c_float
 
 _SIGS = {
     "moe_last_error": (ctypes.c_char_p, []),
@@ -49,6 +51,14 @@ _SIGS = {
     "moe_route_topk": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P]),
     "moe_route_topk_capture": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _P, _I32, _I64, _I32, _I64, _P]),
     "moe_replay_load": (ctypes.c_int, [_P, _I32, _I32, _I64, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _P]),
+    "moe_route_scored": (ctypes.c_int, [_P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, _F32, _P, _P, _P, _P,
+                                        _I32, _I64, _I32, _I64, _P]),
+    "moe_replay_scored": (ctypes.c_int, [_P, _I32, _I32, _I64, _I32, _I64, _I64, _P, _I32, _I32, _I32, _I32, _F32, _P, _P,
+                                         _P, _P]),
+    "moe_route_scored_backward": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _P]),
+    "moe_route_scored_backward_parts": (ctypes.c_int, [_P, _P, _I64, _I32, _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _F32,
+                                                       _P, _P, _P]),
+    "moe_balance_bias": (ctypes.c_int, [_P, _P, _I32, _F32, _I32, _P, _P]),
     "moe_permute_workspace": (ctypes.c_int, [_I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "moe_permute": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, _I64, _P, _P, _P, _P,
                                    _P, _I32, _P, _P, _P, _I32, _P, _SZ, _P, _P]),
@@ -503,6 +513,129 @@ def combine_backward(dy, y_perm, pair_row, w, rcap=None, quant=True, pow2=False)
     _call("moe_combine_backward", _p(dy), _p(y_perm), _p(pair_row), _p(w), T, k, d, rcap, _p(dyq), _p(dys),
           _p(d_gate), _flag(pow2), _stream(dev))
     return dyq, dys, d_gate
+
+
+# ---------------------------------------------------------------- routing by scores
+
+SRC_TYPES = {torch.bfloat16: SRC_BF16, torch.float32: SRC_F32}
+
+
+class Scoring:
+    """How experts are chosen and weighted: score "softmax" or "sigmoid"; groups
+    neighbouring experts each, of which the top_groups with the largest sums of
+    their group_top best stay; weights over their sum if renorm, times scale."""
+
+    def __init__(self, score="sigmoid", groups=1, top_groups=1, group_top=2, renorm=True, scale=1.0):
+        if score not in SCORES:
+            raise ValueError(f"unknown score {score!r}: one of {', '.join(SCORES)}")
+        self.score, self.groups, self.top_groups, self.group_top = score, groups, top_groups, group_top
+        self.renorm, self.scale = bool(renorm), float(scale)
+        self.code = SCORES[score]
+
+    def choice(self):
+        """The choice's arguments as the C entry point takes them."""
+        return self.groups, self.top_groups, self.group_top, self.renorm, self.scale
+
+
+def _logits_type(t, what="logits"):
+    if t.dtype not in SRC_TYPES:
+        raise TypeError(f"{what}: bf16 or fp32, got {t.dtype}")
+    return SRC_TYPES[t.dtype]
+
+
+def record_args(rec, layer, s0, k, dev):
+    """The record's arguments of a C entry point: pointer, layers, length, layer, first token."""
+    if rec.dim() != 3 or rec.shape[1] != k:
+        raise ValueError(f"record: expected [layers, {k}, tokens], got {tuple(rec.shape)}")
+    _dense(rec, rec.shape, torch.int32, "record", dev)
+    return rec.data_ptr(), rec.shape[0], rec.shape[2], layer, s0
+
+
+def route_scored(logits, k, scoring, bias=None, load=None, capture=None, out=None):
+    """(ids int32 [T, k], w fp32 [T, k]) chosen from logits [T, E] (fp32 or bf16).
+
+    bias fp32 [E] moves the choice only; load int32 [E] counts on; capture =
+    (rec [NL, k, S] int32, layer, s0) also records the ids; ``out`` = (ids, w)
+    receives them without allocating."""
+    lt = _logits_type(logits)
+    T, E = logits.shape
+    dev = _dev(logits)
+    _dense(logits, (T, E), logits.dtype, "logits", dev)
+    if bias is not None:
+        _dense(bias, (E,), torch.float32, "bias", dev)
+    if load is not None:
+        _dense(load, (E,), torch.int32, "load", dev)
+    ids, w = _ids_w(out, T, k, dev)
+    rec = (None, 0, 0, 0, 0) if capture is None else record_args(*capture, k, dev)
+    launch("moe_route_scored", dev, logits.data_ptr(), lt, T, E, k, scoring.code, None if bias is None else bias.data_ptr(),
+           *scoring.choice(), ids.data_ptr(), w.data_ptr(), None if load is None else load.data_ptr(), *rec)
+    return ids, w
+
+
+def replay_scored(rec, layer, s0, logits, scoring, status=None, out=None):
+    """Router Replay: ids = rec[layer, :, s0:s0+T].T and their weights from logits [T, E]."""
+    lt = _logits_type(logits)
+    T, E = logits.shape
+    dev = _dev(logits)
+    _dense(logits, (T, E), logits.dtype, "logits", dev)
+    k = rec.shape[1]
+    p, NL, S, layer, s0 = record_args(rec, layer, s0, k, dev)
+    if status is not None:
+        _dense(status, (1,), torch.int32, "status", dev)
+    ids, w = _ids_w(out, T, k, dev)
+    launch("moe_replay_scored", dev, p, NL, k, S, layer, s0, T, logits.data_ptr(), lt, E, scoring.code, scoring.renorm,
+           scoring.scale, ids.data_ptr(), w.data_ptr(), None if status is None else status.data_ptr())
+    return ids, w
+
+
+def _ids_w(out, T, k, dev):
+    if out is None:
+        return (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev))
+    return _dense(out[0], (T, k), torch.int32, "ids", dev), _dense(out[1], (T, k), torch.float32, "w", dev)
+
+
+def route_scored_backward(d_w, logits, ids, scoring, out=None):
+    """d_logits [T, E] of logits' type for d_w fp32 [T, k]."""
+    lt = _logits_type(logits)
+    T, E = logits.shape
+    dev = _dev(logits)
+    _dense(logits, (T, E), logits.dtype, "logits", dev)
+    k = ids.shape[1]
+    _dense(ids, (T, k), torch.int32, "ids", dev)
+    _dense(d_w, (T, k), torch.float32, "d_w", dev)
+    out = torch.empty_like(logits) if out is None else _dense(out, (T, E), logits.dtype, "d_logits", dev)
+    launch("moe_route_scored_backward", dev, d_w.data_ptr(), logits.data_ptr(), lt, ids.data_ptr(), T, k, E, scoring.code,
+           scoring.renorm, scoring.scale, out.data_ptr())
+    return out
+
+
+def route_scored_backward_parts(gate_part, pair_row, rcap, d, logits, ids, scoring):
+    """(d_gate [T, k], d_logits [T, E]) from the partials of combine_backward_rows."""
+    lt = _logits_type(logits)
+    T, E = logits.shape
+    dev = _dev(logits)
+    _dense(logits, (T, E), logits.dtype, "logits", dev)
+    k = ids.shape[1]
+    _dense(ids, (T, k), torch.int32, "ids", dev)
+    _dense(pair_row, (T, k), torch.int32, "pair_row", dev)
+    _dense(gate_part, (rcap, GATE_PARTS), torch.float32, "gate_part", dev)
+    d_gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+    out = torch.empty_like(logits)
+    launch("moe_route_scored_backward_parts", dev, gate_part.data_ptr(), pair_row.data_ptr(), rcap, d, logits.data_ptr(), lt,
+           ids.data_ptr(), T, k, E, scoring.code, scoring.renorm, scoring.scale, d_gate.data_ptr(), out.data_ptr())
+    return d_gate, out
+
+
+def balance_bias(load, bias, step, out=None, clear=True):
+    """bias + step * sign(mean(load) - load) for int32 load [E] (set to 0 if
+    clear), fp32 bias [E]; ``out`` may be bias itself."""
+    dev = _dev(load)
+    E = load.numel()
+    _dense(load, (E,), torch.int32, "load", dev)
+    _dense(bias, (E,), torch.float32, "bias", dev)
+    out = torch.empty_like(bias) if out is None else _dense(out, (E,), torch.float32, "out", dev)
+    launch("moe_balance_bias", dev, load.data_ptr(), bias.data_ptr(), E, step, bool(clear), out.data_ptr())
+    return out
 
 
 # ---------------------------------------------------------------- activations in 8 bits

@@ -1,0 +1,313 @@
+"""Routing by scores on the GPU against plain 64-bit forms: ids equal, weights
+and gradients within the bounds scores_ref derives."""
+
+import numpy as np
+import pytest
+import torch
+
+import scores_ref as R
+from gpu_util import DEV, np64, npi, say
+from moe_expert_layer_r3_amd import ops
+from moe_expert_layer_r3_amd.block import RoutePlan
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def make(T, E, seed, kind="f32", special=""):
+    rng = np.random.default_rng(seed)
+    l = rng.standard_normal((T, E)) * 1.3
+    if special == "ties":
+        l = np.round(l)
+    elif special == "saturated":      # sigmoid scores that round to 1, to 0 and to subnormal values
+        l = rng.choice([20.0, 40.0, 90.0, 800.0, -90.0, -100.0, -103.9, -800.0, 0.5], size=(T, E))
+    elif special == "masked":
+        l[rng.random((T, E)) < 0.4] = -np.inf
+        l[rng.random((T, E)) < 0.2] = R.LOWEST[kind]
+        l[::5] = -np.inf              # rows with nothing left
+        l[1::7] = R.LOWEST[kind]
+        l[2::7, 1:] = -np.inf         # rows with one expert left
+    elif special == "nan":
+        l[rng.random((T, E)) < 0.1] = np.nan
+        l[rng.random((T, E)) < 0.1] = -np.inf
+        l[::6, 0] = np.inf
+        l[3] = np.nan
+    elif special == "zeros":
+        l[:] = np.where(rng.random((T, E)) < 0.5, 0.0, -0.0)
+    return torch.tensor(l).to(TYPES[kind]).to(DEV)
+
+
+def close(got, ref, tol, what):
+    g = np64(got)
+    assert np.array_equal(np.isnan(g), np.isnan(ref)), what + ": NaN elsewhere"
+    bad = ~(np.abs(g - ref) <= tol) & ~np.isnan(ref)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(bad, np.abs(g - ref) / np.maximum(tol, 1e-300), 0)), g.shape)
+        raise AssertionError(f"{what}: {bad.sum()} of {bad.size} outside, at {i}: got {g[i]!r}, want {ref[i]!r} +- {tol[i]:.3g}")
+
+
+def check_route(T, E, k, score, kind="f32", special="", bias=False, groups=1, top_groups=1, group_top=2, renorm=True,
+                scale=1.0, seed=0, train=True):
+    say(f"route T={T} E={E} k={k} {score} {kind} {special} bias={bias} groups={groups}/{top_groups}/{group_top} "
+        f"renorm={renorm} scale={scale}")
+    lg = make(T, E, 100 + seed, kind, special)
+    b = None
+    if bias:
+        b = torch.tensor(np.random.default_rng(7 + seed).standard_normal(E).astype(np.float32) * 0.1).to(DEV)
+    sc = ops.Scoring(score, groups=groups, top_groups=top_groups, group_top=group_top, renorm=renorm, scale=scale)
+    plan = RoutePlan(T, E, k, sc, logits_dtype=TYPES[kind], train=train, device=DEV)
+    load = torch.full((E,), 5, dtype=torch.int32, device=DEV)
+    rec = torch.full((3, k, T + 9), -7, dtype=torch.int32, device=DEV)
+    ids, w = plan.forward(lg, bias=b, load=load, capture=(rec, 1, 4))
+    l = np64(lg)
+    s = R.scores(l, kind, score)
+    ref = R.choice(l, s, kind, k, None if b is None else npi(b), groups, top_groups, group_top)
+    assert np.array_equal(npi(ids), ref), "ids"
+    rw, _ = R.weights(l, s, kind, ref, score, renorm, scale)
+    close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"] + 2.0 ** -46 * abs(scale) * (rw != 0), "w")
+    want = np.full((3, k, T + 9), -7, dtype=np.int32)
+    want[1, :, 4:4 + T] = ref.T
+    assert np.array_equal(npi(rec), want), "record"
+    assert np.array_equal(npi(load), 5 + np.bincount(ref.ravel(), minlength=E)), "load"
+    if train and special not in ("nan",):
+        d_w = torch.tensor(np.random.default_rng(9 + seed).standard_normal((T, k)).astype(np.float32)).to(DEV)
+        got = plan.backward(d_w, lg)
+        g, size = R.gradient(l, s, kind, ref, np64(d_w), score, renorm, scale)
+        close(got, g, R.ROUND[kind] * np.abs(g) + R.TINY[kind] + 2.0 ** -46 * size, "d_logits")
+    # the record replayed gives the same weights, bit for bit
+    i2, w2 = RoutePlan(T, E, k, sc, logits_dtype=TYPES[kind], device=DEV).replay(rec, 1, 4, lg)
+    assert torch.equal(i2, ids)
+    assert torch.equal(w2.view(torch.int32), w.view(torch.int32)) or special == "nan", "replayed weights"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups,group_top", [
+    (1, 256, 8, 8, 4, 2), (1, 8, 2, 1, 1, 2), (129, 256, 8, 8, 4, 2), (33, 256, 8, 1, 1, 2), (67, 60, 6, 5, 2, 1),
+    (40, 160, 6, 8, 3, 1), (9, 1, 1, 1, 1, 1), (21, 16, 16, 1, 1, 2), (30, 64, 16, 4, 1, 2), (12, 1024, 16, 64, 7, 2),
+    (17, 1000, 9, 10, 3, 2), (50, 384, 8, 1, 1, 2), (26, 131, 5, 1, 1, 2), (35, 128, 4, 64, 64, 2), (44, 512, 8, 16, 4, 2),
+    (31, 48, 8, 48, 48, 1), (28, 24, 7, 12, 5, 2), (64, 257, 10, 1, 1, 2), (19, 260, 3, 2, 1, 2),
+])
+def test_route(score, renorm, kind, T, E, k, groups, top_groups, group_top):
+    check_route(T, E, k, score, kind=kind, bias=(T + E) % 2 == 0, groups=groups, top_groups=top_groups, group_top=group_top,
+                renorm=renorm, scale=2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("special", ["ties", "saturated", "masked", "nan", "zeros"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top", [
+    (256, 8, 8, 4, 2), (256, 8, 1, 1, 2), (60, 6, 5, 2, 1), (24, 12, 4, 2, 2), (600, 16, 3, 2, 2), (64, 8, 1, 1, 2),
+])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_special(special, score, E, k, groups, top_groups, group_top, bias):
+    check_route(71, E, k, score, special=special, bias=bias, groups=groups, top_groups=top_groups, group_top=group_top,
+                renorm=not bias, scale=1.5)
+    check_route(71, E, k, score, kind="bf16", special=special, bias=bias, groups=groups, top_groups=top_groups,
+                group_top=group_top, renorm=bias)
+
+
+def test_bias_of_infinity_and_nan():
+    T, E, k = 20, 64, 8
+    lg = make(T, E, 5)
+    b = torch.zeros(E, device=DEV)
+    b[3], b[5], b[7] = float("inf"), float("-inf"), float("nan")
+    ids, w = ops.route_scored(lg, k, ops.Scoring("sigmoid"), bias=b)
+    l = np64(lg)
+    s = R.scores(l, "f32", "sigmoid")
+    ref = R.choice(l, s, "f32", k, npi(b))
+    assert np.array_equal(npi(ids), ref) and (ref[:, 0] == 3).all()
+    rw, _ = R.weights(l, s, "f32", ref, "sigmoid", True, 1.0)
+    close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"], "w")
+
+
+def test_close_scores_are_ordered_as_rounded():
+    """Logits a few ulps apart: scores that round to the same value tie by id, others do not."""
+    E, T, k = 256, 64, 8
+    rng = np.random.default_rng(3)
+    l = np.float32(1.0) + rng.integers(0, 40, size=(T, E)).astype(np.float32) * np.float32(2.0 ** -23)
+    lg = torch.tensor(l).to(DEV)
+    for score in ("sigmoid", "softmax"):
+        for groups, top in ((1, 1), (8, 4)):
+            sc = ops.Scoring(score, groups=groups, top_groups=top)
+            b = torch.tensor(rng.integers(-3, 3, size=E).astype(np.float32) * np.float32(2.0 ** -24)).to(DEV)
+            for bias in (None, b):
+                ids, _ = ops.route_scored(lg, k, sc, bias=bias)
+                s = R.scores(l.astype(np.float64), "f32", score)
+                ref = R.choice(l.astype(np.float64), s, "f32", k, None if bias is None else npi(b), groups, top, 2)
+                assert np.array_equal(npi(ids), ref), (score, groups, bias is None)
+
+
+def test_many_tokens():
+    """More tokens than one pass of the grid takes, offsets past 2^31: the last rows are right."""
+    T, E, k = (1 << 22) + 4097, 520, 8
+    say(f"route T={T} E={E}")
+    tail = 300
+    lg = torch.randn((T, E), device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    plan = RoutePlan(T, E, k, ops.Scoring("sigmoid", groups=4, top_groups=2), train=True, device=DEV)
+    ids, w = plan.forward(lg)
+    l = np64(lg[-tail:])
+    s = R.scores(l, "f32", "sigmoid")
+    ref = R.choice(l, s, "f32", k, None, 4, 2, 2)
+    assert np.array_equal(npi(ids[-tail:]), ref)
+    rw, _ = R.weights(l, s, "f32", ref, "sigmoid", True, 1.0)
+    close(w[-tail:], rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"], "w")
+    d_w = torch.ones((T, k), device=DEV) * torch.arange(k, device=DEV)
+    g, size = R.gradient(l, s, "f32", ref, np64(d_w[-tail:]), "sigmoid", True, 1.0)
+    got = plan.backward(d_w, lg)
+    close(got[-tail:], g, R.ROUND["f32"] * np.abs(g) + R.TINY["f32"] + 2.0 ** -46 * size, "d_logits")
+    assert int((ids[::4099] >= E).sum()) == 0
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("E,k", [(256, 8), (60, 3), (700, 16)])
+def test_replay(score, renorm, E, k):
+    T, S, s0 = 203, 500, 131
+    say(f"replay {score} renorm={renorm} E={E} k={k}")
+    rng = np.random.default_rng(11)
+    rec = [rng.permuted(np.tile(np.arange(E), (S, 1)), axis=1)[:, :k].T for _ in range(3)]
+    rec = np.ascontiguousarray(np.stack(rec).astype(np.int32))
+    rec[1, 0, s0 + 5] = E             # outside
+    rec[1, k - 1, s0 + 6] = -1
+    rec[1, 1, s0 + 9] = rec[1, 0, s0 + 9]   # twice
+    lg = make(T, E, 2)
+    sc = ops.Scoring(score, renorm=renorm, scale=2.0)
+    plan = RoutePlan(T, E, k, sc, train=True, device=DEV)
+    ids, w = plan.replay(torch.tensor(rec).to(DEV), 1, s0, lg)
+    assert int(plan.status.item()) == ops.FLAG_BAD_ID | ops.FLAG_DUP_ID
+    ref = rec[1, :, s0:s0 + T].T
+    assert np.array_equal(npi(ids), ref)
+    good = ((ref >= 0) & (ref < E)).all(axis=1)
+    l = np64(lg)
+    s = R.scores(l, "f32", score)
+    safe = np.where(good[:, None], ref, 0)
+    rw, _ = R.weights(l, s, "f32", safe, score, renorm, 2.0)
+    rw = np.where(good[:, None], rw, 0.0)
+    close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"], "w")
+    d_w = torch.tensor(rng.standard_normal((T, k)).astype(np.float32)).to(DEV)
+    g, size = R.gradient(l, s, "f32", safe, np64(d_w), score, renorm, 2.0)
+    g[~good], size[~good] = 0.0, 0.0
+    close(plan.backward(d_w, lg), g, R.ROUND["f32"] * np.abs(g) + R.TINY["f32"] + 2.0 ** -46 * size, "d_logits")
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+def test_gradient_against_differences(score, renorm):
+    """d_logits against central differences of the 64-bit weights at fixed ids."""
+    T, E, k, scale = 5, 24, 4, 1.7
+    lg = make(T, E, 21)
+    sc = ops.Scoring(score, renorm=renorm, scale=scale)
+    plan = RoutePlan(T, E, k, sc, train=True, device=DEV)
+    ids, _ = plan.forward(lg)
+    d_w = torch.tensor(np.random.default_rng(4).standard_normal((T, k)).astype(np.float32)).to(DEV)
+    got = np64(plan.backward(d_w, lg))
+    l, i, dw, h = np64(lg), npi(ids), np64(d_w), 1e-5
+
+    def loss(v):
+        w, _ = R.weights(v, R.scores(v, "f32", score), "f32", i, score, renorm, scale)
+        return (w * dw).sum(axis=1)
+    for e in range(E):
+        step = np.zeros((T, E))
+        step[:, e] = h
+        diff = (loss(l + step) - loss(l - step)) / (2 * h)
+        # third derivatives below 10 sum |d_w|: 10 h^2 / 6; differences of 64-bit values: 1e-15 / h
+        tol = np.abs(dw).sum(axis=1) * scale * (2 * h * h + 1e-9) + 2.0 ** -23 * np.abs(diff)
+        assert (np.abs(got[:, e] - diff) <= tol).all(), e
+
+
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("softmax", False)])
+def test_backward_from_partials(score, renorm):
+    T, E, k, d, rows = 77, 40, 5, 1024, 300
+    rng = np.random.default_rng(13)
+    lg = make(T, E, 3)
+    sc = ops.Scoring(score, renorm=renorm, scale=2.0)
+    ids, w = ops.route_scored(lg, k, sc)
+    part = torch.tensor(rng.standard_normal((rows, ops.GATE_PARTS)).astype(np.float32)).to(DEV)
+    pair_row = torch.tensor(rng.integers(-1, rows, size=(T, k)).astype(np.int32)).to(DEV)
+    groups = -(-(d // 128) // max(4, -(-(d // 128) // ops.GATE_PARTS)))
+    p = np64(part)[:, :groups]
+    pr = npi(pair_row)
+    dg = np.where(pr >= 0, p.sum(axis=1)[np.maximum(pr, 0)], 0.0)
+    err = np.where(pr >= 0, np.abs(p).sum(axis=1)[np.maximum(pr, 0)], 0.0) * groups * 2.0 ** -24
+    d_gate, d_logits = ops.route_scored_backward_parts(part, pair_row, rows, d, lg, ids, sc)
+    close(d_gate, dg, err, "d_gate")
+    l = np64(lg)
+    s = R.scores(l, "f32", score)
+    g, size = R.gradient(l, s, "f32", npi(ids), np64(d_gate), score, renorm, 2.0)
+    close(d_logits, g, R.ROUND["f32"] * np.abs(g) + R.TINY["f32"] + 2.0 ** -46 * size, "d_logits")
+
+
+@pytest.mark.parametrize("E", [1, 7, 64, 256, 1000, 1024])
+def test_balance(E):
+    rng = np.random.default_rng(E)
+    load = rng.integers(0, 1 << 30, size=E).astype(np.int32)
+    load[: E // 3] = load.astype(np.int64).sum() // E     # at or next to the mean
+    bias = rng.standard_normal(E).astype(np.float32)
+    ld, bd = torch.tensor(load).to(DEV), torch.tensor(bias).to(DEV)
+    total = int(load.astype(np.int64).sum())
+    want = bias + np.float32(0.001) * np.array([np.sign(total - int(n) * E) for n in load], dtype=np.float32)
+    out = ops.balance_bias(ld, bd, 0.001, clear=False)
+    assert np.array_equal(npi(out), want) and np.array_equal(npi(ld), load) and np.array_equal(npi(bd), bias)
+    assert ops.balance_bias(ld, bd, 0.001, out=bd) is bd
+    assert np.array_equal(npi(bd), want) and int(ld.abs().sum()) == 0
+    even = torch.full((E,), 9, dtype=torch.int32, device=DEV)
+    assert torch.equal(ops.balance_bias(even, bd, 0.5), bd)
+
+
+def test_balance_evens_the_load():
+    """Choice, load and bias in turn: the largest share of an expert falls towards the mean."""
+    T, E, k = 4096, 64, 4
+    lg = make(T, E, 17) + torch.linspace(-1.5, 1.5, E, device=DEV)
+    bias, load = torch.zeros(E, device=DEV), torch.zeros(E, dtype=torch.int32, device=DEV)
+    plan = RoutePlan(T, E, k, ops.Scoring("sigmoid"), device=DEV)
+    spread = []
+    for _ in range(150):
+        plan.forward(lg, bias=bias, load=load)
+        spread.append(int(load.max()) - int(load.min()))
+        ops.balance_bias(load, bias, 0.01, out=bias)
+    assert spread[-1] < spread[0] / 4
+
+
+def test_empty_batch_and_no_train():
+    plan = RoutePlan(0, 16, 2, ops.Scoring(), train=True, device=DEV)
+    lg = torch.empty((0, 16), device=DEV)
+    ids, w = plan.forward(lg)
+    assert ids.shape == (0, 2) and plan.backward(torch.empty((0, 2), device=DEV), lg).shape == (0, 16)
+    plan = RoutePlan(4, 16, 2, ops.Scoring(), device=DEV)
+    with pytest.raises(ValueError):
+        plan.backward(torch.zeros((4, 2), device=DEV), torch.zeros((4, 16), device=DEV))
+    with pytest.raises(ValueError):
+        plan.forward(torch.zeros((5, 16), device=DEV))
+    with pytest.raises(ValueError):
+        plan.forward(torch.zeros((4, 16), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        plan.forward(torch.zeros((4, 32), device=DEV)[:, ::2])
+    with pytest.raises(ops.MoeError):
+        ops.route_scored(torch.zeros((4, 16), device=DEV), 9, ops.Scoring(groups=4, top_groups=2))
+    with pytest.raises(ops.MoeError):
+        ops.route_scored(torch.zeros(80, device=DEV)[1:65].view(4, 16), 2, ops.Scoring())
+
+
+def test_graph_and_streams():
+    """Captured and replayed several times with other work between, and on a side stream."""
+    T, E, k = 512, 256, 8
+    sc = ops.Scoring("sigmoid", groups=8, top_groups=4, scale=2.5)
+    lg, bias = make(T, E, 31), torch.zeros(E, device=DEV)
+    load = torch.zeros(E, dtype=torch.int32, device=DEV)
+    plan = RoutePlan(T, E, k, sc, train=True, device=DEV)
+    graph = plan.capture(lg, bias=bias, load=load)
+    load.zero_()
+    for seed in range(3):
+        new = make(T, E, 40 + seed)
+        lg.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        ids, w = ops.route_scored(new, k, sc, bias=bias)
+        assert torch.equal(plan.ids, ids) and torch.equal(plan.w, w)
+        assert int(load.sum()) == (seed + 1) * T * k
+    side = torch.cuda.Stream()
+    other = RoutePlan(T, E, k, sc, train=True, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a = other.forward(lg, bias=bias)
+    side.synchronize()
+    assert torch.equal(a[0], plan.ids) and torch.equal(a[1], plan.w)
