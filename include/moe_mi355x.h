@@ -613,6 +613,69 @@ int moe_gated_ffn_backward(const uint16_t* dy, const uint16_t* x, int64_t ldx, c
 int moe_gated_ffn_backward_grouped(int64_t T, int64_t d, int64_t f, int32_t dx, int32_t dW13, int32_t dW2, int32_t dbias,
                                    int32_t* yes);
 
+/* ---- the norms around the layer: from the residual stream and back to it ---
+ * ("RL at 1T scale", section "Wide Expert Parallelism": what every token passes
+ * once per layer besides its experts)
+ * norm(v; w)[c] = v[c] * rho * w[c],  rho = 1 / sqrt(mean of v^2 over the row + eps).
+ * The residual stream is bf16 or fp32 (MOE_SRC_*), what the products read and write
+ * is bf16; weights and gates are bf16 or fp32. Sums, rho and everything between
+ * load and store are fp32 (a row whose mean square passes fp32's range gets rho = 0).
+ * Matrices are row-major [T, d]; ld* as the dense products' above (a multiple of 8
+ * from d to 2^22), the others dense.  d is a multiple of 8 from 8 to 2^20,
+ * 0 <= T <= 2^30, eps > 0, scales finite; matrices, weights, gates of d or T x d
+ * elements, workspaces: 16-byte aligned. T = 0 is a no-op (the backward functions
+ * then write zeros to the gradients of weights and of a gate per channel).
+ * Outputs overlap no input, workspace or other output, but where it is said.    */
+
+/* h = norm(x; w) bf16 [T, d];  rstd (NULL: not kept) [T] fp32 = rho.
+ *   x [T, d] of x_type (row stride ldx), w [d] of w_type.                       */
+int moe_norm(const void* x, int32_t x_type, int64_t ldx, const void* w, int32_t w_type, int64_t T, int64_t d, float eps,
+             uint16_t* h, float* rstd, hipStream_t stream);
+
+/* Gradients of moe_norm: with xh = x * rstd, a = dh * w
+ *     dx = rstd (a - xh mean(a xh)) + dx_add        dw = sum over the tokens of dh * xh
+ *   dh [T, d] bf16, rstd as kept by the forward, dx_add [T, d] of x_type or NULL
+ *   (may be dx), dx [T, d] of x_type and dw [d] of w_type, each NULL to skip it.  */
+int moe_norm_backward_workspace(int64_t T, int64_t d, size_t* bytes);
+int moe_norm_backward(const uint16_t* dh, const void* x, int32_t x_type, int64_t ldx, const void* w, int32_t w_type,
+                      const float* rstd, const void* dx_add, int64_t T, int64_t d, void* dx, void* dw,
+                      void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* What a gate has one value for: each column [d], each token [T], each element [T, d]. */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 };
+
+/* The layer's output y joined to the residual stream r, and the next layer's input:
+ *     n     = norm(y; w_post)                 (w_post NULL: n = y)
+ *     r_out = r_scale * r + y_scale * g * n   of r_type;  g = gate_act(gate), 1 without a gate
+ *     h     = norm(r_out as stored; w_pre)    (w_pre NULL: none; h is then not written)
+ *   y [T, d] bf16 (ldy), r [T, d] of r_type (ldr), gate of gate_type by gate_kind
+ *   (one of MOE_GATE_*), gate_act MOE_ACT_NONE or MOE_ACT_SIGMOID, w_post, w_pre
+ *   [d] of w_type.  r_out [T, d] of r_type (may be r where ldr == d), h bf16.
+ *   rstd_post, rstd_pre [T] fp32: rho of y and of r_out for the backward (each
+ *   may be NULL).                                                               */
+int moe_join(const uint16_t* y, int64_t ldy, const void* r, int32_t r_type, int64_t ldr, const void* w_post,
+             const void* gate, int32_t gate_kind, int32_t gate_type, int32_t gate_act, float r_scale, float y_scale,
+             const void* w_pre, int32_t w_type, int64_t T, int64_t d, float eps, void* r_out, uint16_t* h,
+             float* rstd_post, float* rstd_pre, hipStream_t stream);
+
+/* Gradients of moe_join for d_out [T, d] of r_type (of r_out along the residual
+ * stream; NULL: 0) and dh [T, d] bf16 (of h; NULL without w_pre):
+ *     D    = d_out + rstd_pre (a - rh mean(a rh)),   a = dh * w_pre,  rh = r_out * rstd_pre
+ *     dr   = r_scale * D           dn = y_scale * D * g          dw_pre = sum of dh * rh
+ *     dgate = y_scale * D * n * gate_act'(gate), summed over what shares a gate
+ *     dy   = rstd_post (b - yh mean(b yh)),   b = dn * w_post,  yh = y * rstd_post  (w_post NULL: dn)
+ *     dw_post = sum of dn * yh                (sums over the tokens)
+ *   y, gate, w_post, w_pre and the constants as given to the forward, r_out (dense)
+ *   and rstd_* as written by it (r_out is not read without w_pre).  dr [T, d] of r_type
+ *   (may be d_out), dy [T, d] bf16, dw_post, dw_pre [d] of w_type, dgate of
+ *   gate_type and the gate's shape, each NULL to skip it.                       */
+int moe_join_backward_workspace(int64_t T, int64_t d, size_t* bytes);
+int moe_join_backward(const void* d_out, const uint16_t* dh, const uint16_t* y, int64_t ldy, const void* r_out,
+                      int32_t r_type, const void* w_post, const void* gate, int32_t gate_kind, int32_t gate_type,
+                      int32_t gate_act, float r_scale, float y_scale, const void* w_pre, int32_t w_type,
+                      const float* rstd_post, const float* rstd_pre, int64_t T, int64_t d, void* dr, uint16_t* dy,
+                      void* dw_post, void* dw_pre, void* dgate, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ---- activations kept in 8 bits between forward and backward ---------------
  * Rows in blocks of 128 columns (the last one shorter if cols % 128 != 0), one
  * fp32 scale each:

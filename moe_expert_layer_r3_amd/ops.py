@@ -24,6 +24,7 @@ GEMM_THIN_SPLIT = 0x1000  # thin last 288-row m-tiles of a SwiGLU product split 
 SRC_BF16, SRC_F32 = 0, 1
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}  # MOE_ACT_*
 SCORES = {"softmax": 0, "sigmoid": 1}  # MOE_SCORE_*
+GATES = {"none": 0, "channel": 1, "token": 2, "full": 3}  # MOE_GATE_*
 SAVES = {"none": 0, "bf16": 1, "int8": 2}  # MOE_SAVE_*
 DENSE_PRODUCTS = {"forward": 0, "gated": 1, "gated_int8": 2, "gradient": 3}  # MOE_PRODUCT_*
 DENSE_KERNELS = ("thin", "slab", "small", "tiles", "half", "wide")           # MOE_DENSE_*
@@ -98,6 +99,14 @@ _SIGS = {
                                               _P, _P, _P, _P, _SZ, _P]),
     "moe_gated_ffn_backward_grouped": (ctypes.c_int, [_I64, _I64, _I64, _I32, _I32, _I32, _I32,
                                                       ctypes.POINTER(_I32)]),
+    "moe_norm": (ctypes.c_int, [_P, _I32, _I64, _P, _I32, _I64, _I64, _F32, _P, _P, _P]),
+    "moe_norm_backward_workspace": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_norm_backward": (ctypes.c_int, [_P, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_join": (ctypes.c_int, [_P, _I64, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _F32, _F32, _P, _I32, _I64, _I64, _F32,
+                                _P, _P, _P, _P, _P]),
+    "moe_join_backward_workspace": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "moe_join_backward": (ctypes.c_int, [_P, _P, _P, _I64, _P, _I32, _P, _P, _I32, _I32, _I32, _F32, _F32, _P, _I32, _P, _P,
+                                         _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_act_save": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "moe_act_restore": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P]),
 }
