@@ -1,6 +1,8 @@
 // The norms around the layer: in front of it (moe_norm), and behind it together
 // with the gate, the scaled residual sum and the next layer's norm (moe_join), and
 // their gradients.
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -39,7 +41,7 @@ struct JoinGradArgs {
     void* dr;
     uint16_t* dy;
     void* dgate;                             // per token or element
-    float *part_post, *part_pre, *part_gate;  // [gridDim.x, d] each, NULL: not wanted
+    float *part_pre, *part_y;  // partial sums over the tokens, NULL: not wanted
 };
 
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
@@ -84,12 +86,18 @@ __device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float v) {
     else static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
 }
 
-__device__ __forceinline__ float sigmoid32(float x) { return 1.0f / (1.0f + expf(-x)); }
-// gate and its slope
-__device__ __forceinline__ float gate_value(float x, int act) { return act == MOE_ACT_SIGMOID ? sigmoid32(x) : x; }
-__device__ __forceinline__ float gate_slope(float x, int act) {
-    return act == MOE_ACT_SIGMOID ? sigmoid32(x) * sigmoid32(-x) : 1.0f;
+// Gate and its slope. The exponential of -|x| serves both, without cancellation:
+// e / (1 + e)^2 is the slope on either side.
+struct Gate {
+    float value, slope;
+};
+__device__ __forceinline__ Gate gate_of(float x, int act) {
+    if (act != MOE_ACT_SIGMOID) return {x, 1.0f};
+    const float e = expf(-fabsf(x)), q = 1.0f / (1.0f + e);
+    return {x >= 0.f ? q : e * q, e * q * q};
 }
+__device__ __forceinline__ float gate_value(float x, int act) { return gate_of(x, act).value; }
+__device__ __forceinline__ float gate_slope(float x, int act) { return gate_of(x, act).slope; }
 
 // Sum over the workgroup, the same in every thread; `slot` alternates so that one
 // barrier does.
@@ -270,12 +278,11 @@ __global__ __launch_bounds__(NT) void join_backward_kernel(JoinGradArgs a) {
                 const float yh = v[j] * rho_y, n = a.w_post ? yh * w[j] : v[j];
                 const float dz = a.y_scale * D[j], dn = dz * gate_value(g[j], a.gate_act);
                 dg[j] = dz * n;
-                p[j] = dn * yh;
+                p[j] = (a.gate_kind == MOE_GATE_CHANNEL ? dz : dn) * yh;
                 o[j] = a.w_post ? rho_y * (dn * w[j] - yh * sn) : dn;
             }
             if (a.dy) store8(a.dy, t * d + c, false, o);
-            if (a.part_post) add8(a.part_post, c, p);
-            if (a.part_gate) add8(a.part_gate, c, dg);
+            if (a.part_y) add8(a.part_y, c, p);
             if (a.gate_kind == MOE_GATE_FULL && a.dgate) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) dg[j] *= gate_slope(g[j], a.gate_act);
@@ -285,33 +292,366 @@ __global__ __launch_bounds__(NT) void join_backward_kernel(JoinGradArgs a) {
     }
 }
 
-// Sums of the partial rows, in order, 64 columns to a wave and 4 waves to the rows.
-struct ColumnSum {
-    const float* part;
-    void* out;
-    bool f32;
-    const void* gate;  // != NULL: times the slope of the gate's activation
-    bool gate_f32;
+// ---------------------------------------------------------------- rows in registers
+//
+// A team holds a row: every thread one chunk of eight columns, the same columns in
+// every row, so that weights and column sums stay in its registers. Rows of up to
+// 512 columns: teams of L lanes (a power of two) of a wave, no barriers; longer
+// ones: a workgroup of up to 1024 threads, one barrier per sum. The next row's loads
+// go out before this row's sums are waited for.
+
+// Sum over aligned groups of L lanes (a power of two up to 64), in every lane.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float swap16_add(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap32_add(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+template <int N>
+__device__ __forceinline__ void lanes_sum(float (&v)[N], int L) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (L > 1) v[i] = dpp_add<0xB1>(v[i]);    // lane xor 1
+        if (L > 2) v[i] = dpp_add<0x4E>(v[i]);    // lane xor 2
+        if (L > 4) v[i] = dpp_add<0x141>(v[i]);   // mirrored in 8
+        if (L > 8) v[i] = dpp_add<0x140>(v[i]);   // mirrored in 16
+        if (L > 16) v[i] = swap16_add(v[i]);
+        if (L > 32) v[i] = swap32_add(v[i]);
+    }
+}
+// Sums over the team, in every thread; lds alternates between calls.
+template <bool WAVE, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], int L, float (*lds)[16][4], int& slot) {
+    if constexpr (WAVE) {
+        lanes_sum(v, L);
+    } else {
+        lanes_sum(v, 64);
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 15, waves = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds[slot][wave][i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = lane < waves ? lds[slot][lane][i] : 0.f;
+        lanes_sum(v, 16);
+        slot ^= 1;
+    }
+}
+
+// eight columns as they lie in memory
+template <bool F32>
+struct Chunk {
+    u4 q[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        const u4* s = reinterpret_cast<const u4*>(static_cast<const char*>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) q[k] = s[k];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) q[k] = u4{0u, 0u, 0u, 0u};
+    }
+    // keeps the values packed over this point: unpacked ones are made anew behind it
+    __device__ __forceinline__ void pin() {
+#pragma unroll
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) asm volatile("" : "+v"(q[k]));
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (F32) return __uint_as_float(q[j >> 2][j & 3]);
+        else return (j & 1) ? bf16_hi(q[0][j >> 1]) : bf16_lo(q[0][j >> 1]);
+    }
+};
+
+struct Team {
+    int64_t row, rows;  // first row, and how many teams there are
+    int64_t c;          // first column
+    bool on;            // the thread has columns
+};
+template <bool WAVE>
+__device__ __forceinline__ Team team_of(int64_t d, int L) {
+    if constexpr (WAVE) {
+        const int lane = threadIdx.x & 63, per = 64 / L;
+        const int64_t wave = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+        const int64_t c = (lane & (L - 1)) * 8;
+        return {wave * per + lane / L, (int64_t)gridDim.x * (blockDim.x >> 6) * per, c, c < d};
+    } else {
+        const int64_t c = (int64_t)threadIdx.x * 8;
+        return {blockIdx.x, gridDim.x, c, c < d};
+    }
+}
+
+// eight exponentials at once would not fit the registers
+__device__ __forceinline__ void two_at_a_time(int j) {
+    if (j & 1) __builtin_amdgcn_sched_barrier(0);
+}
+
+enum { FULL_NONE = 0, FULL_BF16 = 1, FULL_F32 = 2 };  // a gate per element, and its type
+
+// Y: with y, else a norm of r alone. Waves of one workgroup run rows of their own in
+// the WAVE form; a team without a row left computes on the last one and stores nothing.
+template <bool RF32, bool Y, int FULL, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a, int L) {
+    __shared__ float lds[2][16][4];
+    int slot = 0;
+    const int64_t d = a.d;
+    const Team tm = team_of<WAVE>(d, L);
+    float wz[8], wn[8];  // of y: y_scale, the norm's weight, a channel's gate; of the next norm
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wz[j] = a.y_scale, wn[j] = 0.f;
+    if (tm.on) {
+        float v[8];
+        if (Y && a.w_post) {
+            load8(v, a.w_post, tm.c, a.w_f32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wz[j] *= v[j];
+        }
+        if (Y && a.gate_kind == MOE_GATE_CHANNEL) {
+            load8(v, a.gate, tm.c, a.gate_f32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wz[j] *= gate_value(v[j], a.gate_act);
+        }
+        if (a.w_pre) load8(wn, a.w_pre, tm.c, a.w_f32);
+    }
+    Chunk<false> y, y1;
+    Chunk<RF32> r, r1;
+    Chunk<FULL == FULL_F32> g, g1;
+    y1.zero(), r1.zero(), g1.zero();
+    auto fetch = [&](int64_t t) {
+        if (!tm.on) return;
+        r1.load(a.r, t * a.ldr + tm.c);
+        if constexpr (Y) y1.load(a.y, t * a.ldy + tm.c);
+        if constexpr (FULL != FULL_NONE) g1.load(a.gate, t * d + tm.c);
+    };
+    // the WAVE form's teams of one wave go round together
+    const int64_t last = a.T - 1;
+    fetch(tm.row < a.T ? tm.row : last);
+    for (int64_t t0 = WAVE ? tm.row & ~(int64_t)(64 / L - 1) : tm.row; t0 < a.T; t0 += tm.rows) {
+        const int64_t t = WAVE ? t0 + (tm.row & (64 / L - 1)) : t0;
+        const bool live = !WAVE || t < a.T;
+        y = y1, r = r1, g = g1;
+        if (t0 + tm.rows < a.T) fetch(t + tm.rows < a.T ? t + tm.rows : last);
+        float rv[8];
+        if constexpr (Y) {
+            float f = 1.0f;
+            if (a.w_post) {
+                float s[1] = {0.f};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[0] += y[j] * y[j];
+                team_sum<WAVE>(s, L, lds, slot);
+                f = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+                if (a.rstd_post && live && tm.c == 0) a.rstd_post[t] = f;
+            }
+            if (a.gate_kind == MOE_GATE_TOKEN) f *= gate_value(load1(a.gate, live ? t : last, a.gate_f32), a.gate_act);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float z = y[j] * f * wz[j];
+                if constexpr (FULL != FULL_NONE) z *= gate_value(g[j], a.gate_act);
+                rv[j] = stored(a.r_scale * r[j] + z, RF32);
+            }
+            if (live && tm.on) store8(a.r_out, t * d + tm.c, RF32, rv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rv[j] = r[j];
+        }
+        if (!a.w_pre) continue;
+        float s[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] += rv[j] * rv[j];
+        team_sum<WAVE>(s, L, lds, slot);
+        const float rho = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+        if (live && tm.on) {
+            if (a.rstd_pre && tm.c == 0) a.rstd_pre[t] = rho;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rv[j] = rv[j] * rho * wn[j];
+            store8(a.h, t * d + tm.c, false, rv);
+        }
+    }
+}
+
+// The gradients. With z = g n and a = dh w_pre the mean that dy's norm needs,
+//     sum D z = sum d_out z + rho (sum a z - mean(a rh) sum rh z),
+// comes from sums that do not wait for mean(a rh): one round of four sums per row.
+// Sums over the tokens: dh rh, and D g yh (a channel's gate, the same for all of
+// them, is put in at the end).
+template <bool RF32, bool Y, int FULL, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_backward_kernel(JoinGradArgs a, int L) {
+    __shared__ float lds[2][16][4];
+    int slot = 0;
+    const int64_t d = a.d;
+    const Team tm = team_of<WAVE>(d, L);
+    float wz[8], wn[8];  // of y: the norm's weight, a channel's gate; of the next norm
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wz[j] = 1.0f, wn[j] = 0.f;
+    if (tm.on) {
+        float v[8];
+        if (Y && a.w_post) load8(wz, a.w_post, tm.c, a.w_f32);
+        if (Y && a.gate_kind == MOE_GATE_CHANNEL) {
+            load8(v, a.gate, tm.c, a.gate_f32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wz[j] *= gate_value(v[j], a.gate_act);
+        }
+        if (a.w_pre) load8(wn, a.w_pre, tm.c, a.w_f32);
+    }
+    float acc_n[8], acc_y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc_n[j] = acc_y[j] = 0.f;
+    Chunk<false> y, y1, h, h1;
+    Chunk<RF32> r, r1, o, o1;
+    Chunk<FULL == FULL_F32> g, g1;
+    y1.zero(), h1.zero(), r1.zero(), o1.zero(), g1.zero();
+    auto fetch = [&](int64_t t) {
+        if (!tm.on) return;
+        if (a.w_pre) {
+            h1.load(a.dh, t * d + tm.c);
+            r1.load(a.r_out, t * a.ldr + tm.c);
+        }
+        if (a.d_out) o1.load(a.d_out, t * d + tm.c);
+        if constexpr (Y) y1.load(a.y, t * a.ldy + tm.c);
+        if constexpr (FULL != FULL_NONE) g1.load(a.gate, t * d + tm.c);
+    };
+    const int64_t last = a.T - 1;
+    // (with a gate per element the next row's chunks would not fit the registers)
+    if constexpr (FULL == FULL_NONE) fetch(tm.row < a.T ? tm.row : last);
+    for (int64_t t0 = WAVE ? tm.row & ~(int64_t)(64 / L - 1) : tm.row; t0 < a.T; t0 += tm.rows) {
+        const int64_t t = WAVE ? t0 + (tm.row & (64 / L - 1)) : t0;
+        const bool live = !WAVE || t < a.T;
+        const int64_t tt = live ? t : last;
+        if constexpr (FULL != FULL_NONE) fetch(tt);
+        y = y1, h = h1, r = r1, o = o1, g = g1;
+        if constexpr (FULL == FULL_NONE)
+            if (t0 + tm.rows < a.T) fetch(t + tm.rows < a.T ? t + tm.rows : last);
+        const float rho = a.w_pre ? a.rstd_pre[tt] : 0.f;
+        const float rho_y = Y && a.w_post ? a.rstd_post[tt] : 1.f;
+        float gt = 1.f, gs = 0.f;
+        if (Y && a.gate_kind == MOE_GATE_TOKEN) {
+            const float v = load1(a.gate, tt, a.gate_f32);
+            gt = gate_value(v, a.gate_act);
+            gs = gate_slope(v, a.gate_act);
+        }
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float aj = h[j] * wn[j], rh = r[j] * rho;
+            s[0] += aj * rh;
+            if constexpr (Y) {
+                float z = y[j] * rho_y * wz[j];
+                if constexpr (FULL != FULL_NONE) z *= gate_value(g[j], a.gate_act);
+                s[1] += o[j] * z;
+                s[2] += aj * z;
+                s[3] += rh * z;
+                if constexpr (FULL != FULL_NONE) two_at_a_time(j);
+            }
+        }
+        if constexpr (Y) {
+            team_sum<WAVE>(s, L, lds, slot);
+        } else {
+            float s1[1] = {s[0]};
+            team_sum<WAVE>(s1, L, lds, slot);
+            s[0] = s1[0];
+        }
+        y.pin(), h.pin(), r.pin(), o.pin(), g.pin();
+        const float mean = s[0] / (float)d;
+        float sn = 0.f;
+        if constexpr (Y) {
+            const float sum = a.y_scale * (s[1] + rho * (s[2] - mean * s[3]));
+            if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && live && tm.c == 0) store1(a.dgate, t, a.gate_f32, sum * gs);
+            sn = sum * gt / (float)d;
+        }
+        if (!live || !tm.on) continue;
+        float dr[8], dy[8], dg[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float rh = r[j] * rho, D = o[j] + rho * (h[j] * wn[j] - rh * mean);
+            acc_n[j] += h[j] * rh;
+            dr[j] = a.r_scale * D;
+            if constexpr (Y) {
+                const float yh = y[j] * rho_y, dz = a.y_scale * D;
+                float q = dz * gt;
+                if constexpr (FULL != FULL_NONE) {
+                    const Gate f = gate_of(g[j], a.gate_act);
+                    q *= f.value;
+                    dg[j] = dz * (yh * wz[j]) * f.slope;
+                }
+                acc_y[j] += q * yh;
+                dy[j] = a.w_post ? rho_y * (q * wz[j] - yh * sn) : q * wz[j];
+                if constexpr (FULL != FULL_NONE) two_at_a_time(j);
+            }
+        }
+        if (a.dr) store8(a.dr, t * d + tm.c, RF32, dr);
+        if constexpr (Y) {
+            if (a.dy) store8(a.dy, t * d + tm.c, false, dy);
+            if constexpr (FULL != FULL_NONE)
+                if (a.dgate) store8(a.dgate, t * d + tm.c, FULL == FULL_F32, dg);
+        }
+    }
+    // one partial row per workgroup or wave
+    int64_t part = blockIdx.x;
+    if constexpr (WAVE) {
+        part = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+        for (int m = L; m < 64; m <<= 1)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc_n[j] += __shfl_xor(acc_n[j], m);
+                acc_y[j] += __shfl_xor(acc_y[j], m);
+            }
+        if ((threadIdx.x & 63) >= L) return;
+    }
+    if (!tm.on) return;
+    if (a.part_pre) store8(a.part_pre, part * d + tm.c, true, acc_n);
+    if (Y && a.part_y) store8(a.part_y, part * d + tm.c, true, acc_y);
+}
+
+// The columns' sums over the partial rows, 64 columns to a workgroup and its 16
+// waves over the rows, in a fixed order; then dw_pre, or dw_post and a channel's
+// dgate, which share one sum q: dw_post = g q, dgate = w_post slope(gate) q.
+struct ColumnSums {
+    const float *pre, *y;
+    int64_t rows, d;
+    void *dw_pre, *dw_post, *dgate;
+    const void *w_post, *gate;
+    bool w_f32, gate_f32, channel;
     int act;
 };
-struct ColumnSums {
-    ColumnSum s[3];
-    int64_t rows, d;
-};
-__global__ __launch_bounds__(256) void column_sums_kernel(ColumnSums a) {
-    __shared__ float lds[4][64];
-    const ColumnSum q = a.s[blockIdx.y];
+__global__ __launch_bounds__(1024) void column_sums_kernel(ColumnSums a) {
+    __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    const bool of_y = a.pre == nullptr || blockIdx.y == 1;
+    const float* p = (of_y ? a.y : a.pre) + (c < a.d ? c : a.d - 1);
     float s = 0.f;
-    if (c < a.d)
-        for (int64_t i = wave; i < a.rows; i += 4) s += q.part[i * a.d + c];
+#pragma unroll 8
+    for (int64_t i = wave; i < a.rows; i += 16) s += p[i * a.d];
     lds[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= a.d) return;
-    s = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
-    if (q.gate) s *= gate_slope(load1(q.gate, c, q.gate_f32), q.act);
-    store1(q.out, c, q.f32, s);
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s += lds[i][lane];
+    if (!of_y) {
+        store1(a.dw_pre, c, a.w_f32, s);
+        return;
+    }
+    const float g = a.channel ? load1(a.gate, c, a.gate_f32) : 0.f;
+    if (a.dw_post) store1(a.dw_post, c, a.w_f32, a.channel ? s * gate_value(g, a.act) : s);
+    if (a.dgate) {
+        if (a.w_post) s *= load1(a.w_post, c, a.w_f32);
+        store1(a.dgate, c, a.gate_f32, s * gate_slope(g, a.act));
+    }
+}
+
+// zeros for the gradients of weights and of a channel's gate without tokens
+__global__ __launch_bounds__(256) void zero_columns_kernel(void* a, void* b, void* g, int64_t d, bool w_f32, bool gate_f32) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= d) return;
+    if (a) store1(a, c, w_f32, 0.f);
+    if (b) store1(b, c, w_f32, 0.f);
+    if (g) store1(g, c, gate_f32, 0.f);
 }
 
 // ---------------------------------------------------------------- host
@@ -338,50 +678,101 @@ int check_gate(const char* what, int32_t kind, int32_t type, int32_t act, const 
     return MOE_OK;
 }
 
-// workgroups of a backward launch, each with its partial sums: twice the compute
-// units, fewer where the partial sums would pass 2^27 elements
-int64_t backward_blocks(int64_t T, int64_t d) {
-    int64_t n = 2 * (int64_t)num_cus();
-    n = n < (1 << 27) / d ? n : (1 << 27) / d;
-    return T < n ? T : n;
+// How a launch takes rows of d columns: in registers up to 8192 (a chunk of eight to
+// each of up to 1024 threads), read again for each sum beyond.
+constexpr int64_t MAX_ROW = 8192;
+struct Shape {
+    int L, threads, per;  // lanes of a team in a wave (0: a workgroup to a row); rows of a workgroup at a time
+};
+Shape shape_of(int64_t d) {
+    if (d > MAX_ROW) return {0, NT, 1};
+    const int chunks = (int)(d / 8);
+    if (chunks > 64) return {0, (chunks + 63) / 64 * 64, 1};
+    int L = 1;
+    while (L < chunks) L <<= 1;
+    return {L, 256, 4 * (64 / L)};
 }
-size_t backward_bytes(int64_t T, int64_t d, int sums) { return (size_t)backward_blocks(T, d) * d * sums * sizeof(float); }
+// workgroups of a backward launch: enough to fill the compute units, but eight rows at
+// least to each where there are more rows than units, for the partial sums' sake
+int64_t backward_blocks(int64_t T, int64_t d) {
+    const Shape s = shape_of(d);
+    const int64_t cus = num_cus(), units = (T + s.per - 1) / s.per;
+    int64_t n = cus * (1024 / s.threads);
+    const int64_t most = units / 8 > cus ? units / 8 : cus;
+    n = n < most ? n : most;
+    if (d > MAX_ROW) n = n < (1 << 27) / d ? n : (1 << 27) / d;
+    return units < n ? units : n;
+}
+int64_t partial_rows(int64_t T, int64_t d) { return backward_blocks(T, d) * (shape_of(d).L ? 4 : 1); }
+size_t backward_bytes(int64_t T, int64_t d, int sums) { return (size_t)partial_rows(T, d) * d * sums * sizeof(float); }
 
-dim3 row_grid(int64_t T) { return dim3((unsigned)(T < (1 << 22) ? T : 1 << 22)); }
+// f(Y, FULL as integral constants)
+template <typename F>
+void with_gate(bool y, int32_t kind, bool f32, F&& f) {
+    if (!y) f(std::false_type{}, std::integral_constant<int, FULL_NONE>{});
+    else if (kind != MOE_GATE_FULL) f(std::true_type{}, std::integral_constant<int, FULL_NONE>{});
+    else if (f32) f(std::true_type{}, std::integral_constant<int, FULL_F32>{});
+    else f(std::true_type{}, std::integral_constant<int, FULL_BF16>{});
+}
 
+template <bool RF32>
+void launch_join(const JoinArgs& a, hipStream_t stream) {
+    const Shape s = shape_of(a.d);
+    const int64_t units = (a.T + s.per - 1) / s.per, most = (int64_t)num_cus() * (2048 / s.threads);
+    const dim3 grid((unsigned)(units < most ? units : most)), block(s.threads);
+    if (a.d > MAX_ROW) {
+        join_kernel<RF32><<<grid, block, 0, stream>>>(a);
+        return;
+    }
+    with_gate(a.y != nullptr, a.gate_kind, a.gate_f32, [&](auto y, auto full) {
+        if (s.L) join_rows_kernel<RF32, y.value, full.value, true><<<grid, block, 0, stream>>>(a, s.L);
+        else join_rows_kernel<RF32, y.value, full.value, false><<<grid, block, 0, stream>>>(a, s.L);
+    });
+}
+template <bool RF32>
+void launch_join_backward(const JoinGradArgs& a, hipStream_t stream) {
+    const Shape s = shape_of(a.d);
+    const dim3 grid((unsigned)backward_blocks(a.T, a.d)), block(s.threads);
+    if (a.d > MAX_ROW) {
+        join_backward_kernel<RF32><<<grid, block, 0, stream>>>(a);
+        return;
+    }
+    with_gate(a.y != nullptr, a.gate_kind, a.gate_f32, [&](auto y, auto full) {
+        if (s.L) join_rows_backward_kernel<RF32, y.value, full.value, true><<<grid, block, 0, stream>>>(a, s.L);
+        else join_rows_backward_kernel<RF32, y.value, full.value, false><<<grid, block, 0, stream>>>(a, s.L);
+    });
+}
 
-// the weights' gradients from the partial sums (T == 0: zeros)
-int launch_column_sums(ColumnSums& s, int n, hipStream_t stream) {
-    if (n == 0) return MOE_OK;
-    column_sums_kernel<<<dim3((unsigned)((s.d + 63) / 64), n), dim3(256), 0, stream>>>(s);
-    MOE_LAUNCH_CHECK("column_sums_kernel");
+int launch_forward(const JoinArgs& a, bool r_f32, hipStream_t stream) {
+    if (r_f32) launch_join<true>(a, stream);
+    else launch_join<false>(a, stream);
+    MOE_LAUNCH_CHECK("join_rows_kernel");
     return MOE_OK;
 }
 
+// dw_gate: of a gate per channel
 int launch_backward(JoinGradArgs a, bool r_f32, void* dw_post, void* dw_pre, void* dw_gate, void* ws, hipStream_t stream) {
-    const int64_t nb = backward_blocks(a.T, a.d);
-    ColumnSums s = {};
-    s.rows = nb;
-    s.d = a.d;
-    int n = 0;
-    float* p = static_cast<float*>(ws);
-    auto want = [&](void* out, bool f32, const void* gate, float** part) {
-        if (!out) return;
-        s.s[n++] = {p, out, f32, gate, a.gate_f32, a.gate_act};
-        *part = p;
-        p += nb * a.d;
-    };
-    want(dw_post, a.w_f32, nullptr, &a.part_post);
-    want(dw_pre, a.w_f32, nullptr, &a.part_pre);
-    want(dw_gate, a.gate_f32, a.gate, &a.part_gate);
-    if (a.T > 0) {
-        if (r_f32) join_backward_kernel<true><<<dim3((unsigned)nb), dim3(NT), 0, stream>>>(a);
-        else join_backward_kernel<false><<<dim3((unsigned)nb), dim3(NT), 0, stream>>>(a);
-        MOE_LAUNCH_CHECK("join_backward_kernel");
-    } else {
-        for (int i = 0; i < n; ++i) s.s[i].gate = nullptr;
+    if (a.T == 0) {
+        if (!dw_post && !dw_pre && !dw_gate) return MOE_OK;
+        zero_columns_kernel<<<dim3((unsigned)((a.d + 255) / 256)), dim3(256), 0, stream>>>(dw_post, dw_pre, dw_gate, a.d,
+                                                                                           a.w_f32, a.gate_f32);
+        MOE_LAUNCH_CHECK("zero_columns_kernel");
+        return MOE_OK;
     }
-    return launch_column_sums(s, n, stream);
+    const int64_t rows = partial_rows(a.T, a.d);
+    float* p = static_cast<float*>(ws);
+    int n = 0;
+    if (dw_pre) a.part_pre = p + rows * a.d * n++;
+    if (dw_post || dw_gate) a.part_y = p + rows * a.d * n++;
+    if (r_f32) launch_join_backward<true>(a, stream);
+    else launch_join_backward<false>(a, stream);
+    MOE_LAUNCH_CHECK("join_rows_backward_kernel");
+    if (n == 0) return MOE_OK;
+    const ColumnSums s = {a.part_pre, a.part_y, rows, a.d, dw_pre, dw_post, dw_gate, a.w_post, a.gate, a.w_f32, a.gate_f32,
+                          a.gate_kind == MOE_GATE_CHANNEL, a.gate_act};
+    column_sums_kernel<<<dim3((unsigned)((a.d + 63) / 64), n), dim3(1024), 0, stream>>>(s);
+    MOE_LAUNCH_CHECK("column_sums_kernel");
+    return MOE_OK;
 }
 
 }  // namespace
@@ -409,10 +800,7 @@ extern "C" int moe_norm(const void* x, int32_t x_type, int64_t ldx, const void* 
     a.d = d;
     a.h = h;
     a.rstd_pre = rstd;
-    if (x_type == MOE_SRC_F32) join_kernel<true><<<row_grid(T), dim3(NT), 0, stream>>>(a);
-    else join_kernel<false><<<row_grid(T), dim3(NT), 0, stream>>>(a);
-    MOE_LAUNCH_CHECK("join_kernel");
-    return MOE_OK;
+    return launch_forward(a, x_type == MOE_SRC_F32, stream);
 }
 
 extern "C" int moe_norm_backward_workspace(int64_t T, int64_t d, size_t* bytes) {
@@ -478,17 +866,14 @@ extern "C" int moe_join(const uint16_t* y, int64_t ldy, const void* r, int32_t r
                 MOE_ERR_SHAPE, "join: y, r, weights, r_out and h: 16-byte aligned");
     JoinArgs a = {y, ldy, r, ldr, w_post, gate, w_pre, gate_kind, gate_kind == MOE_GATE_NONE ? MOE_ACT_NONE : gate_act,
                   w_type == MOE_SRC_F32, gate_type == MOE_SRC_F32, r_scale, y_scale, eps, T, d, r_out, h, rstd_post, rstd_pre};
-    if (r_type == MOE_SRC_F32) join_kernel<true><<<row_grid(T), dim3(NT), 0, stream>>>(a);
-    else join_kernel<false><<<row_grid(T), dim3(NT), 0, stream>>>(a);
-    MOE_LAUNCH_CHECK("join_kernel");
-    return MOE_OK;
+    return launch_forward(a, r_type == MOE_SRC_F32, stream);
 }
 
 extern "C" int moe_join_backward_workspace(int64_t T, int64_t d, size_t* bytes) {
     clear_error();
     MOE_REQUIRE(bytes, MOE_ERR_NULL, "join_backward_workspace: NULL bytes");
     if (const int rc = check_rows("join_backward_workspace", T, d)) return rc;
-    *bytes = backward_bytes(T, d, 3);
+    *bytes = backward_bytes(T, d, 2);
     return MOE_OK;
 }
 
@@ -505,7 +890,7 @@ extern "C" int moe_join_backward(const void* d_out, const uint16_t* dh, const ui
     MOE_REQUIRE(w_post || !dw_post, MOE_ERR_NULL, "join_backward: dw_post without w_post");
     MOE_REQUIRE(w_pre || !dw_pre, MOE_ERR_NULL, "join_backward: dw_pre without w_pre");
     MOE_REQUIRE(gate_kind != MOE_GATE_NONE || !dgate, MOE_ERR_NULL, "join_backward: dgate without a gate");
-    const int sums = (dw_post != nullptr) + (dw_pre != nullptr) + (dgate && gate_kind == MOE_GATE_CHANNEL);
+    const int sums = (dw_pre != nullptr) + (dw_post || (dgate && gate_kind == MOE_GATE_CHANNEL));
     if (T > 0) {
         MOE_REQUIRE(y && (d_out || dh), MOE_ERR_NULL, "join_backward: NULL y, or neither d_out nor dh");
         MOE_REQUIRE((w_pre != nullptr) == (dh != nullptr), MOE_ERR_NULL, "join_backward: dh goes with w_pre");
