@@ -1,6 +1,8 @@
 // Routing by scores: the choice of experts from softmax or sigmoid scores with a
 // balance bias and groups, its replay from a record, its gradient, and the update
 // of the bias.
+#include <type_traits>
+
 #include "common.hpp"
 #include "gate_parts.hpp"
 #include "route_keys.hpp"
@@ -15,10 +17,13 @@ struct ScoreArgs {
     const float* bias;
     int64_t T;
     int E, k, groups, top_groups, group_top;
+    bool renorm;
     float scale;
+    int lds_wave;     // floats of LDS for each wave
+    int inv_S;        // ceil(2^22 / (E / groups)): e * inv_S >> 22 is e's group
+    int group_slots;  // the power of two that holds the groups
     int32_t* ids;
     float* w;
-    int32_t* load;
     int32_t* rec;  // of this layer and first token
     int64_t rec_stride;
 };
@@ -42,12 +47,57 @@ __device__ __forceinline__ double wave_sum64(double v) {
     return v;
 }
 
+// A value of the lane that a butterfly step over LPR lanes pairs this one with.
+template <int CTRL>
+__device__ __forceinline__ float dpp32(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int STEP>
+__device__ __forceinline__ float partner(float v) {
+    if constexpr (STEP == 0) return dpp32<0xB1>(v);         // lane xor 1
+    else if constexpr (STEP == 1) return dpp32<0x4E>(v);    // lane xor 2
+    else if constexpr (STEP == 2) return dpp32<0x141>(v);   // mirrored in 8
+    else if constexpr (STEP == 3) return dpp32<0x140>(v);   // mirrored in 16
+    else return __shfl_xor(v, 16);
+}
+template <int STEP>
+__device__ __forceinline__ double partner(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const float lo = partner<STEP>(__uint_as_float((uint32_t)b)), hi = partner<STEP>(__uint_as_float((uint32_t)(b >> 32)));
+    return __builtin_bit_cast(double, ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo));
+}
+template <int LPR, typename T, typename F>
+__device__ __forceinline__ T team_reduce(T v, F&& f) {
+    v = f(v, partner<0>(v));
+    v = f(v, partner<1>(v));
+    v = f(v, partner<2>(v));
+    if constexpr (LPR >= 16) v = f(v, partner<3>(v));
+    if constexpr (LPR >= 32) v = f(v, partner<4>(v));
+    return v;
+}
+template <int LPR, typename T>
+__device__ __forceinline__ T team_sum(T v) {
+    return team_reduce<LPR>(v, [](T x, T y) { return x + y; });
+}
+template <int LPR>
+__device__ __forceinline__ float team_max(float v) {
+    return team_reduce<LPR>(v, [](float x, float y) { return fmaxf(x, y); });
+}
+
+// exp by the hardware's exp2: off by (2 |x| + 3) 2^-24 of itself at most (the
+// difference x, its product and exp2 are rounded).
+__device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
 // Maximum and sum of exponentials of a row that a wave holds, masked experts left
 // out. A NaN anywhere makes the sum NaN (fmaxf passes over it, exp does not).
+// EXACT: in 64 bits, for the choice. Otherwise the terms are exp32's, added in 64 bits,
+// for weights and gradients: the sum is off by (2 ln E + 3) 2^-24 of itself (the mean
+// |x| weighted by exp(x) is ln E at most), the same in every kernel, whatever the order
+// of its terms.
 struct RowStat {
     double m, inv;
 };
-template <bool F32, int VPL>
+template <bool F32, bool EXACT, int VPL>
 __device__ __forceinline__ RowStat row_stat(const float (&l)[VPL], int lane, int E) {
     float m = -INFINITY;
 #pragma unroll
@@ -57,7 +107,10 @@ __device__ __forceinline__ RowStat row_stat(const float (&l)[VPL], int lane, int
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (lane + 64 * i < E && !is_masked<F32>(l[i])) sum += exp((double)l[i] - (double)m);
+        if (lane + 64 * i < E && !is_masked<F32>(l[i])) {
+            if constexpr (EXACT) sum += exp((double)l[i] - (double)m);
+            else sum += (double)exp32(l[i] - m);
+        }
     sum = wave_sum64(sum);
     return {(double)m, sum == 0.0 ? 0.0 : 1.0 / sum};
 }
@@ -69,112 +122,438 @@ __device__ __forceinline__ double score(float l, RowStat st) {
 }
 
 // Weights of the chosen experts: lane j < k of a group of WIDTH lanes has logit l
-// (masked: the expert has no weight) and, without renorm, score s. Sums go in
-// ascending slot order.
-template <bool F32, bool SIGMOID, bool RENORM, int WIDTH>
-__device__ __forceinline__ double share(float l, double s, int lane, int k) {
-    if constexpr (!RENORM) return s;
+// (masked: the expert has no weight) and, without renorm, score s. The sum is a
+// butterfly over eight or sixteen lanes, zeros past the k-th: the same wherever the
+// slots stand in lanes of their own.
+template <bool F32, bool SIGMOID, int WIDTH>
+__device__ __forceinline__ double share(float l, double s, int lane, int k, bool renorm) {
+    if (!renorm) return s;
     if constexpr (!SIGMOID) {
         float m = lane < k && !is_masked<F32>(l) ? l : -INFINITY;
-        m = group_max<WIDTH>(m);
+        m = team_max<WIDTH>(m);
         s = is_masked<F32>(l) ? 0.0 : exp((double)l - (double)m);
     }
-    double sum = 0.0;
-    for (int j = 0; j < k; ++j) sum += __shfl(s, j, WIDTH);
+    const double sum = team_sum<WIDTH>(lane < k ? s : 0.0);
     return sum == 0.0 ? 0.0 : s / sum;
+}
+
+// Accesses of a wave's own LDS region before this point are done before those behind it.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ---------------------------------------------------------------- choice
 
-// One wave per token: lane l holds experts l, l + 64, ...; k rounds of a wave-wide
-// maximum over the keys of the groups that stay.
-template <bool F32, bool SIGMOID, bool RENORM, int VPL>
-__global__ __launch_bounds__(256) void score_topk_kernel(ScoreArgs a) {
-    __shared__ float group_c[4][64 * VPL];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int E = a.E, k = a.k;
-    for (int64_t row0 = (int64_t)blockIdx.x * 4; row0 < a.T; row0 += (int64_t)gridDim.x * 4) {
-        const int64_t row = row0 + wave;
-        const bool live = row < a.T;
-        const int64_t base = (live ? row : 0) * E;
-        float l[VPL];
+// One row by a whole wave, as it is defined: scores in 64 bits, rounded. Lane l holds
+// experts l, l + 64, ...; k rounds of a wave-wide maximum over the keys of the groups
+// that stay. lds: E floats of this wave. Rare where the kernel below calls it, and a
+// function of its own so that its registers are not the caller's.
+typedef const __attribute__((address_space(4))) ScoreArgs* KernelArgs;
+typedef __attribute__((address_space(3))) float* LdsFloats;
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+    return ((uint64_t)hi << 32) | lo;
+}
+template <bool F32, bool SIGMOID, int VPL>
+__device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_t row_, LdsFloats lds) {
+    const __attribute__((address_space(4))) ScoreArgs& a = *(KernelArgs)uniform((uint64_t)args);
+    const int64_t row = (int64_t)uniform((uint64_t)row_);
+    const int lane = threadIdx.x & 63, E = a.E, k = a.k;
+    const int64_t base = row * E;
+    float l[VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 64 * i;
-            l[i] = e < E ? logit<F32>(a.logits, base + e) : 0.f;
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 64 * i;
+        l[i] = e < E ? logit<F32>(a.logits, base + e) : 0.f;
+    }
+    RowStat st = {0.0, 0.0};
+    if constexpr (!SIGMOID) st = row_stat<F32, true, VPL>(l, lane, E);
+    uint64_t key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 64 * i;
+        key[i] = 0ull;
+        if (e < E) {
+            float c = (float)score<F32, SIGMOID>(l[i], st);
+            if (a.bias) c += a.bias[e];
+            if (is_masked<F32>(l[i])) c = -INFINITY;
+            key[i] = route_key(c, e);
+            if (a.groups > 1) lds[e] = c == c ? c : -INFINITY;
         }
-        RowStat st = {0.0, 0.0};
-        if constexpr (!SIGMOID) st = row_stat<F32, VPL>(l, lane, E);
-        uint64_t key[VPL];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 64 * i;
-            key[i] = 0ull;
-            if (e < E) {
-                float c = (float)score<F32, SIGMOID>(l[i], st);
-                if (a.bias) c += a.bias[e];
-                if (is_masked<F32>(l[i])) c = -INFINITY;
-                key[i] = route_key(c, e);
-                group_c[wave][e] = c == c ? c : -INFINITY;
+    }
+    if (a.groups > 1) {
+        wave_sync();
+        // 64 / GP lanes to a group, GP the power of two that holds the groups
+        int gp = 1;
+        while (gp < a.groups) gp <<= 1;
+        const int lpg = 64 / gp, S = E / a.groups;
+        const int g = lane / lpg, sub = lane % lpg;
+        float t1 = -INFINITY, t2 = -INFINITY;
+        if (g < a.groups) {
+            for (int i = sub; i < S; i += lpg) {
+                const float v = lds[g * S + i];
+                t2 = fmaxf(t2, fminf(t1, v));
+                t1 = fmaxf(t1, v);
             }
         }
+        for (int m = 1; m < lpg; m <<= 1) {
+            const float o1 = __shfl_xor(t1, m), o2 = __shfl_xor(t2, m);
+            t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+            t1 = fmaxf(t1, o1);
+        }
+        const float v = a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+        int ahead = 0;
+        for (int o = 0; o < a.groups; ++o) {
+            const float ov = __shfl(v, o * lpg);
+            ahead += (ov > v) | ((ov == v) & (o < g));
+        }
+        const uint64_t stay = __ballot(g < a.groups && ahead < a.top_groups);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane + 64 * i;
+            if (e < E && !((stay >> (e / S * lpg)) & 1ull)) key[i] = 0ull;
+        }
+        wave_sync();  // the next row's values
+    }
+    uint64_t thr = ~0ull, mine = 0ull;
+    for (int s = 0; s < k; ++s) {
+        uint64_t b = 0ull;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) b = (key[i] < thr && key[i] > b) ? key[i] : b;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) {
+            const uint64_t o = __shfl_xor(b, m);
+            b = o > b ? o : b;
+        }
+        thr = b;
+        if (lane == s) mine = b;
+    }
+    const int id = lane < k ? route_key_id(mine) : 0;
+    const float ls = logit<F32>(a.logits, base + id);
+    if constexpr (!SIGMOID)
+        if (!a.renorm) st = row_stat<F32, false, VPL>(l, lane, E);
+    const double h = share<F32, SIGMOID, 16>(ls, score<F32, SIGMOID>(ls, st), lane, k, a.renorm);
+    if (lane < k) {
+        a.ids[row * k + lane] = id;
+        a.w[row * k + lane] = (float)((double)a.scale * h);
+        if (a.rec) a.rec[(int64_t)lane * a.rec_stride + row] = id;
+    }
+}
+
+__device__ __forceinline__ KernelArgs kernel_args() { return (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(); }
+
+// Every row exactly: more groups that count than 32 lanes hold.
+template <bool F32, bool SIGMOID, int VPL>
+__global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
+    extern __shared__ float lds_all[];
+    const int wave = threadIdx.x >> 6;
+    for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < a.T; row += (int64_t)gridDim.x * 4)
+        choose_exactly<F32, SIGMOID, VPL>(kernel_args(), row, (LdsFloats)(lds_all + wave * a.lds_wave));
+}
+
+// Sorting networks over keys as doubles: one v_max_f64 and one v_min_f64 an exchange.
+template <int N>
+__device__ __forceinline__ void dclean(double* k) {  // a bitonic run, descending
+#pragma unroll
+    for (int s = N / 2; s >= 1; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if ((i & s) == 0) dce(k[i], k[i + s]);
+}
+template <int N>
+__device__ __forceinline__ void dsort(double* k) {
+    if constexpr (N == 8) dsort8(k);
+    else {
+        dce(k[0], k[1]);
+        dce(k[2], k[3]);
+        dce(k[0], k[2]);
+        dce(k[1], k[3]);
+        dce(k[1], k[2]);
+    }
+}
+// the N largest of two descending runs of N
+template <int N>
+__device__ __forceinline__ void dmerge(double* a, const double* b) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a[i] = __builtin_fmax(a[i], b[N - 1 - i]);
+    dclean<N>(a);
+}
+
+template <int STEP, int KT>
+__device__ __forceinline__ void merge_partner(double* g) {
+    double o[KT];
+#pragma unroll
+    for (int i = 0; i < KT; ++i) o[i] = partner<STEP>(g[i]);
+    dmerge<KT>(g, o);
+}
+
+// LPR lanes to a row, VPL logits to a lane (4 neighbours in every 4 LPR), k <= KT.
+//
+// The choice is defined by scores that are rounded from 64 bits, but 32 bits decide
+// nearly every row: with c' from the hardware's exp2 and reciprocal,
+//     |c' - c| <= margin(c') / 2,   margin(c) = A + B |c|,
+// the order of two experts whose c' are a margin apart is the order of their c. A row is
+// certain if its groups, its k picks among themselves and the last pick and every
+// expert behind it are; the others (a tie is one) are chosen anew by the whole wave.
+// Errors, u = 2^-24: exp2 and reciprocal are good to 2 u; a sigmoid score s is off by
+// s (1 - s) |l| u 3/2 (the argument's roundings) + 6 u s, a softmax score by
+// s (2 |l - m| + 2 ln E + 10) u (its own exp32 and the sum's).
+// Bias NULL: c = s, and A = 0, B = 32 u + 8 u |l| resp. 128 u + 16 u |l - m| with the
+// pick's own l (s |l| only falls behind it). With a bias: A = 16 u resp. 64 u max(s),
+// and B = 8 u for the two sums' roundings. A group's value is a sum of two: twice A and B.
+// Keys: c' as a double with the expert's id in the bits that 32-bit values leave
+// zero. A lane passes on its KT / 2 largest; a lane whose last passed one could
+// still be a pick makes the row uncertain.
+template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
+__global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
+    extern __shared__ float lds_all[];
+    constexpr int ROWS = 64 / LPR, LK = KT / 2, N4 = VPL / 4;
+    constexpr float U = 5.9604644775390625e-8f, LOW = -3.402823466e38f;
+    const int lane = threadIdx.x & 63, team = lane / LPR, wave = threadIdx.x >> 6;
+    const int k = a.k, S = a.E / a.groups;
+    float* lds = lds_all + wave * a.lds_wave;
+    const bool vec = (a.E & 3) == 0;
+    const int E = a.E;
+    int p = lane & (LPR - 1);
+    const int64_t step = (int64_t)gridDim.x * 4 * ROWS;
+    for (int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * ROWS; row0 < a.T; row0 += step) {
+        // what follows from these is made anew for each row: it would not fit the registers
+        asm volatile("" : "+v"(p));
+        const int64_t row = row0 + team;
+        const bool live = row < a.T;
+        const int64_t base = (live ? row : row0) * E;
+        float c[VPL];
+        if (vec) {
+#pragma unroll
+            for (int j = 0; j < N4; ++j) {
+                const int e = 4 * LPR * j + 4 * p;
+                float4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (e < E) {
+                    if constexpr (F32) {
+                        q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + e);
+                    } else {
+                        const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + base + e);
+                        q = {bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y)};
+                    }
+                }
+                c[4 * j] = q.x, c[4 * j + 1] = q.y, c[4 * j + 2] = q.z, c[4 * j + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
+                c[i] = e < E ? logit<F32>(a.logits, base + e) : -INFINITY;
+            }
+        }
+        // c' of experts, LOW for masked ones, NaN and none
+        float A = 0.f, m = 0.f;
+        double sum = 1.0;
+        if constexpr (!SIGMOID) {
+            m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                c[i] = is_masked<F32>(c[i]) ? -INFINITY : c[i];
+                m = fmaxf(m, c[i]);
+            }
+            m = team_max<LPR>(m);
+            m = m == -INFINITY ? 0.f : m;
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const float v = exp32(c[i] - m);
+                sum += (double)v;
+                c[i] = c[i] == -INFINITY ? LOW : v;
+            }
+            sum = team_sum<LPR>(sum);
+            const float inv = sum == 0.0 ? 0.f : 1.0f / (float)sum;
+            if (a.bias) A = 64.f * U * inv;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) c[i] = c[i] == LOW ? LOW : c[i] * inv;
+        } else {
+            if (a.bias) A = 16.f * U;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[i] * -1.4426950408889634f));
+                c[i] = is_masked<F32>(c[i]) ? LOW : s;
+            }
+        }
+        if (a.bias) {
+#pragma unroll
+            for (int j = 0; j < N4; ++j) {
+                const int e = 4 * LPR * j + 4 * p;
+                float4 q = {0.f, 0.f, 0.f, 0.f};
+                if (vec) {
+                    if (e < E) q = *reinterpret_cast<const float4*>(a.bias + e);
+                } else {
+                    if (e < E) q.x = a.bias[e];
+                    if (e + 1 < E) q.y = a.bias[e + 1];
+                    if (e + 2 < E) q.z = a.bias[e + 2];
+                    if (e + 3 < E) q.w = a.bias[e + 3];
+                }
+                const float b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[4 * j + i] = c[4 * j + i] == LOW ? LOW : c[4 * j + i] + b[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_fmed3f(c[i], LOW, -LOW);
+        bool unsure = false;
         if (a.groups > 1) {
-            __syncthreads();
-            // 64 / GP lanes to a group, GP the power of two that holds the groups
-            int gp = 1;
-            while (gp < a.groups) gp <<= 1;
-            const int lpg = 64 / gp, S = E / a.groups;
-            const int g = lane / lpg, sub = lane % lpg;
-            float t1 = -INFINITY, t2 = -INFINITY;
-            if (g < a.groups) {
-                for (int i = sub; i < S; i += lpg) {
-                    const float v = group_c[wave][g * S + i];
-                    t2 = fmaxf(t2, fminf(t1, v));
-                    t1 = fmaxf(t1, v);
+            const int SP = S + ((12 - (S & 7)) & 7);  // a group's stride: 4 more than a multiple of 8
+            float* mine = lds + team * (a.groups * SP);
+            const bool quads = (S & 3) == 0;
+            if (quads) {
+#pragma unroll
+                for (int j = 0; j < N4; ++j) {
+                    const int e = 4 * LPR * j + 4 * p;
+                    if (e < E)
+                        *reinterpret_cast<float4*>(mine + e + (int)((uint32_t)(e * a.inv_S) >> 22) * (SP - S)) =
+                            float4{c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]};
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
+                    if (e < E) mine[e + (int)((uint32_t)(e * a.inv_S) >> 22) * (SP - S)] = c[i];
                 }
             }
-            for (int m = 1; m < lpg; m <<= 1) {
-                const float o1 = __shfl_xor(t1, m), o2 = __shfl_xor(t2, m);
+            wave_sync();
+            const int lpg = LPR / a.group_slots, g = p / lpg, sub = p - g * lpg;
+            float t1 = LOW, t2 = LOW;
+            auto take = [&](float v) {
+                t2 = __builtin_amdgcn_fmed3f(t1, t2, v);
+                t1 = fmaxf(t1, v);
+            };
+            if (g < a.groups) {
+                const float* q = mine + g * SP;
+                if (quads) {
+#pragma unroll 4
+                    for (int i = 4 * sub; i < S; i += 4 * lpg) {
+                        const float4 v = *reinterpret_cast<const float4*>(q + i);
+                        take(v.x), take(v.y), take(v.z), take(v.w);
+                    }
+                } else {
+                    for (int i = sub; i < S; i += lpg) take(q[i]);
+                }
+            }
+            for (int x = 1; x < lpg; x <<= 1) {
+                const float o1 = __shfl_xor(t1, x), o2 = __shfl_xor(t2, x);
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
                 t1 = fmaxf(t1, o1);
             }
-            const float v = a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
+            const float v = a.group_top == 2 && t2 > LOW ? t1 + t2 : t1;
             int ahead = 0;
             for (int o = 0; o < a.groups; ++o) {
-                const float ov = __shfl(v, o * lpg);
+                const float ov = __shfl(v, o * lpg, LPR);
                 ahead += (ov > v) | ((ov == v) & (o < g));
             }
-            const uint64_t stay = __ballot(g < a.groups && ahead < a.top_groups);
+            const bool stays = g < a.groups && ahead < a.top_groups;
+            const float least = -team_max<LPR>(stays ? -v : LOW);
+            const float next = team_max<LPR>(g < a.groups && !stays ? v : LOW);
+            // without a bias: the largest error that B can stand for at this value
+            const float B = a.bias ? 16.f * U : SIGMOID ? 2.f * (32.f + 8.f * 104.f) * U : 2.f * (128.f + 16.f * 104.f) * U;
+            unsure = !(least - next > 2.f * A + B * fmaxf(fabsf(least), fabsf(next)));
+            const uint32_t stay = (uint32_t)(__ballot(stays) >> (team * LPR));
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = lane + 64 * i;
-                if (e < E && !((stay >> (e / S * lpg)) & 1ull)) key[i] = 0ull;
+            for (int j = 0; j < N4; ++j) {
+                const int e = 4 * LPR * j + 4 * p;
+                if (quads) {
+                    const bool out = !((stay >> ((uint32_t)(e * a.inv_S) >> 22) * lpg) & 1u);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[4 * j + i] = out ? LOW : c[4 * j + i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!((stay >> ((uint32_t)((e + i) * a.inv_S) >> 22) * lpg) & 1u)) c[4 * j + i] = LOW;
+                }
             }
-            __syncthreads();  // the next row's values
+            wave_sync();  // the next row's values
         }
-        uint64_t thr = ~0ull, mine = 0ull;
-        for (int s = 0; s < k; ++s) {
-            uint64_t b = 0ull;
+        // the lane's LK largest keys, run by run
+        double key[LK];
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) b = (key[i] < thr && key[i] > b) ? key[i] : b;
+        for (int r = 0; r < VPL; r += LK) {
+            double run[LK];
 #pragma unroll
-            for (int m = 32; m >= 1; m >>= 1) {
-                const uint64_t o = __shfl_xor(b, m);
-                b = o > b ? o : b;
+            for (int i = 0; i < LK; ++i) {
+                const uint64_t b = __builtin_bit_cast(uint64_t, (double)c[r + i]);
+                run[i] = __builtin_bit_cast(double, b | (uint32_t)(4 * LPR * ((r + i) >> 2) + 4 * p + (i & 3)));
             }
-            thr = b;
-            if (lane == s) mine = b;
+            dsort<LK>(run);
+            if (r == 0) {
+#pragma unroll
+                for (int i = 0; i < LK; ++i) key[i] = run[i];
+            } else {
+                dmerge<LK>(key, run);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const int id = lane < k ? route_key_id(mine) : 0;
-        const float ls = logit<F32>(a.logits, base + id);
-        const double h = share<F32, SIGMOID, RENORM, 64>(ls, score<F32, SIGMOID>(ls, st), lane, k);
-        if (live && lane < k) {
-            a.ids[row * k + lane] = id;
-            a.w[row * k + lane] = (float)((double)a.scale * h);
-            if (a.rec) a.rec[(int64_t)lane * a.rec_stride + row] = id;
-            if (a.load) atomicAdd(a.load + id, 1);
+        double top[KT];
+        // both lanes' passed keys whole: the larger and the smaller halves of a bitonic run
+#pragma unroll
+        for (int i = 0; i < LK; ++i) {
+            const double o = partner<0>(key[LK - 1 - i]);
+            top[i] = __builtin_fmax(key[i], o);
+            top[LK + i] = __builtin_fmin(key[i], o);
         }
+        dclean<LK>(top);
+        dclean<LK>(top + LK);
+        merge_partner<1, KT>(top);
+        merge_partner<2, KT>(top);
+        if constexpr (LPR >= 16) merge_partner<3, KT>(top);
+        if constexpr (LPR >= 32) merge_partner<4, KT>(top);
+        // lane j has pick j
+        double mine = top[0];
+#pragma unroll
+        for (int i = 1; i < KT; ++i) mine = p == i ? top[i] : mine;
+        const float v = (float)mine;
+        const int id = (int)((uint32_t)__builtin_bit_cast(uint64_t, mine) & 1023u);
+        const float l = logit<F32>(a.logits, base + (id < E ? id : 0));
+        float margin;
+        if constexpr (SIGMOID) margin = a.bias ? A + 8.f * U * fabsf(v) : (32.f + 8.f * fminf(fabsf(l), 104.f)) * U * v;
+        else margin = a.bias ? A + 8.f * U * fabsf(v) : (128.f + 16.f * fminf(fabsf(l - m), 104.f)) * U * v;
+        const float next = dpp32<0x101>(v), next_margin = dpp32<0x101>(margin);  // of lane + 1 in its 16
+        if (p < k - 1) unsure |= !(v - next > fmaxf(margin, next_margin));
+        if (p == k - 1) unsure |= !(v > 0.5f * LOW);
+        const float bar = __shfl(v - margin, k - 1, LPR);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < LK; ++i) n += (float)key[i] >= bar;
+        if (VPL > LK) unsure |= n == LK;
+        unsure |= team_sum<LPR>((float)n) != (float)k;
+        const uint64_t unsure_all = __ballot(unsure && live);
+        constexpr uint64_t TEAM = LPR == 64 ? ~0ull : (1ull << LPR) - 1;
+        if (live && !((unsure_all >> (team * LPR)) & TEAM)) {
+            RowStat st = {(double)m, 0.0};
+            if constexpr (!SIGMOID) st.inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+            const double s = a.renorm && !SIGMOID ? 0.0 : score<F32, SIGMOID>(l, st);
+            const double h = share<F32, SIGMOID, (LPR < 16 ? LPR : 16)>(l, s, p, k, a.renorm);
+            if (p < k) {
+                a.ids[row * k + p] = id;
+                a.w[row * k + p] = (float)((double)a.scale * h);
+                if (a.rec) a.rec[(int64_t)p * a.rec_stride + row] = id;
+            }
+        }
+        if (unsure_all == 0) continue;
+        for (int t = 0; t < ROWS; ++t)
+            if ((unsure_all >> (t * LPR)) & TEAM)
+                choose_exactly<F32, SIGMOID, (LPR * VPL + 63) / 64>(kernel_args(), row0 + t, (LdsFloats)lds);
     }
+}
+
+// load[e] += how often e stands in ids, counted in LDS first.
+__global__ __launch_bounds__(1024) void score_load_kernel(const int32_t* ids, int64_t n, int E, int32_t* load) {
+    __shared__ int32_t count[MAX_E];
+    for (int e = threadIdx.x; e < E; e += 1024) count[e] = 0;
+    __syncthreads();
+    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024)
+        atomicAdd(&count[ids[i]], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 1024)
+        if (count[e]) atomicAdd(load + e, count[e]);
 }
 
 // ---------------------------------------------------------------- replay
@@ -199,7 +578,7 @@ __global__ __launch_bounds__(256) void score_replay_kernel(ScoreArgs a, int32_t*
             dup |= __shfl_xor(dup, m, 16);
         }
         const float l = logit<F32>(a.logits, t * E + (bad ? 0 : id));
-        const double h = share<F32, SIGMOID, RENORM, 16>(l, score<F32, SIGMOID>(l, RowStat{0.0, 0.0}), lane, k);
+        const double h = share<F32, SIGMOID, 16>(l, score<F32, SIGMOID>(l, RowStat{0.0, 0.0}), lane, k, RENORM);
         if (live && lane < k) {
             a.ids[row * k + lane] = id;
             a.w[row * k + lane] = bad ? 0.f : (float)((double)a.scale * h);
@@ -221,7 +600,7 @@ __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int3
             const int e = lane + 64 * i;
             l[i] = e < E ? logit<F32>(a.logits, row * E + e) : 0.f;
         }
-        const RowStat st = row_stat<F32, VPL>(l, lane, E);
+        const RowStat st = row_stat<F32, false, VPL>(l, lane, E);
         const int id = lane < k ? a.rec[(int64_t)lane * a.rec_stride + row] : 0;
         const bool bad = __ballot(lane < k && (id < 0 || id >= E)) != 0;
         bool dup = false;
@@ -284,11 +663,11 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
                 const int e = lane + 64 * i;
                 l[i] = e < E ? logit<F32>(a.logits, row * E + e) : 0.f;
             }
-            st = row_stat<F32, VPL>(l, lane, E);
+            st = row_stat<F32, false, VPL>(l, lane, E);
         }
         const float ls = logit<F32>(a.logits, row * E + (bad ? 0 : id));
         const double s = score<F32, SIGMOID>(ls, st);
-        const double h = share<F32, SIGMOID, RENORM, 64>(ls, s, lane, k);
+        const double h = share<F32, SIGMOID, 16>(ls, s, lane, k, RENORM);
         double dot = 0.0;
         if constexpr (RENORM || !SIGMOID) {
             const double p = h * (double)dw;
@@ -376,6 +755,56 @@ void with_vpl(int E, F&& f) {
     else f(std::integral_constant<int, 16>{});
 }
 
+template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
+void launch_topk(ScoreArgs a, hipStream_t stream) {
+    constexpr int ROWS = 64 / LPR;
+    if (a.groups > 1) {
+        const int S = a.E / a.groups, SP = S + ((12 - (S & 7)) & 7);
+        a.lds_wave = ROWS * a.groups * SP;
+    }
+    score_topk_kernel<F32, SIGMOID, LPR, VPL, KT>
+        <<<row_blocks(a.T, 4 * ROWS), 256, (size_t)a.lds_wave * 4 * sizeof(float), stream>>>(a);
+}
+
+// The lanes of a row hold its logits, and its groups one each at least.
+template <bool F32, bool SIGMOID>
+void launch_choice_of(ScoreArgs a, hipStream_t stream) {
+    const int E = a.E, G = a.groups;
+    const int S = E / G;
+    a.inv_S = ((1 << 22) + S - 1) / S;
+    a.group_slots = 1;
+    while (a.group_slots < G) a.group_slots <<= 1;
+    if (G > 32) {
+        a.lds_wave = E;
+        with_vpl(E, [&](auto v) {
+            score_topk_exact_kernel<F32, SIGMOID, v.value>
+                <<<row_blocks(a.T, 4), 256, (size_t)a.lds_wave * 4 * sizeof(float), stream>>>(a);
+        });
+    } else if (G <= 8 && a.k <= 8 && E <= 256) {
+        if (E <= 64) launch_topk<F32, SIGMOID, 8, 8, 8>(a, stream);
+        else if (E <= 128) launch_topk<F32, SIGMOID, 8, 16, 8>(a, stream);
+        else launch_topk<F32, SIGMOID, 8, 32, 8>(a, stream);
+    } else if (G <= 16 && E <= 512) {
+        if (E <= 128) launch_topk<F32, SIGMOID, 16, 8, 16>(a, stream);
+        else if (E <= 256) launch_topk<F32, SIGMOID, 16, 16, 16>(a, stream);
+        else if (a.k <= 8) launch_topk<F32, SIGMOID, 16, 32, 8>(a, stream);
+        else launch_topk<F32, SIGMOID, 16, 32, 16>(a, stream);
+    } else {
+        if (a.k <= 8) launch_topk<F32, SIGMOID, 32, 32, 8>(a, stream);
+        else launch_topk<F32, SIGMOID, 32, 32, 16>(a, stream);
+    }
+}
+void launch_choice(const ScoreArgs& a, int32_t type, int32_t score, hipStream_t stream) {
+    const bool sig = score == MOE_SCORE_SIGMOID;
+    if (type == MOE_SRC_F32) {
+        if (sig) launch_choice_of<true, true>(a, stream);
+        else launch_choice_of<true, false>(a, stream);
+    } else {
+        if (sig) launch_choice_of<false, true>(a, stream);
+        else launch_choice_of<false, false>(a, stream);
+    }
+}
+
 int launch_backward(ScoreGradArgs a, int32_t type, int32_t score, int32_t renorm, bool parts, hipStream_t stream) {
     with_forms(type, score, renorm, [&](auto t, auto s, auto r) {
         with_vpl(a.E, [&](auto v) {
@@ -415,15 +844,28 @@ extern "C" int moe_route_scored(const void* logits, int32_t logits_type, int64_t
     if (T == 0) return MOE_OK;
     MOE_REQUIRE(logits && ids && w, MOE_ERR_NULL, "route_scored: NULL logits/ids/w");
     MOE_REQUIRE(aligned16(logits), MOE_ERR_SHAPE, "route_scored: logits: 16-byte aligned");
-    ScoreArgs a = {logits, bias, T, E, k, groups, top_groups == groups ? 1 : top_groups, group_top, scale, ids, w, load,
-                   rec ? rec + (int64_t)layer * k * seq_len + s0 : nullptr, seq_len};
-    if (top_groups == groups) a.groups = 1;  // every group stays
-    with_forms(logits_type, score, renorm, [&](auto t, auto s, auto r) {
-        with_vpl(E, [&](auto v) {
-            score_topk_kernel<t.value, s.value, r.value, v.value><<<row_blocks(T, 4), 256, 0, stream>>>(a);
-        });
-    });
+    ScoreArgs a = {};
+    a.logits = logits;
+    a.bias = bias;
+    a.T = T;
+    a.E = E;
+    a.k = k;
+    a.groups = top_groups == groups ? 1 : groups;  // every group stays
+    a.top_groups = top_groups;
+    a.group_top = group_top;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.ids = ids;
+    a.w = w;
+    a.rec = rec ? rec + (int64_t)layer * k * seq_len + s0 : nullptr;
+    a.rec_stride = seq_len;
+    launch_choice(a, logits_type, score, stream);
     MOE_LAUNCH_CHECK("score_topk_kernel");
+    if (load) {
+        const int64_t n = T * k, blocks = (n + 16383) / 16384;
+        score_load_kernel<<<dim3((unsigned)(blocks < 32 ? blocks : 32)), dim3(1024), 0, stream>>>(ids, n, E, load);
+        MOE_LAUNCH_CHECK("score_load_kernel");
+    }
     return MOE_OK;
 }
 

@@ -4,14 +4,27 @@ Bounds: weights and gradients are computed in 64 bits from a token's own
 logits and rounded once, so a value v is off by at most 2^-24 |v| in fp32
 (2^-8 |v| in bf16, 2^-24 more for the way through fp32), by half the smallest
 step where it is subnormal (steps of 2^-149 in fp32, of 2^-126 / 2^7 = 2^-133 in
-bf16: 2^-134, and 2^-150 more for the way through fp32), and 2^-46 of the terms it is a difference of (some 20 roundings of
-2^-53 and exp's few ulps)."""
+bf16: 2^-134, and 2^-150 more for the way through fp32), and by 2^-46 of the terms
+it is a difference of (some 20 roundings of 2^-53 and exp's few ulps).
+
+Softmax scores that are not renormalised divide by a sum over the whole row, whose
+terms exp(x), x = l - m <= 0, are 32-bit ones: the difference x, its product with
+log2 e and the hardware's exp2 (good to one ulp, 2 u with u = 2^-24) make a term off
+by at most (2 |x| + 3) u of itself; the sum (in 64 bits) is then off by the mean of
+that weighted with exp(x) / sum, and the mean |x| is ln E at most (it is the
+distribution's entropy less ln sum): (2 ln E + 3) u (row_err). A gradient's own score
+is such a term over such a sum: (2 |x| + 2 ln E + 6) u."""
 
 import numpy as np
 
 LOWEST = {"f32": -3.4028234663852886e38, "bf16": -3.3895313892515355e38}
 ROUND = {"f32": 2.0 ** -24 * 1.001, "bf16": (2.0 ** -8 + 2.0 ** -24) * 1.001}
 TINY = {"f32": 2.0 ** -149, "bf16": 2.0 ** -134 + 2.0 ** -150}
+U = 2.0 ** -24
+
+
+def row_err(E, score, renorm):
+    return (2 * np.log(E) + 3) * U if score == "softmax" and not renorm else 0.0
 
 
 def masked(l, kind):
@@ -95,4 +108,8 @@ def gradient(l, s, kind, ids, d_w, score, renorm, scale):
     if score == "softmax" and not renorm:
         out -= s * scale * dot
         big += s * scale * np.abs(share * d_w).sum(axis=1, keepdims=True)
+        # in units of the 2^-46 that the callers allow: the chosen scores and the row's own
+        off = masked(l, kind)
+        x = np.where(off, 0.0, l.max(axis=1, keepdims=True) - np.where(off, 0.0, l))
+        big *= 1.0 + 2.0 ** 46 * (2 * x + 4 * np.log(E) + 12) * U
     return out, np.abs(big)

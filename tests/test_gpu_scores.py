@@ -64,7 +64,7 @@ def check_route(T, E, k, score, kind="f32", special="", bias=False, groups=1, to
     ref = R.choice(l, s, kind, k, None if b is None else npi(b), groups, top_groups, group_top)
     assert np.array_equal(npi(ids), ref), "ids"
     rw, _ = R.weights(l, s, kind, ref, score, renorm, scale)
-    close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"] + 2.0 ** -46 * abs(scale) * (rw != 0), "w")
+    close(w, rw, (R.ROUND["f32"] + R.row_err(E, score, renorm)) * np.abs(rw) + R.TINY["f32"] + 2.0 ** -46 * abs(scale) * (rw != 0), "w")
     want = np.full((3, k, T + 9), -7, dtype=np.int32)
     want[1, :, 4:4 + T] = ref.T
     assert np.array_equal(npi(rec), want), "record"
@@ -183,7 +183,7 @@ def test_replay(score, renorm, E, k):
     safe = np.where(good[:, None], ref, 0)
     rw, _ = R.weights(l, s, "f32", safe, score, renorm, 2.0)
     rw = np.where(good[:, None], rw, 0.0)
-    close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"], "w")
+    close(w, rw, (R.ROUND["f32"] + R.row_err(E, score, renorm)) * np.abs(rw) + R.TINY["f32"], "w")
     d_w = torch.tensor(rng.standard_normal((T, k)).astype(np.float32)).to(DEV)
     g, size = R.gradient(l, s, "f32", safe, np64(d_w), score, renorm, 2.0)
     g[~good], size[~good] = 0.0, 0.0
