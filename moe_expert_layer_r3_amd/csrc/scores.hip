@@ -19,9 +19,10 @@ struct ScoreArgs {
     int E, k, groups, top_groups, group_top;
     bool renorm;
     float scale;
-    int lds_wave;     // floats of LDS for each wave
-    int inv_S;        // ceil(2^22 / (E / groups)): e * inv_S >> 22 is e's group
-    int group_slots;  // the power of two that holds the groups
+    int lds_wave, lds_row;     // floats of LDS for each wave, and for each of its rows
+    int inv_S;                 // ceil(2^22 / (E / groups)): e * inv_S >> 22 is e's group
+    int group_bits, lpr_bits;  // logarithms of the power of two that holds the groups, and of a row's lanes
+    int spread, spread_mod;    // first four that a group's lanes read: group * spread mod spread_mod
     int32_t* ids;
     float* w;
     int32_t* rec;  // of this layer and first token
@@ -254,73 +255,117 @@ __global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
         choose_exactly<F32, SIGMOID, VPL>(kernel_args(), row, (LdsFloats)(lds_all + wave * a.lds_wave));
 }
 
-// Sorting networks over keys as doubles: one v_max_f64 and one v_min_f64 an exchange.
+// Sorting networks over keys as doubles: one v_max_f64 and one v_min_f64 an exchange
+// (written out: the compiler would make each key canonical first, which they are).
+__device__ __forceinline__ double kmax(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double kmin(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ void exchange(double& a, double& b) {
+    const double x = a, y = b;
+    a = kmax(x, y);
+    b = kmin(x, y);
+}
 template <int N>
-__device__ __forceinline__ void dclean(double* k) {  // a bitonic run, descending
+__device__ __forceinline__ void sort_bitonic(double* k) {  // descending
 #pragma unroll
     for (int s = N / 2; s >= 1; s >>= 1)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if ((i & s) == 0) dce(k[i], k[i + s]);
+            if ((i & s) == 0) exchange(k[i], k[i + s]);
 }
 template <int N>
-__device__ __forceinline__ void dsort(double* k) {
-    if constexpr (N == 8) dsort8(k);
-    else {
-        dce(k[0], k[1]);
-        dce(k[2], k[3]);
-        dce(k[0], k[2]);
-        dce(k[1], k[3]);
-        dce(k[1], k[2]);
-    }
+__device__ __forceinline__ void sort_keys(double* k) {  // Batcher's odd-even merge sort
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i <= (q - 1 < N - 1 - j - q ? q - 1 : N - 1 - j - q); ++i)
+                    if ((i + j) / (2 * p) == (i + j + q) / (2 * p)) exchange(k[i + j], k[i + j + q]);
 }
 // the N largest of two descending runs of N
 template <int N>
-__device__ __forceinline__ void dmerge(double* a, const double* b) {
+__device__ __forceinline__ void merge_keys(double* a, const double* b) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) a[i] = __builtin_fmax(a[i], b[N - 1 - i]);
-    dclean<N>(a);
+    for (int i = 0; i < N; ++i) a[i] = kmax(a[i], b[N - 1 - i]);
+    sort_bitonic<N>(a);
 }
-
 template <int STEP, int KT>
 __device__ __forceinline__ void merge_partner(double* g) {
     double o[KT];
 #pragma unroll
     for (int i = 0; i < KT; ++i) o[i] = partner<STEP>(g[i]);
-    dmerge<KT>(g, o);
+    merge_keys<KT>(g, o);
+}
+
+// Two distances, u = 2^-24 and the hardware's exp2 and reciprocal good to 2 u, that
+// decide what order 32 bits are certain of.
+constexpr float U = 5.9604644775390625e-8f, LOW = -3.402823466e38f;
+// Logits at least this far apart, the larger one l: their scores, exact, differ by more
+// than two roundings to 32 bits (a softmax score by a factor exp(l - l'), a sigmoid one by
+// 1 + (1 - s)(l - l'), 1 - s = 1 / (1 + exp(l))). Where scores leave the normal
+// range, infinite: nothing is certain there.
+template <bool SIGMOID>
+__device__ __forceinline__ float logit_margin(float l, float top) {
+    if constexpr (SIGMOID) return l < -80.f ? INFINITY : 8.f * U * (1.0f + exp32(l));
+    else return l < top - 60.f || top == -LOW ? INFINITY : 8.f * U;
+}
+// c' = s' + bias at least this far apart, s' scores up to s_max: s' is off by
+// s (1 - s) |l| u 3/2 (the argument's roundings) + 6 u s <= 6.4 u (sigmoid) or
+// s (2 |l - m| + 2 ln E + 10) u <= 25 u s_max (softmax: s |l - m| <= s_max / e); the sums' and the
+// definition's own roundings are 2 u |c| each side.
+template <bool SIGMOID>
+__device__ __forceinline__ float choice_margin(float c, float s_max) {
+    return (SIGMOID ? 16.f * U : 64.f * U * s_max) + 8.f * U * fabsf(c);
+}
+// A group's two scores s' without a bias, relative to their sum: off by (1 - s) |l| u 3/2 + 6 u
+// or (2 |l - m| + 2 ln E + 10) u each, |l| up to 80, and one more rounding. Tiny sums, infinite.
+template <bool SIGMOID>
+__device__ __forceinline__ float group_margin(float v) {
+    return v < 1e-30f ? INFINITY : (SIGMOID ? 400.f : 512.f) * U * v;
 }
 
 // LPR lanes to a row, VPL logits to a lane (4 neighbours in every 4 LPR), k <= KT.
 //
 // The choice is defined by scores that are rounded from 64 bits, but 32 bits decide
-// nearly every row: with c' from the hardware's exp2 and reciprocal,
-//     |c' - c| <= margin(c') / 2,   margin(c) = A + B |c|,
-// the order of two experts whose c' are a margin apart is the order of their c. A row is
-// certain if its groups, its k picks among themselves and the last pick and every
-// expert behind it are; the others (a tie is one) are chosen anew by the whole wave.
-// Errors, u = 2^-24: exp2 and reciprocal are good to 2 u; a sigmoid score s is off by
-// s (1 - s) |l| u 3/2 (the argument's roundings) + 6 u s, a softmax score by
-// s (2 |l - m| + 2 ln E + 10) u (its own exp32 and the sum's).
-// Bias NULL: c = s, and A = 0, B = 32 u + 8 u |l| resp. 128 u + 16 u |l - m| with the
-// pick's own l (s |l| only falls behind it). With a bias: A = 16 u resp. 64 u max(s),
-// and B = 8 u for the two sums' roundings. A group's value is a sum of two: twice A and B.
-// Keys: c' as a double with the expert's id in the bits that 32-bit values leave
-// zero. A lane passes on its KT / 2 largest; a lane whose last passed one could
-// still be a pick makes the row uncertain.
-template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
+// nearly every row. With a bias the experts are ordered by c' = s' + bias from the
+// hardware's exp2 and reciprocal, without one by their logits (which no rounding
+// touches: equal logits have equal scores, and the id decides). A row is certain if
+// its groups, its k picks among themselves and the last pick and every expert
+// behind it are the margins above apart; the others are chosen anew by the whole wave.
+// Keys: c' or the logit as a double with the id in the bits that 32-bit values leave
+// zero. A lane passes on its 8 largest; one whose last passed key comes near the last
+// pick makes the row uncertain.
+template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int KT>
 __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
-    constexpr int ROWS = 64 / LPR, LK = KT / 2, N4 = VPL / 4;
-    constexpr float U = 5.9604644775390625e-8f, LOW = -3.402823466e38f;
+    constexpr int ROWS = 64 / LPR, LK = 8, N4 = VPL / 4;
     const int lane = threadIdx.x & 63, team = lane / LPR, wave = threadIdx.x >> 6;
     const int k = a.k, S = a.E / a.groups;
     float* lds = lds_all + wave * a.lds_wave;
     const bool vec = (a.E & 3) == 0;
     const int E = a.E;
     int p = lane & (LPR - 1);
+    // groups of whole fours: the group of each four, five bits each
+    const bool quads = (S & 3) == 0;
+    uint32_t group_of[(N4 + 5) / 6];
+#pragma unroll
+    for (int i = 0; i < (N4 + 5) / 6; ++i) group_of[i] = 0;
+#pragma unroll
+    for (int j = 0; j < N4; ++j)
+        group_of[j / 6] |= ((uint32_t)((4 * LPR * j + 4 * p) * a.inv_S) >> 22 & 31u) << (5 * (j % 6));
     const int64_t step = (int64_t)gridDim.x * 4 * ROWS;
     for (int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * ROWS; row0 < a.T; row0 += step) {
-        // what follows from these is made anew for each row: it would not fit the registers
+        // what follows from this is made anew for each row: it would not fit the registers
         asm volatile("" : "+v"(p));
         const int64_t row = row0 + team;
         const bool live = row < a.T;
@@ -330,8 +375,8 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
 #pragma unroll
             for (int j = 0; j < N4; ++j) {
                 const int e = 4 * LPR * j + 4 * p;
-                float4 q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (e < E) {
+                float4 q = {LOW, LOW, LOW, LOW};
+                if (4 * LPR * (j + 1) <= E || e < E) {
                     if constexpr (F32) {
                         q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + e);
                     } else {
@@ -345,48 +390,51 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                c[i] = e < E ? logit<F32>(a.logits, base + e) : -INFINITY;
+                c[i] = e < E ? logit<F32>(a.logits, base + e) : LOW;
             }
         }
-        // c' of experts, LOW for masked ones, NaN and none
-        float A = 0.f, m = 0.f;
+        // LOW for masked experts (and none); a NaN stays one for now
+        float least = c[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) least = fminf(least, c[i]);
+        const bool some_masked = __ballot(is_masked<F32>(least)) != 0;
+        if (some_masked) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) c[i] = is_masked<F32>(c[i]) ? LOW : c[i];
+        }
+        bool unsure = false;
+        float m = 0.f, s_max = 1.f;
         double sum = 1.0;
         if constexpr (!SIGMOID) {
-            m = -INFINITY;
+            m = LOW;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                c[i] = is_masked<F32>(c[i]) ? -INFINITY : c[i];
-                m = fmaxf(m, c[i]);
-            }
+            for (int i = 0; i < VPL; ++i) m = fmaxf(m, c[i]);
             m = team_max<LPR>(m);
-            m = m == -INFINITY ? 0.f : m;
-            sum = 0.0;
+            if (BIAS || !a.renorm) {
+                sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const float v = exp32(c[i] - m);
-                sum += (double)v;
-                c[i] = c[i] == -INFINITY ? LOW : v;
+                for (int i = 0; i < VPL; ++i) sum += c[i] == LOW ? 0.0 : (double)exp32(c[i] - m);
+                sum = team_sum<LPR>(sum);
+                s_max = sum == 0.0 ? 0.f : 1.0f / (float)sum;
             }
-            sum = team_sum<LPR>(sum);
-            const float inv = sum == 0.0 ? 0.f : 1.0f / (float)sum;
-            if (a.bias) A = 64.f * U * inv;
+            // one NaN is in every score of its row
+            bool nan = false;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) c[i] = c[i] == LOW ? LOW : c[i] * inv;
-        } else {
-            if (a.bias) A = 16.f * U;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(c[i] * -1.4426950408889634f));
-                c[i] = is_masked<F32>(c[i]) ? LOW : s;
-            }
+            for (int i = 0; i < VPL; ++i) nan |= c[i] != c[i];
+            unsure = nan;
         }
-        if (a.bias) {
+        // score of a logit, 0 of LOW
+        auto score32 = [&](float l) {
+            if constexpr (SIGMOID) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l * -1.4426950408889634f));
+            else return exp32(l - m) * s_max;
+        };
+        if constexpr (BIAS) {
 #pragma unroll
             for (int j = 0; j < N4; ++j) {
                 const int e = 4 * LPR * j + 4 * p;
                 float4 q = {0.f, 0.f, 0.f, 0.f};
                 if (vec) {
-                    if (e < E) q = *reinterpret_cast<const float4*>(a.bias + e);
+                    if (4 * LPR * (j + 1) <= E || e < E) q = *reinterpret_cast<const float4*>(a.bias + e);
                 } else {
                     if (e < E) q.x = a.bias[e];
                     if (e + 1 < E) q.y = a.bias[e + 1];
@@ -394,46 +442,63 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
                     if (e + 3 < E) q.w = a.bias[e + 3];
                 }
                 const float b[4] = {q.x, q.y, q.z, q.w};
+                float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c[4 * j + i] = c[4 * j + i] == LOW ? LOW : c[4 * j + i] + b[i];
+                for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_fmed3f(score32(c[4 * j + i]) + b[i], LOW, -LOW);
+                if (some_masked) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = c[4 * j + i] == LOW ? LOW : v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[4 * j + i] = v[i];
             }
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_fmed3f(c[i], LOW, -LOW);
-        bool unsure = false;
+            for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_fmed3f(c[i], LOW, -LOW) + 0.0f;  // (-0 is 0)
+        }
         if (a.groups > 1) {
-            const int SP = S + ((12 - (S & 7)) & 7);  // a group's stride: 4 more than a multiple of 8
-            float* mine = lds + team * (a.groups * SP);
-            const bool quads = (S & 3) == 0;
-            if (quads) {
+            // each group's largest two by lanes of their own, through LDS
+            const bool sums = a.group_top == 2;
+            const bool scores = !BIAS && sums;
+            float* mine = lds + team * a.lds_row;
+            if (vec) {
 #pragma unroll
                 for (int j = 0; j < N4; ++j) {
                     const int e = 4 * LPR * j + 4 * p;
-                    if (e < E)
-                        *reinterpret_cast<float4*>(mine + e + (int)((uint32_t)(e * a.inv_S) >> 22) * (SP - S)) =
-                            float4{c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]};
+                    float4 q = {c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]};
+                    if (scores) {
+                        q.x = q.x == LOW ? LOW : score32(q.x), q.y = q.y == LOW ? LOW : score32(q.y);
+                        q.z = q.z == LOW ? LOW : score32(q.z), q.w = q.w == LOW ? LOW : score32(q.w);
+                    }
+                    if (4 * LPR * (j + 1) <= E || e < E) *reinterpret_cast<float4*>(mine + e) = q;
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
                     const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                    if (e < E) mine[e + (int)((uint32_t)(e * a.inv_S) >> 22) * (SP - S)] = c[i];
+                    if (e < E) mine[e] = scores && c[i] != LOW ? score32(c[i]) : c[i];
                 }
             }
             wave_sync();
-            const int lpg = LPR / a.group_slots, g = p / lpg, sub = p - g * lpg;
+            const int lpg = LPR >> a.group_bits, g = p >> (a.lpr_bits - a.group_bits), sub = p & (lpg - 1);
             float t1 = LOW, t2 = LOW;
             auto take = [&](float v) {
                 t2 = __builtin_amdgcn_fmed3f(t1, t2, v);
                 t1 = fmaxf(t1, v);
             };
             if (g < a.groups) {
-                const float* q = mine + g * SP;
+                const float* q = mine + g * S;
                 if (quads) {
+                    // the lanes start at fours of their own: on different banks
+                    const int n = S >> 2, first = (g * a.spread) & (a.spread_mod - 1);
+                    int i = sub + first * lpg;
+                    i = i < n ? i : sub;
 #pragma unroll 4
-                    for (int i = 4 * sub; i < S; i += 4 * lpg) {
-                        const float4 v = *reinterpret_cast<const float4*>(q + i);
+                    for (int x = sub; x < n; x += lpg) {
+                        const float4 v = *reinterpret_cast<const float4*>(q + 4 * i);
                         take(v.x), take(v.y), take(v.z), take(v.w);
+                        i += lpg;
+                        i = i < n ? i : sub;
                     }
                 } else {
                     for (int i = sub; i < S; i += lpg) take(q[i]);
@@ -444,30 +509,33 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
                 t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
                 t1 = fmaxf(t1, o1);
             }
-            const float v = a.group_top == 2 && t2 > LOW ? t1 + t2 : t1;
+            const float v = sums && t2 > LOW ? t1 + t2 : t1;
             int ahead = 0;
             for (int o = 0; o < a.groups; ++o) {
                 const float ov = __shfl(v, o * lpg, LPR);
                 ahead += (ov > v) | ((ov == v) & (o < g));
             }
             const bool stays = g < a.groups && ahead < a.top_groups;
-            const float least = -team_max<LPR>(stays ? -v : LOW);
+            const float last = -team_max<LPR>(stays ? -v : LOW);
             const float next = team_max<LPR>(g < a.groups && !stays ? v : LOW);
-            // without a bias: the largest error that B can stand for at this value
-            const float B = a.bias ? 16.f * U : SIGMOID ? 2.f * (32.f + 8.f * 104.f) * U : 2.f * (128.f + 16.f * 104.f) * U;
-            unsure = !(least - next > 2.f * A + B * fmaxf(fabsf(least), fabsf(next)));
+            const float far = BIAS ? 2.f * choice_margin<SIGMOID>(fmaxf(fabsf(last), fabsf(next)), s_max)
+                                   : scores ? group_margin<SIGMOID>(last) : logit_margin<SIGMOID>(last, m);
+            // (equal logits are equal, and the lower group stays)
+            unsure |= !(last - next > far || (!BIAS && !sums && last == next && last > 0.5f * LOW));
             const uint32_t stay = (uint32_t)(__ballot(stays) >> (team * LPR));
+            if (quads) {
 #pragma unroll
-            for (int j = 0; j < N4; ++j) {
-                const int e = 4 * LPR * j + 4 * p;
-                if (quads) {
-                    const bool out = !((stay >> ((uint32_t)(e * a.inv_S) >> 22) * lpg) & 1u);
+                for (int j = 0; j < N4; ++j) {
+                    const uint32_t at = (group_of[j / 6] >> (5 * (j % 6)) & 31u) << (a.lpr_bits - a.group_bits);
+                    const bool out = !((stay >> at) & 1u);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) c[4 * j + i] = out ? LOW : c[4 * j + i];
-                } else {
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!((stay >> ((uint32_t)((e + i) * a.inv_S) >> 22) * lpg) & 1u)) c[4 * j + i] = LOW;
+                for (int i = 0; i < VPL; ++i) {
+                    const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
+                    if (!((stay >> (((uint32_t)(e * a.inv_S) >> 22) << (a.lpr_bits - a.group_bits))) & 1u)) c[i] = LOW;
                 }
             }
             wave_sync();  // the next row's values
@@ -480,27 +548,36 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
 #pragma unroll
             for (int i = 0; i < LK; ++i) {
                 const uint64_t b = __builtin_bit_cast(uint64_t, (double)c[r + i]);
-                run[i] = __builtin_bit_cast(double, b | (uint32_t)(4 * LPR * ((r + i) >> 2) + 4 * p + (i & 3)));
+                uint32_t id = (uint32_t)(4 * p) | (uint32_t)(4 * LPR * ((r + i) >> 2) + (i & 3));
+                // by the logit: the lower id's key is the larger one, of positive and of negative values
+                if constexpr (!BIAS) id ^= ~((int32_t)(b >> 32) >> 31) & 1023;
+                run[i] = __builtin_bit_cast(double, b | id);
             }
-            dsort<LK>(run);
+            sort_keys<LK>(run);
             if (r == 0) {
 #pragma unroll
                 for (int i = 0; i < LK; ++i) key[i] = run[i];
             } else {
-                dmerge<LK>(key, run);
+                merge_keys<LK>(key, run);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         double top[KT];
-        // both lanes' passed keys whole: the larger and the smaller halves of a bitonic run
+        if constexpr (KT == LK) {
 #pragma unroll
-        for (int i = 0; i < LK; ++i) {
-            const double o = partner<0>(key[LK - 1 - i]);
-            top[i] = __builtin_fmax(key[i], o);
-            top[LK + i] = __builtin_fmin(key[i], o);
+            for (int i = 0; i < LK; ++i) top[i] = kmax(key[i], partner<0>(key[LK - 1 - i]));
+            sort_bitonic<LK>(top);
+        } else {
+            // both lanes' passed keys whole: the larger and the smaller half of a bitonic run
+#pragma unroll
+            for (int i = 0; i < LK; ++i) {
+                const double o = partner<0>(key[LK - 1 - i]);
+                top[i] = kmax(key[i], o);
+                top[KT - LK + i] = kmin(key[i], o);
+            }
+            sort_bitonic<LK>(top);
+            sort_bitonic<LK>(top + KT - LK);
         }
-        dclean<LK>(top);
-        dclean<LK>(top + LK);
         merge_partner<1, KT>(top);
         merge_partner<2, KT>(top);
         if constexpr (LPR >= 16) merge_partner<3, KT>(top);
@@ -510,22 +587,25 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
 #pragma unroll
         for (int i = 1; i < KT; ++i) mine = p == i ? top[i] : mine;
         const float v = (float)mine;
-        const int id = (int)((uint32_t)__builtin_bit_cast(uint64_t, mine) & 1023u);
+        int id = (int)((uint32_t)__builtin_bit_cast(uint64_t, mine) & 1023u);
+        if constexpr (!BIAS) id ^= ~((int32_t)(__builtin_bit_cast(uint64_t, mine) >> 32) >> 31) & 1023;
         const float l = logit<F32>(a.logits, base + (id < E ? id : 0));
-        float margin;
-        if constexpr (SIGMOID) margin = a.bias ? A + 8.f * U * fabsf(v) : (32.f + 8.f * fminf(fabsf(l), 104.f)) * U * v;
-        else margin = a.bias ? A + 8.f * U * fabsf(v) : (128.f + 16.f * fminf(fabsf(l - m), 104.f)) * U * v;
+        const float margin = BIAS ? choice_margin<SIGMOID>(v, s_max) : logit_margin<SIGMOID>(v, m);
         const float next = dpp32<0x101>(v), next_margin = dpp32<0x101>(margin);  // of lane + 1 in its 16
-        if (p < k - 1) unsure |= !(v - next > fmaxf(margin, next_margin));
+        if (p < k - 1) unsure |= !(v - next > fmaxf(margin, next_margin) || (!BIAS && v == next));
         if (p == k - 1) unsure |= !(v > 0.5f * LOW);
-        const float bar = __shfl(v - margin, k - 1, LPR);
-        int n = 0;
+        const float last = __shfl(v, k - 1, LPR), bar = last - __shfl(margin, k - 1, LPR);
+        const double last_key = __shfl(mine, k - 1, LPR);
 #pragma unroll
-        for (int i = 0; i < LK; ++i) n += (float)key[i] >= bar;
-        if (VPL > LK) unsure |= n == LK;
-        unsure |= team_sum<LPR>((float)n) != (float)k;
+        for (int i = 0; i < LK; ++i) {
+            const float x = (float)key[i];
+            const bool near = !(x < bar);
+            unsure |= near && key[i] < last_key && (BIAS || x != last);
+            // (what the lane did not pass on comes behind its last key)
+            if (VPL > LK && i == LK - 1) unsure |= near;
+        }
         const uint64_t unsure_all = __ballot(unsure && live);
-        constexpr uint64_t TEAM = LPR == 64 ? ~0ull : (1ull << LPR) - 1;
+        constexpr uint64_t TEAM = (1ull << LPR) - 1;
         if (live && !((unsure_all >> (team * LPR)) & TEAM)) {
             RowStat st = {(double)m, 0.0};
             if constexpr (!SIGMOID) st.inv = sum == 0.0 ? 0.0 : 1.0 / sum;
@@ -538,6 +618,7 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
             }
         }
         if (unsure_all == 0) continue;
+#pragma unroll 1
         for (int t = 0; t < ROWS; ++t)
             if ((unsure_all >> (t * LPR)) & TEAM)
                 choose_exactly<F32, SIGMOID, (LPR * VPL + 63) / 64>(kernel_args(), row0 + t, (LdsFloats)lds);
@@ -758,12 +839,17 @@ void with_vpl(int E, F&& f) {
 template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
 void launch_topk(ScoreArgs a, hipStream_t stream) {
     constexpr int ROWS = 64 / LPR;
+    a.lpr_bits = LPR == 8 ? 3 : LPR == 16 ? 4 : 5;
     if (a.groups > 1) {
-        const int S = a.E / a.groups, SP = S + ((12 - (S & 7)) & 7);
-        a.lds_wave = ROWS * a.groups * SP;
+        // rows half the 64 banks apart
+        a.lds_row = (a.E + 3) / 4 * 4;
+        a.lds_row += (96 - a.lds_row % 64) % 64;
+        a.lds_wave = ROWS * a.lds_row;
     }
-    score_topk_kernel<F32, SIGMOID, LPR, VPL, KT>
-        <<<row_blocks(a.T, 4 * ROWS), 256, (size_t)a.lds_wave * 4 * sizeof(float), stream>>>(a);
+    const dim3 grid = row_blocks(a.T, 4 * ROWS);
+    const size_t lds = (size_t)a.lds_wave * 4 * sizeof(float);
+    if (a.bias) score_topk_kernel<F32, SIGMOID, true, LPR, VPL, KT><<<grid, 256, lds, stream>>>(a);
+    else score_topk_kernel<F32, SIGMOID, false, LPR, VPL, KT><<<grid, 256, lds, stream>>>(a);
 }
 
 // The lanes of a row hold its logits, and its groups one each at least.
@@ -772,8 +858,10 @@ void launch_choice_of(ScoreArgs a, hipStream_t stream) {
     const int E = a.E, G = a.groups;
     const int S = E / G;
     a.inv_S = ((1 << 22) + S - 1) / S;
-    a.group_slots = 1;
-    while (a.group_slots < G) a.group_slots <<= 1;
+    while ((1 << a.group_bits) < G) ++a.group_bits;
+    // groups a multiple of 32 floats apart would read the same banks
+    a.spread = S % 32 == 0 ? 1 : 0;
+    a.spread_mod = 8;
     if (G > 32) {
         a.lds_wave = E;
         with_vpl(E, [&](auto v) {
