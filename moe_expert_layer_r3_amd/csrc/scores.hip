@@ -22,7 +22,7 @@ struct ScoreArgs {
     int lds_wave, lds_row;     // floats of LDS for each wave, and for each of its rows
     int inv_S;                 // ceil(2^22 / (E / groups)): e * inv_S >> 22 is e's group
     int group_bits, lpr_bits;  // logarithms of the power of two that holds the groups, and of a row's lanes
-    int spread, spread_mod;    // first four that a group's lanes read: group * spread mod spread_mod
+    int spread;                // a group's lanes start at its four group * spread mod 8
     int32_t* ids;
     float* w;
     int32_t* rec;  // of this layer and first token
@@ -41,6 +41,35 @@ __device__ __forceinline__ bool is_masked(float l) {
     return l <= (F32 ? -3.402823466e38f : -3.389531389e38f);
 }
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+// For weights and gradients, which are rounded to 32 bits: exp(x) from the Taylor
+// polynomial of degree 10 on [-ln 2 / 2, ln 2 / 2] (its remainder 2^-42), a reciprocal from the
+// hardware's and two Newton steps (2^-50): a third of the instructions of the exact ones.
+__device__ __forceinline__ double exp_near(double x) {
+    x = x > 1000.0 ? 1000.0 : x < -1000.0 ? -1000.0 : x;
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(-n, 2.319046813846300e-17, __builtin_fma(-n, 0.6931471805599453, x));
+    double p = 1.0 / 3628800;
+    p = __builtin_fma(p, r, 1.0 / 362880);
+    p = __builtin_fma(p, r, 1.0 / 40320);
+    p = __builtin_fma(p, r, 1.0 / 5040);
+    p = __builtin_fma(p, r, 1.0 / 720);
+    p = __builtin_fma(p, r, 1.0 / 120);
+    p = __builtin_fma(p, r, 1.0 / 24);
+    p = __builtin_fma(p, r, 1.0 / 6);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, (int)n);
+}
+__device__ __forceinline__ double inverse_near(double x) {  // of a positive finite number below 2^1000
+    double y = __builtin_amdgcn_rcp(x);
+    y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+}
+__device__ __forceinline__ double sigmoid_near(double l) {
+    return l < -709.0 ? 0.0 : inverse_near(1.0 + exp_near(-l));  // (0 where sigmoid64 is below 2^-1022)
+}
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll
@@ -115,11 +144,11 @@ __device__ __forceinline__ RowStat row_stat(const float (&l)[VPL], int lane, int
     sum = wave_sum64(sum);
     return {(double)m, sum == 0.0 ? 0.0 : 1.0 / sum};
 }
-template <bool F32, bool SIGMOID>
+template <bool F32, bool SIGMOID, bool EXACT = false>
 __device__ __forceinline__ double score(float l, RowStat st) {
     if (is_masked<F32>(l)) return 0.0;
-    if constexpr (SIGMOID) return sigmoid64(l);
-    else return exp((double)l - st.m) * st.inv;
+    if constexpr (SIGMOID) return EXACT ? sigmoid64(l) : sigmoid_near(l);
+    else return (EXACT ? exp((double)l - st.m) : exp_near((double)l - st.m)) * st.inv;
 }
 
 // Weights of the chosen experts: lane j < k of a group of WIDTH lanes has logit l
@@ -132,7 +161,7 @@ __device__ __forceinline__ double share(float l, double s, int lane, int k, bool
     if constexpr (!SIGMOID) {
         float m = lane < k && !is_masked<F32>(l) ? l : -INFINITY;
         m = team_max<WIDTH>(m);
-        s = is_masked<F32>(l) ? 0.0 : exp((double)l - (double)m);
+        s = is_masked<F32>(l) ? 0.0 : exp_near((double)l - (double)m);
     }
     const double sum = team_sum<WIDTH>(lane < k ? s : 0.0);
     return sum == 0.0 ? 0.0 : s / sum;
@@ -147,9 +176,37 @@ __device__ __forceinline__ void wave_sync() {
 
 // ---------------------------------------------------------------- choice
 
+// Sorting networks over keys as doubles: one v_max_f64 and one v_min_f64 an exchange
+// (written out: the compiler would make each key canonical first, which they are).
+__device__ __forceinline__ double kmax(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double kmin(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+// the largest over the wave, in every lane
+__device__ __forceinline__ double wave_kmax(double v) {
+    v = kmax(v, partner<0>(v));
+    v = kmax(v, partner<1>(v));
+    v = kmax(v, partner<2>(v));
+    v = kmax(v, partner<3>(v));
+    uint64_t b = __builtin_bit_cast(uint64_t, v);
+    auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v = kmax(__builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]), __builtin_bit_cast(double, ((uint64_t)hi[1] << 32) | lo[1]));
+    b = __builtin_bit_cast(uint64_t, v);
+    lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+    hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    return kmax(__builtin_bit_cast(double, ((uint64_t)hi[0] << 32) | lo[0]), __builtin_bit_cast(double, ((uint64_t)hi[1] << 32) | lo[1]));
+}
+
 // One row by a whole wave, as it is defined: scores in 64 bits, rounded. Lane l holds
 // experts l, l + 64, ...; k rounds of a wave-wide maximum over the keys of the groups
-// that stay. lds: E floats of this wave. Rare where the kernel below calls it, and a
+// that stay, as doubles (route_dkey). lds: E floats of this wave. Rare where the kernel below calls it, and a
 // function of its own so that its registers are not the caller's.
 typedef const __attribute__((address_space(4))) ScoreArgs* KernelArgs;
 typedef __attribute__((address_space(3))) float* LdsFloats;
@@ -172,28 +229,27 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
     }
     RowStat st = {0.0, 0.0};
     if constexpr (!SIGMOID) st = row_stat<F32, true, VPL>(l, lane, E);
-    uint64_t key[VPL];
+    double key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 64 * i;
-        key[i] = 0ull;
+        key[i] = 0.0;
         if (e < E) {
-            float c = (float)score<F32, SIGMOID>(l[i], st);
+            float c = (float)score<F32, SIGMOID, true>(l[i], st);
             if (a.bias) c += a.bias[e];
             if (is_masked<F32>(l[i])) c = -INFINITY;
-            key[i] = route_key(c, e);
+            key[i] = route_dkey(c, e);
             if (a.groups > 1) lds[e] = c == c ? c : -INFINITY;
         }
     }
     if (a.groups > 1) {
         wave_sync();
         // 64 / GP lanes to a group, GP the power of two that holds the groups
-        int gp = 1;
-        while (gp < a.groups) gp <<= 1;
-        const int lpg = 64 / gp, S = E / a.groups;
-        const int g = lane / lpg, sub = lane % lpg;
+        const int shift = 6 - a.group_bits, lpg = 1 << shift, S = E / a.groups;
+        const int g = lane >> shift, sub = lane & (lpg - 1);
         float t1 = -INFINITY, t2 = -INFINITY;
         if (g < a.groups) {
+#pragma unroll 4
             for (int i = sub; i < S; i += lpg) {
                 const float v = lds[g * S + i];
                 t2 = fmaxf(t2, fminf(t1, v));
@@ -207,32 +263,28 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
         }
         const float v = a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
         int ahead = 0;
+#pragma unroll 8
         for (int o = 0; o < a.groups; ++o) {
-            const float ov = __shfl(v, o * lpg);
+            const float ov = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), o << shift));
             ahead += (ov > v) | ((ov == v) & (o < g));
         }
         const uint64_t stay = __ballot(g < a.groups && ahead < a.top_groups);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = lane + 64 * i;
-            if (e < E && !((stay >> (e / S * lpg)) & 1ull)) key[i] = 0ull;
+            if (e < E && !((stay >> ((uint32_t)(e * a.inv_S) >> 22 << shift)) & 1ull)) key[i] = 0.0;
         }
         wave_sync();  // the next row's values
     }
-    uint64_t thr = ~0ull, mine = 0ull;
+    double thr = INFINITY, mine = 0.0;
     for (int s = 0; s < k; ++s) {
-        uint64_t b = 0ull;
+        double b = 0.0;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) b = (key[i] < thr && key[i] > b) ? key[i] : b;
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) {
-            const uint64_t o = __shfl_xor(b, m);
-            b = o > b ? o : b;
-        }
-        thr = b;
-        if (lane == s) mine = b;
+        for (int i = 0; i < VPL; ++i) b = key[i] < thr ? kmax(key[i], b) : b;
+        thr = wave_kmax(b);
+        if (lane == s) mine = thr;
     }
-    const int id = lane < k ? route_key_id(mine) : 0;
+    const int id = lane < k ? route_dkey_id(mine) : 0;
     const float ls = logit<F32>(a.logits, base + id);
     if constexpr (!SIGMOID)
         if (!a.renorm) st = row_stat<F32, false, VPL>(l, lane, E);
@@ -246,7 +298,7 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
 
 __device__ __forceinline__ KernelArgs kernel_args() { return (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(); }
 
-// Every row exactly: more groups that count than 32 lanes hold.
+// Every row exactly: more groups that count than 32 lanes hold, or less than four experts.
 template <bool F32, bool SIGMOID, int VPL>
 __global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
@@ -255,18 +307,6 @@ __global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
         choose_exactly<F32, SIGMOID, VPL>(kernel_args(), row, (LdsFloats)(lds_all + wave * a.lds_wave));
 }
 
-// Sorting networks over keys as doubles: one v_max_f64 and one v_min_f64 an exchange
-// (written out: the compiler would make each key canonical first, which they are).
-__device__ __forceinline__ double kmax(double a, double b) {
-    double r;
-    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-    return r;
-}
-__device__ __forceinline__ double kmin(double a, double b) {
-    double r;
-    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-    return r;
-}
 __device__ __forceinline__ void exchange(double& a, double& b) {
     const double x = a, y = b;
     a = kmax(x, y);
@@ -334,6 +374,27 @@ __device__ __forceinline__ float group_margin(float v) {
     return v < 1e-30f ? INFINITY : (SIGMOID ? 400.f : 512.f) * U * v;
 }
 
+// Four neighbouring values, from any element on.
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t h4u __attribute__((ext_vector_type(2), aligned(2)));
+template <bool F32>
+__device__ __forceinline__ void load4(float* v, const void* p) {
+    if constexpr (F32) {
+        const f4u q = *static_cast<const f4u*>(p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else {
+        const h4u q = *static_cast<const h4u*>(p);
+        v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
+    }
+}
+// v[i] = v[i + n] for n = 1 to 3, as far as there are any
+__device__ __forceinline__ void shift4(float* v, int n) {
+    const float a = v[1], b = v[2], c = v[3];
+    v[0] = n == 1 ? a : n == 2 ? b : n == 3 ? c : v[0];
+    v[1] = n == 1 ? b : n == 2 ? c : v[1];
+    v[2] = n == 1 ? c : v[2];
+}
+
 // LPR lanes to a row, VPL logits to a lane (4 neighbours in every 4 LPR), k <= KT.
 //
 // The choice is defined by scores that are rounded from 64 bits, but 32 bits decide
@@ -343,55 +404,61 @@ __device__ __forceinline__ float group_margin(float v) {
 // its groups, its k picks among themselves and the last pick and every expert
 // behind it are the margins above apart; the others are chosen anew by the whole wave.
 // Keys: c' or the logit as a double with the id in the bits that 32-bit values leave
-// zero. A lane passes on its 8 largest; one whose last passed key comes near the last
-// pick makes the row uncertain.
-template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int KT>
-__global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
+// zero. VL of a lane's values come to that: all, or, where the groups that stay hold at
+// most half the experts, those of them alone. A lane passes on its 8 largest; one
+// whose last passed key comes near the last pick makes the row uncertain.
+template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int VL, int KT>
+__global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
-    constexpr int ROWS = 64 / LPR, LK = 8, N4 = VPL / 4;
-    const int lane = threadIdx.x & 63, team = lane / LPR, wave = threadIdx.x >> 6;
-    const int k = a.k, S = a.E / a.groups;
+    constexpr int ROWS = 64 / LPR, LK = 8, N4 = VPL / 4, L4 = VL / 4;
+    const int lane = threadIdx.x & 63, team = lane / LPR;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int E = a.E, k = a.k, S = a.E / a.groups;
     float* lds = lds_all + wave * a.lds_wave;
-    const bool vec = (a.E & 3) == 0;
-    const int E = a.E;
+    const bool quads = (S & 3) == 0;  // groups of whole fours
     int p = lane & (LPR - 1);
-    // groups of whole fours: the group of each four, five bits each
-    const bool quads = (S & 3) == 0;
-    uint32_t group_of[(N4 + 5) / 6];
+    // where a lane's fours of the groups that stay are: the how manieth such group, five bits each
+    uint32_t group_of[(L4 + 5) / 6];
+    if (VL < VPL || a.groups > 1) {
 #pragma unroll
-    for (int i = 0; i < (N4 + 5) / 6; ++i) group_of[i] = 0;
+        for (int i = 0; i < (L4 + 5) / 6; ++i) group_of[i] = 0;
 #pragma unroll
-    for (int j = 0; j < N4; ++j)
-        group_of[j / 6] |= ((uint32_t)((4 * LPR * j + 4 * p) * a.inv_S) >> 22 & 31u) << (5 * (j % 6));
+        for (int j = 0; j < L4; ++j)
+            group_of[j / 6] |= ((uint32_t)((4 * LPR * j + 4 * p) * a.inv_S) >> 22 & 31u) << (5 * (j % 6));
+    }
     const int64_t step = (int64_t)gridDim.x * 4 * ROWS;
-    for (int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * ROWS; row0 < a.T; row0 += step) {
+    float c[VPL];
+    // the logits of a team's row from a wave's first row on
+    auto source = [&](int64_t row0) { return static_cast<const char*>(a.logits) + row0 * E * (F32 ? 4 : 2); };
+    auto offset = [&](int64_t row0) { return (uint32_t)(row0 + team < a.T ? team * E : 0); };
+    auto fetch = [&](int64_t row0) {
+        const char* src = source(row0);
+        const uint32_t base = offset(row0);
+#pragma unroll
+        for (int j = 0; j < N4; ++j)
+            load4<F32>(c + 4 * j, src + (base + (uint32_t)min(4 * LPR * j + 4 * p, E - 4)) * (F32 ? 4u : 2u));
+    };
+    const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * ROWS;
+    if (first < a.T) fetch(first);
+    float* bias = lds_all + 4 * a.lds_wave;
+    if constexpr (BIAS) {
+        for (int e = threadIdx.x; e < LPR * VPL; e += 256) bias[e] = e < E ? a.bias[e] : 0.f;
+        __syncthreads();
+    }
+    for (int64_t row0 = first; row0 < a.T; row0 += step) {
         // what follows from this is made anew for each row: it would not fit the registers
         asm volatile("" : "+v"(p));
         const int64_t row = row0 + team;
         const bool live = row < a.T;
-        const int64_t base = (live ? row : row0) * E;
-        float c[VPL];
-        if (vec) {
+        if (VL == VPL && row0 != first) fetch(row0);
+        if (E & 3) {
+            // a row's last four, read from three before its end at most
 #pragma unroll
-            for (int j = 0; j < N4; ++j) {
-                const int e = 4 * LPR * j + 4 * p;
-                float4 q = {LOW, LOW, LOW, LOW};
-                if (4 * LPR * (j + 1) <= E || e < E) {
-                    if constexpr (F32) {
-                        q = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + base + e);
-                    } else {
-                        const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + base + e);
-                        q = {bf16_lo(h.x), bf16_hi(h.x), bf16_lo(h.y), bf16_hi(h.y)};
-                    }
-                }
-                c[4 * j] = q.x, c[4 * j + 1] = q.y, c[4 * j + 2] = q.z, c[4 * j + 3] = q.w;
-            }
-        } else {
+            for (int j = 0; j < N4; ++j) shift4(c + 4 * j, 4 * LPR * j + 4 * p - (E - 4));
+        }
+        if (E < LPR * VPL) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                c[i] = e < E ? logit<F32>(a.logits, base + e) : LOW;
-            }
+            for (int i = 0; i < VPL; ++i) c[i] = 4 * LPR * (i >> 2) + 4 * p + (i & 3) < E ? c[i] : LOW;
         }
         // LOW for masked experts (and none); a NaN stays one for now
         float least = c[0];
@@ -413,7 +480,10 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
             if (BIAS || !a.renorm) {
                 sum = 0.0;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) sum += c[i] == LOW ? 0.0 : (double)exp32(c[i] - m);
+                for (int i = 0; i < VPL; ++i) {
+                    sum += c[i] == LOW ? 0.0 : (double)exp32(c[i] - m);
+                    if (i % 8 == 7) __builtin_amdgcn_sched_barrier(0);
+                }
                 sum = team_sum<LPR>(sum);
                 s_max = sum == 0.0 ? 0.f : 1.0f / (float)sum;
             }
@@ -431,67 +501,49 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
         if constexpr (BIAS) {
 #pragma unroll
             for (int j = 0; j < N4; ++j) {
-                const int e = 4 * LPR * j + 4 * p;
-                float4 q = {0.f, 0.f, 0.f, 0.f};
-                if (vec) {
-                    if (4 * LPR * (j + 1) <= E || e < E) q = *reinterpret_cast<const float4*>(a.bias + e);
-                } else {
-                    if (e < E) q.x = a.bias[e];
-                    if (e + 1 < E) q.y = a.bias[e + 1];
-                    if (e + 2 < E) q.z = a.bias[e + 2];
-                    if (e + 3 < E) q.w = a.bias[e + 3];
-                }
+                const float4 q = *reinterpret_cast<const float4*>(bias + 4 * LPR * j + 4 * p);
                 const float b[4] = {q.x, q.y, q.z, q.w};
-                float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_fmed3f(score32(c[4 * j + i]) + b[i], LOW, -LOW);
-                if (some_masked) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = c[4 * j + i] == LOW ? LOW : v[i];
+                for (int i = 0; i < 4; ++i) {
+                    const float v = __builtin_amdgcn_fmed3f(score32(c[4 * j + i]) + b[i], LOW, -LOW);
+                    c[4 * j + i] = some_masked && c[4 * j + i] == LOW ? LOW : v;
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) c[4 * j + i] = v[i];
             }
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_fmed3f(c[i], LOW, -LOW) + 0.0f;  // (-0 is 0)
         }
-        if (a.groups > 1) {
+        float v_of[VL];   // the values that are picked from, and the first id of each four
+        int id_of[L4];
+#pragma unroll
+        for (int j = 0; j < L4; ++j) id_of[j] = 4 * LPR * j + 4 * p;
+        if (VL < VPL || a.groups > 1) {
             // each group's largest two by lanes of their own, through LDS
             const bool sums = a.group_top == 2;
             const bool scores = !BIAS && sums;
             float* mine = lds + team * a.lds_row;
-            if (vec) {
 #pragma unroll
-                for (int j = 0; j < N4; ++j) {
-                    const int e = 4 * LPR * j + 4 * p;
-                    float4 q = {c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]};
-                    if (scores) {
-                        q.x = q.x == LOW ? LOW : score32(q.x), q.y = q.y == LOW ? LOW : score32(q.y);
-                        q.z = q.z == LOW ? LOW : score32(q.z), q.w = q.w == LOW ? LOW : score32(q.w);
-                    }
-                    if (4 * LPR * (j + 1) <= E || e < E) *reinterpret_cast<float4*>(mine + e) = q;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VPL; ++i) {
-                    const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                    if (e < E) mine[e] = scores && c[i] != LOW ? score32(c[i]) : c[i];
-                }
+            for (int j = 0; j < N4; ++j) {
+                const int e = 4 * LPR * j + 4 * p;
+                if (LPR * VPL == E || e < E)
+                    *reinterpret_cast<float4*>(mine + e) = float4{c[4 * j], c[4 * j + 1], c[4 * j + 2], c[4 * j + 3]};
             }
+            if (VL < VPL && row0 + step < a.T) fetch(row0 + step);  // all that is needed of these is in LDS now
             wave_sync();
-            const int lpg = LPR >> a.group_bits, g = p >> (a.lpr_bits - a.group_bits), sub = p & (lpg - 1);
+            const int shift = a.lpr_bits - a.group_bits;
+            const int lpg = 1 << shift, g = p >> shift, sub = p & (lpg - 1);
             float t1 = LOW, t2 = LOW;
             auto take = [&](float v) {
+                if (scores) v = v == LOW ? LOW : score32(v);
                 t2 = __builtin_amdgcn_fmed3f(t1, t2, v);
-                t1 = fmaxf(t1, v);
+                t1 = __builtin_amdgcn_fmed3f(t1, v, INFINITY);
             };
             if (g < a.groups) {
                 const float* q = mine + g * S;
                 if (quads) {
                     // the lanes start at fours of their own: on different banks
-                    const int n = S >> 2, first = (g * a.spread) & (a.spread_mod - 1);
-                    int i = sub + first * lpg;
+                    const int n = S >> 2;
+                    int i = sub + ((g * a.spread & 7) << shift);
                     i = i < n ? i : sub;
 #pragma unroll 4
                     for (int x = sub; x < n; x += lpg) {
@@ -512,7 +564,7 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
             const float v = sums && t2 > LOW ? t1 + t2 : t1;
             int ahead = 0;
             for (int o = 0; o < a.groups; ++o) {
-                const float ov = __shfl(v, o * lpg, LPR);
+                const float ov = __shfl(v, o << shift, LPR);
                 ahead += (ov > v) | ((ov == v) & (o < g));
             }
             const bool stays = g < a.groups && ahead < a.top_groups;
@@ -524,31 +576,51 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
             unsure |= !(last - next > far || (!BIAS && !sums && last == next && last > 0.5f * LOW));
             const uint32_t stay = (uint32_t)(__ballot(stays) >> (team * LPR));
             if (quads) {
+                // the fours of the groups that stay, in order; which group is the o-th of them, by a table
+                int* table = reinterpret_cast<int*>(mine + a.lds_row - 32);
+                if (stays && sub == 0) table[__popc(stay & ((1u << p) - 1u)) >> shift] = g;
+                wave_sync();
+                const int n = a.top_groups * S;
 #pragma unroll
-                for (int j = 0; j < N4; ++j) {
-                    const uint32_t at = (group_of[j / 6] >> (5 * (j % 6)) & 31u) << (a.lpr_bits - a.group_bits);
-                    const bool out = !((stay >> at) & 1u);
+                for (int j = 0; j < L4; ++j) {
+                    const int x = 4 * LPR * j + 4 * p;
+                    const int o = (int)(group_of[j / 6] >> (5 * (j % 6)) & 31u);
+                    const int off = (int)__umul24(o, S);
+                    id_of[j] = x < n ? (int)__umul24(table[x < n ? o : 0], S) + (x - off) : 0;
+                }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) c[4 * j + i] = out ? LOW : c[4 * j + i];
+                for (int j = 0; j < L4; ++j) {
+                    const float4 q = *reinterpret_cast<const float4*>(mine + id_of[j]);
+                    v_of[4 * j] = q.x, v_of[4 * j + 1] = q.y, v_of[4 * j + 2] = q.z, v_of[4 * j + 3] = q.w;
+                }
+#pragma unroll
+                for (int j = 0; j < L4; ++j) {
+                    const bool in = 4 * LPR * j + 4 * p < n;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v_of[4 * j + i] = in ? v_of[4 * j + i] : LOW;
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) {
+                for (int i = 0; i < VL; ++i) {
                     const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                    if (!((stay >> (((uint32_t)(e * a.inv_S) >> 22) << (a.lpr_bits - a.group_bits))) & 1u)) c[i] = LOW;
+                    const bool in = (stay >> (((uint32_t)(e * a.inv_S) >> 22) << shift)) & 1u;
+                    v_of[i] = in && e < E ? c[i] : LOW;
                 }
             }
             wave_sync();  // the next row's values
+        } else {
+#pragma unroll
+            for (int i = 0; i < VL; ++i) v_of[i] = c[i];
         }
         // the lane's LK largest keys, run by run
         double key[LK];
 #pragma unroll
-        for (int r = 0; r < VPL; r += LK) {
+        for (int r = 0; r < VL; r += LK) {
             double run[LK];
 #pragma unroll
             for (int i = 0; i < LK; ++i) {
-                const uint64_t b = __builtin_bit_cast(uint64_t, (double)c[r + i]);
-                uint32_t id = (uint32_t)(4 * p) | (uint32_t)(4 * LPR * ((r + i) >> 2) + (i & 3));
+                const uint64_t b = __builtin_bit_cast(uint64_t, (double)v_of[r + i]);
+                uint32_t id = (uint32_t)id_of[(r + i) >> 2] | (uint32_t)(i & 3);
                 // by the logit: the lower id's key is the larger one, of positive and of negative values
                 if constexpr (!BIAS) id ^= ~((int32_t)(b >> 32) >> 31) & 1023;
                 run[i] = __builtin_bit_cast(double, b | id);
@@ -589,7 +661,7 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
         const float v = (float)mine;
         int id = (int)((uint32_t)__builtin_bit_cast(uint64_t, mine) & 1023u);
         if constexpr (!BIAS) id ^= ~((int32_t)(__builtin_bit_cast(uint64_t, mine) >> 32) >> 31) & 1023;
-        const float l = logit<F32>(a.logits, base + (id < E ? id : 0));
+        const float l = logit<F32>(source(row0) + (offset(row0) + (uint32_t)(id < E ? id : 0)) * (F32 ? 4u : 2u), 0);
         const float margin = BIAS ? choice_margin<SIGMOID>(v, s_max) : logit_margin<SIGMOID>(v, m);
         const float next = dpp32<0x101>(v), next_margin = dpp32<0x101>(margin);  // of lane + 1 in its 16
         if (p < k - 1) unsure |= !(v - next > fmaxf(margin, next_margin) || (!BIAS && v == next));
@@ -602,7 +674,7 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
             const bool near = !(x < bar);
             unsure |= near && key[i] < last_key && (BIAS || x != last);
             // (what the lane did not pass on comes behind its last key)
-            if (VPL > LK && i == LK - 1) unsure |= near;
+            if (VL > LK && i == LK - 1) unsure |= near;
         }
         const uint64_t unsure_all = __ballot(unsure && live);
         constexpr uint64_t TEAM = (1ull << LPR) - 1;
@@ -625,13 +697,31 @@ __global__ __launch_bounds__(256, 4) void score_topk_kernel(ScoreArgs a) {
     }
 }
 
-// load[e] += how often e stands in ids, counted in LDS first.
+// load[e] += how often e stands in ids, counted in LDS first: atomics to one kilobyte
+// of memory go one after the other (all 131072 straight to memory took 100 us). 16384 ids to
+// a workgroup, all on their way at once.
+typedef int i4u __attribute__((ext_vector_type(4), aligned(4)));
 __global__ __launch_bounds__(1024) void score_load_kernel(const int32_t* ids, int64_t n, int E, int32_t* load) {
     __shared__ int32_t count[MAX_E];
     for (int e = threadIdx.x; e < E; e += 1024) count[e] = 0;
     __syncthreads();
-    for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 1024)
-        atomicAdd(&count[ids[i]], 1);
+    for (int64_t i0 = (int64_t)blockIdx.x * 16384; i0 < n; i0 += (int64_t)gridDim.x * 16384) {
+        i4u q[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t i = i0 + r * 4096 + threadIdx.x * 4;
+            q[r] = i4u{-1, -1, -1, -1};
+            if (i + 4 <= n) q[r] = *reinterpret_cast<const i4u*>(ids + i);
+            else
+                for (int j = 0; j < 3; ++j)
+                    if (i + j < n) q[r][j] = ids[i + j];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (q[r][j] >= 0) atomicAdd(&count[q[r][j]], 1);
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 1024)
         if (count[e]) atomicAdd(load + e, count[e]);
@@ -756,7 +846,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
         }
         // a slot's gradient of its own logit (softmax without renorm: before the row's part)
         double c = (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
-        if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid64(-(double)ls);
+        if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-(double)ls);
         if (lane >= k || bad) c = 0.0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -840,16 +930,30 @@ template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
 void launch_topk(ScoreArgs a, hipStream_t stream) {
     constexpr int ROWS = 64 / LPR;
     a.lpr_bits = LPR == 8 ? 3 : LPR == 16 ? 4 : 5;
+    const int S = a.E / a.groups;
+    bool half = false;  // the groups that stay hold at most half of what the lanes can
     if (a.groups > 1) {
-        // rows half the 64 banks apart
-        a.lds_row = (a.E + 3) / 4 * 4;
+        // a row's values and 32 more for its table, rows half the 64 banks apart
+        a.lds_row = (a.E + 3) / 4 * 4 + 32;
         a.lds_row += (96 - a.lds_row % 64) % 64;
         a.lds_wave = ROWS * a.lds_row;
+        half = S % 4 == 0 && a.top_groups * S <= LPR * VPL / 2;
     }
-    const dim3 grid = row_blocks(a.T, 4 * ROWS);
-    const size_t lds = (size_t)a.lds_wave * 4 * sizeof(float);
-    if (a.bias) score_topk_kernel<F32, SIGMOID, true, LPR, VPL, KT><<<grid, 256, lds, stream>>>(a);
-    else score_topk_kernel<F32, SIGMOID, false, LPR, VPL, KT><<<grid, 256, lds, stream>>>(a);
+    // as many workgroups as run at once: each has its next rows' logits on their way
+    const int64_t blocks = (a.T + 4 * ROWS - 1) / (4 * ROWS), most = 4 * (int64_t)num_cus();
+    const dim3 grid((unsigned)(blocks < most ? blocks : most));
+    const size_t lds = ((size_t)a.lds_wave * 4 + (a.bias ? LPR * VPL : 0)) * sizeof(float);
+    auto go = [&](auto vl) {
+        if (a.bias) score_topk_kernel<F32, SIGMOID, true, LPR, VPL, vl.value, KT><<<grid, 256, lds, stream>>>(a);
+        else score_topk_kernel<F32, SIGMOID, false, LPR, VPL, vl.value, KT><<<grid, 256, lds, stream>>>(a);
+    };
+    if constexpr (VPL >= 16) {
+        if (half) {
+            go(std::integral_constant<int, VPL / 2>{});
+            return;
+        }
+    }
+    go(std::integral_constant<int, VPL>{});
 }
 
 // The lanes of a row hold its logits, and its groups one each at least.
@@ -860,9 +964,8 @@ void launch_choice_of(ScoreArgs a, hipStream_t stream) {
     a.inv_S = ((1 << 22) + S - 1) / S;
     while ((1 << a.group_bits) < G) ++a.group_bits;
     // groups a multiple of 32 floats apart would read the same banks
-    a.spread = S % 32 == 0 ? 1 : 0;
-    a.spread_mod = 8;
-    if (G > 32) {
+    a.spread = S % 32 == 0;
+    if (G > 32 || E < 4) {
         a.lds_wave = E;
         with_vpl(E, [&](auto v) {
             score_topk_exact_kernel<F32, SIGMOID, v.value>
