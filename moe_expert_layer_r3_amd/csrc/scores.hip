@@ -11,6 +11,7 @@ namespace moe {
 namespace {
 
 constexpr int MAX_E = 1024;
+constexpr float LOW = -3.402823466e38f;  // below every number that counts
 
 struct ScoreArgs {
     const void* logits;
@@ -221,12 +222,11 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
     const int64_t row = (int64_t)uniform((uint64_t)row_);
     const int lane = threadIdx.x & 63, E = a.E, k = a.k;
     const int64_t base = row * E;
-    float l[VPL];
+    float l[VPL], bias[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E ? logit<F32>(a.logits, base + e) : 0.f;
-    }
+    for (int i = 0; i < VPL; ++i) l[i] = logit<F32>(a.logits, base + min(lane + 64 * i, E - 1));
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, E - 1)] : 0.f;
     RowStat st = {0.0, 0.0};
     if constexpr (!SIGMOID) st = row_stat<F32, true, VPL>(l, lane, E);
     double key[VPL];
@@ -236,7 +236,7 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
         key[i] = 0.0;
         if (e < E) {
             float c = (float)score<F32, SIGMOID, true>(l[i], st);
-            if (a.bias) c += a.bias[e];
+            if (a.bias) c += bias[i];
             if (is_masked<F32>(l[i])) c = -INFINITY;
             key[i] = route_dkey(c, e);
             if (a.groups > 1) lds[e] = c == c ? c : -INFINITY;
@@ -298,7 +298,7 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
 
 __device__ __forceinline__ KernelArgs kernel_args() { return (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(); }
 
-// Every row exactly: more groups that count than 32 lanes hold, or less than four experts.
+// Every row exactly: more groups that count than 32 lanes hold, less than four experts, or few rows.
 template <bool F32, bool SIGMOID, int VPL>
 __global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
@@ -349,7 +349,7 @@ __device__ __forceinline__ void merge_partner(double* g) {
 
 // Two distances, u = 2^-24 and the hardware's exp2 and reciprocal good to 2 u, that
 // decide what order 32 bits are certain of.
-constexpr float U = 5.9604644775390625e-8f, LOW = -3.402823466e38f;
+constexpr float U = 5.9604644775390625e-8f;
 // Logits at least this far apart, the larger one l: their scores, exact, differ by more
 // than two roundings to 32 bits (a softmax score by a factor exp(l - l'), a sigmoid one by
 // 1 + (1 - s)(l - l'), 1 - s = 1 / (1 + exp(l))). Where scores leave the normal
@@ -359,13 +359,18 @@ __device__ __forceinline__ float logit_margin(float l, float top) {
     if constexpr (SIGMOID) return l < -80.f ? INFINITY : 8.f * U * (1.0f + exp32(l));
     else return l < top - 60.f || top == -LOW ? INFINITY : 8.f * U;
 }
-// c' = s' + bias at least this far apart, s' scores up to s_max: s' is off by
-// s (1 - s) |l| u 3/2 (the argument's roundings) + 6 u s <= 6.4 u (sigmoid) or
-// s (2 |l - m| + 2 ln E + 10) u <= 25 u s_max (softmax: s |l - m| <= s_max / e); the sums' and the
-// definition's own roundings are 2 u |c| each side.
+// c' = s' + bias at least this far apart, s' scores up to s_max. Each side: s' is off by
+// s (1 - s) (2 + 3/2 |l|) u + 3 u s <= 3.2 u (sigmoid: exp2 and its argument, the sum, the
+// reciprocal) or s (2 |l - m| + 2 ln E + 10) u <= 25 u s_max (softmax: s |l - m| <= s_max / e),
+// the definition's by u / 2, and both sums by u |c|.
 template <bool SIGMOID>
 __device__ __forceinline__ float choice_margin(float c, float s_max) {
-    return (SIGMOID ? 16.f * U : 64.f * U * s_max) + 8.f * U * fabsf(c);
+    return (SIGMOID ? 8.f * U : 64.f * U * s_max) + 4.f * U * fabsf(c);
+}
+// The same for groups' sums of two, size = |c| + |c| of them: their own sum is rounded too.
+template <bool SIGMOID>
+__device__ __forceinline__ float choice_group_margin(float size, float s_max) {
+    return (SIGMOID ? 16.f * U : 128.f * U * s_max) + 12.f * U * size;
 }
 // A group's two scores s' without a bias, relative to their sum: off by (1 - s) |l| u 3/2 + 6 u
 // or (2 |l - m| + 2 ln E + 10) u each, |l| up to 80, and one more rounding. Tiny sums, infinite.
@@ -402,7 +407,9 @@ __device__ __forceinline__ void shift4(float* v, int n) {
 // hardware's exp2 and reciprocal, without one by their logits (which no rounding
 // touches: equal logits have equal scores, and the id decides). A row is certain if
 // its groups, its k picks among themselves and the last pick and every expert
-// behind it are the margins above apart; the others are chosen anew by the whole wave.
+// behind it are the margins above apart. Where only picks, and one expert behind
+// them, come nearer, these few are ordered anew (sigmoid scores with a bias: one row in
+// 1000 of 256 experts); other rows are chosen anew by the whole wave.
 // Keys: c' or the logit as a double with the id in the bits that 32-bit values leave
 // zero. VL of a lane's values come to that: all, or, where the groups that stay hold at
 // most half the experts, those of them alone. A lane passes on its 8 largest; one
@@ -411,6 +418,7 @@ template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int VL, int KT>
 __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
     constexpr int ROWS = 64 / LPR, LK = 8, N4 = VPL / 4, L4 = VL / 4;
+    constexpr uint64_t TEAM = (1ull << LPR) - 1;
     const int lane = threadIdx.x & 63, team = lane / LPR;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int E = a.E, k = a.k, S = a.E / a.groups;
@@ -570,7 +578,9 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
             const bool stays = g < a.groups && ahead < a.top_groups;
             const float last = -team_max<LPR>(stays ? -v : LOW);
             const float next = team_max<LPR>(g < a.groups && !stays ? v : LOW);
-            const float far = BIAS ? 2.f * choice_margin<SIGMOID>(fmaxf(fabsf(last), fabsf(next)), s_max)
+            const float size = team_max<LPR>(
+                BIAS && (v == last || v == next) ? (t1 > LOW ? fabsf(t1) : 0.f) + (t2 > LOW ? fabsf(t2) : 0.f) : 0.f);
+            const float far = BIAS ? choice_group_margin<SIGMOID>(size, s_max)
                                    : scores ? group_margin<SIGMOID>(last) : logit_margin<SIGMOID>(last, m);
             // (equal logits are equal, and the lower group stays)
             unsure |= !(last - next > far || (!BIAS && !sums && last == next && last > 0.5f * LOW));
@@ -661,23 +671,57 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
         const float v = (float)mine;
         int id = (int)((uint32_t)__builtin_bit_cast(uint64_t, mine) & 1023u);
         if constexpr (!BIAS) id ^= ~((int32_t)(__builtin_bit_cast(uint64_t, mine) >> 32) >> 31) & 1023;
-        const float l = logit<F32>(source(row0) + (offset(row0) + (uint32_t)(id < E ? id : 0)) * (F32 ? 4u : 2u), 0);
+        float l = logit<F32>(source(row0) + (offset(row0) + (uint32_t)(id < E ? id : 0)) * (F32 ? 4u : 2u), 0);
         const float margin = BIAS ? choice_margin<SIGMOID>(v, s_max) : logit_margin<SIGMOID>(v, m);
         const float next = dpp32<0x101>(v), next_margin = dpp32<0x101>(margin);  // of lane + 1 in its 16
-        if (p < k - 1) unsure |= !(v - next > fmaxf(margin, next_margin) || (!BIAS && v == next));
+        bool mixed = p < k - 1 && !(v - next > fmaxf(margin, next_margin) || (!BIAS && v == next));
         if (p == k - 1) unsure |= !(v > 0.5f * LOW);
         const float last = __shfl(v, k - 1, LPR), bar = last - __shfl(margin, k - 1, LPR);
         const double last_key = __shfl(mine, k - 1, LPR);
+        // the experts that are not picks and come near the last one
+        int behind = 0;
+        double best = -INFINITY;
 #pragma unroll
         for (int i = 0; i < LK; ++i) {
             const float x = (float)key[i];
-            const bool near = !(x < bar);
-            unsure |= near && key[i] < last_key && (BIAS || x != last);
+            const bool near = !(x < bar) && key[i] < last_key && (BIAS || x != last);
+            behind += near;
+            best = near ? kmax(best, key[i]) : best;
             // (what the lane did not pass on comes behind its last key)
-            if (VL > LK && i == LK - 1) unsure |= near;
+            if (VL > LK && i == LK - 1) unsure |= !(x < bar);
+        }
+        if constexpr (SIGMOID && BIAS) {
+            // The picks and one expert near the last of them: ordered anew by their exact c.
+            behind = (int)team_sum<LPR>((float)behind);
+            unsure |= behind > 1;
+            mixed |= behind == 1;
+            mixed = ((__ballot(mixed && !unsure && live) >> (team * LPR)) & TEAM) != 0;
+            if (__ballot(mixed)) {
+                best = team_reduce<LPR>(best, [](double x, double y) { return kmax(x, y); });
+                const int id9 = behind ? (int)((uint32_t)__builtin_bit_cast(uint64_t, best) & 1023u) : 0;
+                const float l9 = logit<F32>(source(row0) + (offset(row0) + (uint32_t)id9) * (F32 ? 4u : 2u), 0);
+                const float c = (float)sigmoid64((double)l) + bias[id], c9 = (float)sigmoid64((double)l9) + bias[id9];
+                int rank = behind && (c9 > c || (c9 == c && id9 < id)), rank9 = 0;
+                for (int q = 0; q < k; ++q) {
+                    const float cq = __shfl(c, q, LPR);
+                    const int iq = __shfl(id, q, LPR);
+                    rank += cq > c || (cq == c && iq < id);
+                    rank9 += cq > c9 || (cq == c9 && iq < id9);
+                }
+                int pick = rank9 == p ? id9 : id;
+                for (int q = 0; q < k; ++q) {
+                    const int rq = __shfl(rank, q, LPR), iq = __shfl(id, q, LPR);
+                    pick = rq == p ? iq : pick;
+                }
+                if (mixed && p < k) {
+                    id = pick;
+                    l = logit<F32>(source(row0) + (offset(row0) + (uint32_t)id) * (F32 ? 4u : 2u), 0);
+                }
+            }
+        } else {
+            unsure |= mixed || behind;
         }
         const uint64_t unsure_all = __ballot(unsure && live);
-        constexpr uint64_t TEAM = (1ull << LPR) - 1;
         if (live && !((unsure_all >> (team * LPR)) & TEAM)) {
             RowStat st = {(double)m, 0.0};
             if constexpr (!SIGMOID) st.inv = sum == 0.0 ? 0.0 : 1.0 / sum;
@@ -759,34 +803,66 @@ __global__ __launch_bounds__(256) void score_replay_kernel(ScoreArgs a, int32_t*
     }
 }
 
-// One wave per token where the whole row does (softmax without renorm).
+// A row that 16 lanes hold: lane p the logits 64 j + 4 p + i, and its softmax.
+template <bool F32, int VPL>
+struct Row16 {
+    float l[VPL];
+    RowStat st;
+    float m;
+    __device__ __forceinline__ void load(const void* logits, int64_t row, int E, int p) {
+        const char* src = static_cast<const char*>(logits) + row * E * (F32 ? 4 : 2);
+        if (E >= 4) {
+#pragma unroll
+            for (int j = 0; j < VPL / 4; ++j)
+                load4<F32>(l + 4 * j, src + (uint32_t)min(64 * j + 4 * p, E - 4) * (F32 ? 4u : 2u));
+            if (E & 3) {
+#pragma unroll
+                for (int j = 0; j < VPL / 4; ++j) shift4(l + 4 * j, 64 * j + 4 * p - (E - 4));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) l[i] = logit<F32>(src, min(64 * (i >> 2) + 4 * p + (i & 3), E - 1));
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            l[i] = 64 * (i >> 2) + 4 * p + (i & 3) < E && !is_masked<F32>(l[i]) ? l[i] : LOW;
+        m = LOW;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+        m = team_max<16>(m);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) sum += l[i] == LOW ? 0.0 : (double)exp32(l[i] - m);
+        sum = team_sum<16>(sum);
+        st = {(double)m, sum == 0.0 ? 0.0 : 1.0 / sum};
+    }
+};
+
+// 16 lanes per token where the whole row does (softmax without renorm).
 template <bool F32, int VPL>
 __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int32_t* status) {
-    const int lane = threadIdx.x & 63, E = a.E, k = a.k;
-    const int64_t step = (int64_t)gridDim.x * 4;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.T; row += step) {
-        float l[VPL];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 64 * i;
-            l[i] = e < E ? logit<F32>(a.logits, row * E + e) : 0.f;
-        }
-        const RowStat st = row_stat<F32, false, VPL>(l, lane, E);
-        const int id = lane < k ? a.rec[(int64_t)lane * a.rec_stride + row] : 0;
-        const bool bad = __ballot(lane < k && (id < 0 || id >= E)) != 0;
-        bool dup = false;
+    const int lane = threadIdx.x & 15, E = a.E, k = a.k;
+    for (int64_t row0 = (int64_t)blockIdx.x * 16; row0 < a.T; row0 += (int64_t)gridDim.x * 16) {
+        const int64_t row = row0 + (threadIdx.x >> 4);
+        const bool live = row < a.T;
+        const int64_t t = live ? row : row0;
+        const int id = lane < k ? a.rec[(int64_t)lane * a.rec_stride + t] : 0;
+        Row16<F32, VPL> r;
+        r.load(a.logits, t, E, lane);
+        int bad = lane < k && (id < 0 || id >= E), dup = 0;
         for (int j = 0; j < k; ++j) {
-            const int o = __shfl(id, j);
+            const int o = __shfl(id, j, 16);
             dup |= lane < k && j < lane && o == id;
         }
-        dup = __ballot(dup) != 0;
-        if (lane < k) {
-            const float ls = logit<F32>(a.logits, row * E + (bad ? 0 : id));
+        bad = ((__ballot(bad) >> (threadIdx.x & 48)) & 0xFFFF) != 0;
+        dup = ((__ballot(dup) >> (threadIdx.x & 48)) & 0xFFFF) != 0;
+        const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));
+        if (live && lane < k) {
             a.ids[row * k + lane] = id;
-            a.w[row * k + lane] = bad ? 0.f : (float)((double)a.scale * score<F32, false>(ls, st));
+            a.w[row * k + lane] = bad ? 0.f : (float)((double)a.scale * score<F32, false>(ls, r.st));
         }
         const int flags = (bad ? MOE_FLAG_BAD_ID : 0) | (dup ? MOE_FLAG_DUP_ID : 0);
-        if (lane == 0 && flags && status) atomicOr(status, flags);
+        if (live && lane == 0 && flags && status) atomicOr(status, flags);
     }
 }
 
@@ -804,67 +880,116 @@ struct ScoreGradArgs {
     float scale;
     float* d_gate;
     void* d_logits;
+    int lds_wave;  // floats of LDS for each wave
 };
 
-// One wave per token: the first k lanes have a slot each; every lane then writes
-// its elements of the row, each the sum of the slots that hold its expert.
+// 16 lanes per token, four tokens to a wave: lane j < k has slot j; the slots' values go
+// into the rows' place in LDS, from which whole rows are written. Bound by writing
+// [T, E] (and reading it, where every logit has a gradient).
 template <bool F32, bool SIGMOID, bool RENORM, bool PARTS, int VPL>
 __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
-    const int lane = threadIdx.x & 63, E = a.E, k = a.k;
-    const int64_t step = (int64_t)gridDim.x * 4;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.T; row += step) {
+    constexpr bool WHOLE = !SIGMOID && !RENORM;
+    extern __shared__ float lds_all[];
+    const int lane = threadIdx.x & 63, p = lane & 15, team = lane >> 4, E = a.E, k = a.k;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int EP = WHOLE ? (E + 3) & ~3 : E;  // a row's floats in LDS
+    float* lds = lds_all + wave * a.lds_wave;
+    float* mine = lds + team * EP;
+    const int64_t step = (int64_t)gridDim.x * 16;
+    for (int64_t row0 = ((int64_t)blockIdx.x * 4 + wave) * 4; row0 < a.T; row0 += step) {
+        const int64_t row = row0 + team;
+        const bool live = row < a.T;
+        const int64_t t = live ? row : row0;
+        const int id = p < k ? a.ids[t * k + p] : 0;
         float dw = 0.f;
         if constexpr (PARTS) {
-            if (lane < k) {
-                const int r = a.pair_row[row * k + lane];
-                if (r >= 0)
-                    for (int g = 0; g < a.ngroups; ++g) dw += a.part[(int64_t)r * MOE_GATE_PARTS + g];
-                a.d_gate[row * k + lane] = dw;
+            if (p < k) {
+                const int r = a.pair_row[t * k + p];
+                if (r >= 0) {
+                    const float* q = a.part + (int64_t)r * MOE_GATE_PARTS;
+                    for (int g = 0; g < a.ngroups; ++g) dw += q[g];
+                }
+                if (live) a.d_gate[row * k + p] = dw;
             }
-        } else if (lane < k) {
-            dw = a.d_w[row * k + lane];
+        } else if (p < k) {
+            dw = a.d_w[t * k + p];
         }
-        const int id = lane < k ? a.ids[row * k + lane] : 0;
-        const bool bad = __ballot(lane < k && (id < 0 || id >= E)) != 0;
-        float l[VPL];
-        RowStat st = {0.0, 0.0};
-        if constexpr (!SIGMOID && !RENORM) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = lane + 64 * i;
-                l[i] = e < E ? logit<F32>(a.logits, row * E + e) : 0.f;
-            }
-            st = row_stat<F32, false, VPL>(l, lane, E);
-        }
-        const float ls = logit<F32>(a.logits, row * E + (bad ? 0 : id));
-        const double s = score<F32, SIGMOID>(ls, st);
-        const double h = share<F32, SIGMOID, 16>(ls, s, lane, k, RENORM);
+        // zeros to the rows' place
+        for (int i = 4 * lane; i < 4 * EP; i += 256) *reinterpret_cast<float4*>(lds + i) = float4{0.f, 0.f, 0.f, 0.f};
+        const bool outside = p < k && (id < 0 || id >= E);
+        const bool bad = ((__ballot(outside) >> (16 * team)) & 0xFFFF) != 0;
+        Row16<F32, VPL> r;
+        r.st = {0.0, 0.0};
+        if constexpr (WHOLE) r.load(a.logits, t, E, p);
+        const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));
+        const double s = score<F32, SIGMOID>(ls, r.st);
+        const double h = share<F32, SIGMOID, 16>(ls, s, p, k, RENORM);
         double dot = 0.0;
-        if constexpr (RENORM || !SIGMOID) {
-            const double p = h * (double)dw;
-            for (int j = 0; j < k; ++j) dot += __shfl(p, j);
-        }
-        // a slot's gradient of its own logit (softmax without renorm: before the row's part)
-        double c = (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
+        if constexpr (RENORM || WHOLE) dot = team_sum<16>(p < k ? h * (double)dw : 0.0);
+        // the slot's gradient of its own logit; WHOLE: of its score
+        double c = WHOLE ? (double)a.scale * (double)dw : (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
         if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-(double)ls);
-        if (lane >= k || bad) c = 0.0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = lane + 64 * i;
-            double acc = 0.0;
+        wave_sync();
+        const bool on = p < k && !bad;
+        if (on) reinterpret_cast<int*>(mine)[id] = p;
+        wave_sync();
+        // an expert in several slots (a record may have that): each of them writes the sum
+        if (__ballot(on && reinterpret_cast<int*>(mine)[id] != p)) {
+            double sum = 0.0;
             for (int j = 0; j < k; ++j) {
-                const int o = __shfl(id, j);
-                const double oc = __shfl(c, j);
-                if (o == e) acc += oc;
+                const int o = __shfl(id, j, 16);
+                const double oc = __shfl(c, j, 16);
+                sum += o == id ? oc : 0.0;
             }
-            if constexpr (!SIGMOID && !RENORM) {
-                if (!bad && e < E) acc -= score<F32, false>(l[i], st) * (double)a.scale * dot;
+            c = sum;
+        }
+        wave_sync();
+        if (on) mine[id] = (float)c;
+        wave_sync();
+        if constexpr (WHOLE) {
+            const float scaled = bad ? 0.f : (float)((double)a.scale * dot), inv = bad ? 0.f : (float)r.st.inv;
+            char* out = static_cast<char*>(a.d_logits) + t * E * (F32 ? 4 : 2);
+#pragma unroll
+            for (int j = 0; j < VPL / 4; ++j) {
+                const int e = 64 * j + 4 * p;
+                if (!live || e >= E) continue;
+                const float4 q = *reinterpret_cast<const float4*>(mine + e);
+                float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // (by the root of the score: exp2 gives no values below the normal range)
+                    const float l = r.l[4 * j + i], root = exp32(0.5f * (l - r.m));
+                    v[i] = l == LOW ? 0.f : root * (root * (inv * (v[i] - scaled)));
+                }
+                if (e + 4 <= E) {
+                    if constexpr (F32) *reinterpret_cast<f4u*>(out + e * 4) = f4u{v[0], v[1], v[2], v[3]};
+                    else *reinterpret_cast<h4u*>(out + e * 2) = h4u{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+                } else {
+                    for (int i = 0; i < E - e; ++i) {
+                        if constexpr (F32) reinterpret_cast<float*>(out)[e + i] = v[i];
+                        else reinterpret_cast<uint16_t*>(out)[e + i] = (uint16_t)f32_to_bf16(v[i]);
+                    }
+                }
             }
-            if (e < E) {
-                if constexpr (F32) static_cast<float*>(a.d_logits)[row * E + e] = (float)acc;
-                else static_cast<uint16_t*>(a.d_logits)[row * E + e] = (uint16_t)f32_to_bf16((float)acc);
+        } else {
+            // the four rows are one piece of memory, from a multiple of four elements on
+            const int n = (int)(a.T - row0 < 4 ? a.T - row0 : 4) * E;
+            char* out = static_cast<char*>(a.d_logits) + row0 * E * (F32 ? 4 : 2);
+            for (int i = 4 * lane; i < n; i += 256) {
+                const float4 q = *reinterpret_cast<const float4*>(lds + i);
+                if (i + 4 <= n) {
+                    if constexpr (F32) *reinterpret_cast<float4*>(out + i * 4) = q;
+                    else *reinterpret_cast<uint2*>(out + i * 2) = uint2{cvt_bf16x2(q.x, q.y), cvt_bf16x2(q.z, q.w)};
+                } else {
+                    const float v[4] = {q.x, q.y, q.z, q.w};
+                    for (int j = 0; j < n - i; ++j) {
+                        if constexpr (F32) reinterpret_cast<float*>(out)[i + j] = v[j];
+                        else reinterpret_cast<uint16_t*>(out)[i + j] = (uint16_t)f32_to_bf16(v[j]);
+                    }
+                }
             }
         }
+        wave_sync();  // the next rows' zeros
     }
 }
 
@@ -926,6 +1051,15 @@ void with_vpl(int E, F&& f) {
     else f(std::integral_constant<int, 16>{});
 }
 
+// f(values per lane that hold E experts in 16 lanes)
+template <typename F>
+void with_row16(int E, F&& f) {
+    if (E <= 64) f(std::integral_constant<int, 4>{});
+    else if (E <= 256) f(std::integral_constant<int, 16>{});
+    else if (E <= 512) f(std::integral_constant<int, 32>{});
+    else f(std::integral_constant<int, 64>{});
+}
+
 template <bool F32, bool SIGMOID, int LPR, int VPL, int KT>
 void launch_topk(ScoreArgs a, hipStream_t stream) {
     constexpr int ROWS = 64 / LPR;
@@ -965,7 +1099,10 @@ void launch_choice_of(ScoreArgs a, hipStream_t stream) {
     while ((1 << a.group_bits) < G) ++a.group_bits;
     // groups a multiple of 32 floats apart would read the same banks
     a.spread = S % 32 == 0;
-    if (G > 32 || E < 4) {
+    // A whole wave to a row has the least to do in turn: one token of 256 experts 5.3 us against
+    // 5.9 (1024 tokens 6.0 against 6.5) with the rest of the chip idle, 4096 tokens 9.1 against 7.9;
+    // 64 and 512 experts are faster below (one token 3.5 against 3.5 us and 7.4 against 5.1).
+    if (G > 32 || E < 4 || (E > 128 && E <= 256 && a.T <= 1024)) {
         a.lds_wave = E;
         with_vpl(E, [&](auto v) {
             score_topk_exact_kernel<F32, SIGMOID, v.value>
@@ -997,13 +1134,16 @@ void launch_choice(const ScoreArgs& a, int32_t type, int32_t score, hipStream_t 
 }
 
 int launch_backward(ScoreGradArgs a, int32_t type, int32_t score, int32_t renorm, bool parts, hipStream_t stream) {
+    a.lds_wave = 4 * ((a.E + 3) / 4 * 4);
+    const dim3 grid = row_blocks(a.T, 16);
+    const size_t lds = (size_t)a.lds_wave * 4 * sizeof(float);
     with_forms(type, score, renorm, [&](auto t, auto s, auto r) {
-        with_vpl(a.E, [&](auto v) {
-            if (parts)
-                score_backward_kernel<t.value, s.value, r.value, true, v.value><<<row_blocks(a.T, 4), 256, 0, stream>>>(a);
-            else
-                score_backward_kernel<t.value, s.value, r.value, false, v.value><<<row_blocks(a.T, 4), 256, 0, stream>>>(a);
-        });
+        auto go = [&](auto v) {
+            if (parts) score_backward_kernel<t.value, s.value, r.value, true, v.value><<<grid, 256, lds, stream>>>(a);
+            else score_backward_kernel<t.value, s.value, r.value, false, v.value><<<grid, 256, lds, stream>>>(a);
+        };
+        if constexpr (!s.value && !r.value) with_row16(a.E, go);
+        else go(std::integral_constant<int, 4>{});
     });
     MOE_LAUNCH_CHECK("score_backward_kernel");
     return MOE_OK;
@@ -1086,8 +1226,8 @@ extern "C" int moe_replay_scored(const int32_t* rec, int32_t n_layers, int32_t k
     a.rec_stride = seq_len;
     with_forms(logits_type, score, renorm, [&](auto t, auto s, auto r) {
         if constexpr (!s.value && !r.value)
-            with_vpl(E, [&](auto v) {
-                score_replay_row_kernel<t.value, v.value><<<row_blocks(T, 4), 256, 0, stream>>>(a, dev_status);
+            with_row16(E, [&](auto v) {
+                score_replay_row_kernel<t.value, v.value><<<row_blocks(T, 16), 256, 0, stream>>>(a, dev_status);
             });
         else
             score_replay_kernel<t.value, s.value, r.value><<<row_blocks(T, 16), 256, 0, stream>>>(a, dev_status);
@@ -1105,7 +1245,7 @@ extern "C" int moe_route_scored_backward(const float* d_w, const void* logits, i
     MOE_REQUIRE(d_w && logits && ids && d_logits, MOE_ERR_NULL, "route_scored_backward: NULL argument");
     MOE_REQUIRE(aligned16(logits) && aligned16(d_logits), MOE_ERR_SHAPE,
                 "route_scored_backward: logits and d_logits: 16-byte aligned");
-    return launch_backward({d_w, nullptr, nullptr, 0, logits, ids, T, E, k, scale, nullptr, d_logits}, logits_type, score,
+    return launch_backward({d_w, nullptr, nullptr, 0, logits, ids, T, E, k, scale, nullptr, d_logits, 0}, logits_type, score,
                            renorm, false, stream);
 }
 
@@ -1122,7 +1262,7 @@ extern "C" int moe_route_scored_backward_parts(const float* gate_part, const int
                 "route_scored_backward_parts: NULL argument");
     MOE_REQUIRE(aligned16(logits) && aligned16(d_logits), MOE_ERR_SHAPE,
                 "route_scored_backward_parts: logits and d_logits: 16-byte aligned");
-    return launch_backward({nullptr, gate_part, pair_row, gate_groups(d), logits, ids, T, E, k, scale, d_gate, d_logits},
+    return launch_backward({nullptr, gate_part, pair_row, gate_groups(d), logits, ids, T, E, k, scale, d_gate, d_logits, 0},
                            logits_type, score, renorm, true, stream);
 }
 
