@@ -1,12 +1,14 @@
 """What stands between a model's residual stream and the experts, as plans of
 C-ABI calls on preallocated device buffers (no allocation per step): the choice
-of experts by scores, and the norms in front of and behind the layer.
+of experts by scores, the norms in front of and behind the layer, and a layer's
+training step from residual stream to residual stream.
 
 A plan's outputs are its own buffers, valid until its next call."""
 
 import torch
 
 from . import ops
+from .dense import MoELayerPlan
 from .layer import capture_graph
 from .ops import _dense, _Device, launch, rows_of, workspace_bytes
 
@@ -202,3 +204,41 @@ class JoinPlan:
     def capture(self, y, r, w_post=None, gate=None, w_pre=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
         return capture_graph(lambda: self.forward(y, r, w_post=w_post, gate=gate, w_pre=w_pre), warmup)
+
+
+class MoEBlockPlan:
+    """One layer's training step on the residual stream: with h = norm(r) from the
+    block before (its ``w_next``) or a NormPlan in front of the first,
+
+        y = layer(h)                                      (MoELayerPlan)
+        r_out, h_next = join(y, r)                        (JoinPlan)
+
+    on preallocated buffers.  scoring, act, act8 and router_bias as MoELayerPlan
+    takes them; r_dtype, w_dtype, post, gate, gate_dtype, gate_act, r_scale,
+    y_scale and eps as JoinPlan does; next_norm: whether a block follows."""
+
+    def __init__(self, T, d, f, E, k, fs, scoring=None, act="silu", act8=False, router_bias=False, r_dtype=BF16,
+                 w_dtype=BF16, post=False, next_norm=True, gate="none", gate_dtype=BF16, gate_act="none", r_scale=1.0,
+                 y_scale=1.0, eps=1e-6, device="cuda"):
+        self.layer = MoELayerPlan(T, d, f, E, k, fs, act=act, act8=act8, router_bias=router_bias, scoring=scoring,
+                                  device=device)
+        self.join = JoinPlan(T, d, r_dtype=r_dtype, w_dtype=w_dtype, post=post, pre=next_norm, gate=gate,
+                             gate_dtype=gate_dtype, gate_act=gate_act, r_scale=r_scale, y_scale=y_scale, eps=eps, train=True,
+                             device=self.layer.router.device)
+
+    def forward(self, r, h, Wr, wts, W13s, W2s, br=None, w_post=None, gate=None, w_next=None, replay=None):
+        """(r_out, h_next) for the stream r [T, d] and its norm h [T, d]; weights as
+        MoELayerPlan.forward and JoinPlan.forward take them."""
+        y = self.layer.forward(h, Wr, wts, W13s, W2s, br=br, replay=replay)
+        return self.join.forward(y, r, w_post=w_post, gate=gate, w_pre=w_next)
+
+    def backward(self, d_r, d_h, h, Wr, wts, W13s, W2s, w_post=None, gate=None, w_next=None):
+        """Gradients of the last forward for d_r (of r_out along the stream) and d_h
+        (of h_next; None without it): the layer's (dx as ``dh``, of h) and the
+        join's (``dr``, of r along the stream; dw_post, dw_next, dgate).  The block
+        before takes (dr, dh) as its (d_r, d_h)."""
+        g = self.join.backward(d_r, d_h, self.layer.shared.y, w_post=w_post, gate=gate, w_pre=w_next)
+        out = self.layer.backward(g["dy"], h, Wr, wts, W13s, W2s)
+        out["dh"] = out.pop("dx")
+        out.update(dr=g["dr"], dw_post=g["dw_post"], dw_next=g["dw_pre"], dgate=g["dgate"])
+        return out

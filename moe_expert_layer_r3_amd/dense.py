@@ -176,14 +176,16 @@ class MoELayerPlan:
     [G, U] are kept in 8 bits for the backward (fs % 128 == 0), 1.03 bytes per
     value.  The router's dWr and the shared expert's dW13s are then products with x
     as restored from them (``xr``, valid after a backward until the next call).
+    scoring: experts chosen by scores (see ForwardPlan; ``routed.route_bias`` and
+    ``routed.load`` are the balance bias and the experts' load).
     Needs every expert on this GPU (L == E): under expert parallelism d_logits
     has to be summed over the GPUs between the parts."""
 
-    def __init__(self, T, d, f, E, k, fs, act="silu", act8=False, router_bias=False, device="cuda"):
+    def __init__(self, T, d, f, E, k, fs, act="silu", act8=False, router_bias=False, scoring=None, device="cuda"):
         self.T, self.d = T, d
         self.router = LinearPlan(T, d, E, out_dtype=torch.float32, train=True, bias=router_bias, device=device)
         dv = self.router.device
-        self.routed = TrainPlan(T, d, f, E, E, k, device=dv)
+        self.routed = TrainPlan(T, d, f, E, E, k, device=dv, scoring=scoring)
         self.shared = GatedFFNPlan(T, d, fs, act=act, save="int8" if act8 else "bf16", device=dv)
         self.x8 = self.xr = None
         if act8:
@@ -193,14 +195,15 @@ class MoELayerPlan:
             # gradients of its rows (at least T): no memory of its own
             self.xr = self.routed.dX[:T]
 
-    def forward(self, x, Wr, wts, W13s, W2s, br=None):
+    def forward(self, x, Wr, wts, W13s, W2s, br=None, replay=None):
         """y [T, d]; wts from quantize_weights (with its transposed copies where
-        ``self.routed.transpose_weights``)."""
+        ``self.routed.transpose_weights``); replay = (rec, layer, s0) replays
+        recorded ids."""
         with _Device(self.router.device):
             if self.x8 is not None:
                 ops.act_save(x, out=self.x8)
             logits = self.router.forward(x, Wr, bias=br)
-            y = self.routed.forward(x, logits, wts)
+            y = self.routed.forward(x, logits, wts, replay=replay)
             return self.shared.forward(x, W13s, W2s, residual=y)
 
     def backward(self, dy, x, Wr, wts, W13s, W2s):
@@ -208,7 +211,8 @@ class MoELayerPlan:
         router_bias), dW13 and dW2 (routed experts), dW13s and dW2s.  With act8,
         x is not read (None will do)."""
         with _Device(self.router.device):
-            dx, dW13, dW2, d_logits = self.routed.backward(x, dy, wts)  # (x is in its own 8-bit copies)
+            # (x is in its own 8-bit copies)
+            dx, dW13, dW2, d_logits = self.routed.backward(x, dy, wts, logits=self.router.out)
             if self.x8 is not None:
                 x = ops.act_restore(*self.x8, out=self.xr)
             dx, dWr, dbr = self.router.backward(d_logits, x, Wr, dx_add=dx)

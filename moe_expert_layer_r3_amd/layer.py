@@ -76,12 +76,16 @@ class ForwardPlan:
     """Device buffers for one forward pass of T tokens.  pow2: power-of-two
     (UE8M0) activation scales, applied by the MFMA; the weights must then come
     from quantize_weights(..., pow2=True).  mxfp4: MXFP4 weights (from
-    quantize_weights(..., mxfp4=True)) with power-of-two FP8 activations."""
+    quantize_weights(..., mxfp4=True)) with power-of-two FP8 activations.
+    scoring (ops.Scoring): the experts are chosen and weighted by scores instead
+    of the top-k of raw logits; ``route_bias`` (fp32 [E]) and ``load`` (int32 [E],
+    counted on) may then be set to tensors of the caller."""
 
-    def __init__(self, T, d, f, E, L, k, e0=0, device="cuda", save_gu=False, pow2=False, mxfp4=False):
+    def __init__(self, T, d, f, E, L, k, e0=0, device="cuda", save_gu=False, pow2=False, mxfp4=False, scoring=None):
         self.T, self.d, self.f, self.E, self.L, self.k, self.e0 = T, d, f, E, L, k, e0
         self.sflag = ops.SCALE_POW2 if (pow2 or mxfp4) else 0  # activation quantisers
         self.gflag = self.sflag | (ops.WEIGHT_MXFP4 if mxfp4 else 0)  # forward GEMMs
+        self.scoring, self.route_bias, self.load = scoring, None, None
         self.rcap = ops.row_cap(T, k, L)
         dv = device
         i32, f32, u8, b16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
@@ -107,6 +111,9 @@ class ForwardPlan:
     # each stage is one C-ABI call on the current stream
     def route(self, logits):
         _check(logits, (self.T, self.E), torch.float32, "logits")
+        if self.scoring is not None:
+            ops.route_scored(logits, self.k, self.scoring, bias=self.route_bias, load=self.load, out=(self.ids, self.w))
+            return
         _call("moe_route_topk", _p(logits), self.T, self.E, self.k, _p(self.ids), _p(self.w), _stream())
 
     def replay(self, rec, layer, s0, logits):
@@ -117,6 +124,9 @@ class ForwardPlan:
             raise ValueError(f"record top_k {k} differs from the plan's k {self.k}")
         _check(rec, (NL, self.k, S), torch.int32, "record")
         _check(logits, (self.T, self.E), torch.float32, "logits")
+        if self.scoring is not None:
+            ops.replay_scored(rec, layer, s0, logits, self.scoring, status=self.status, out=(self.ids, self.w))
+            return
         _call("moe_replay_load", _p(rec), NL, k, S, layer, s0, self.T, _p(logits), self.E, _p(self.ids),
               _p(self.w), _p(self.status), _stream())
 
@@ -205,8 +215,8 @@ class TrainPlan(ForwardPlan):
       dW2 = dY^T H, dW13 = [dG, dU]^T X
       softmax-over-selection backward -> d_logits."""
 
-    def __init__(self, T, d, f, E, L, k, e0=0, device="cuda", pow2=False, mxfp4=False):
-        super().__init__(T, d, f, E, L, k, e0=e0, device=device, save_gu=True, pow2=pow2, mxfp4=mxfp4)
+    def __init__(self, T, d, f, E, L, k, e0=0, device="cuda", pow2=False, mxfp4=False, scoring=None):
+        super().__init__(T, d, f, E, L, k, e0=e0, device=device, save_gu=True, pow2=pow2, mxfp4=mxfp4, scoring=scoring)
         # FP8 weights with d, f multiples of 256: the dgrad products read the
         # forward weights [out, in] as their [K, N] operand, so no transposed
         # copy is made; otherwise (MXFP4, or other shapes) they read the copies
@@ -293,16 +303,25 @@ class TrainPlan(ForwardPlan):
               _p(self.xqT_s), _p(self.offsets), self.L, self.rcap, 2 * self.f, self.d, _p(self.dW13), self.sflag,
               _stream())
 
-    def gate_bwd(self):
+    def gate_bwd(self, logits=None):
+        if self.scoring is not None:
+            ops.route_scored_backward_parts(self.gate_part, self.pair_row, self.rcap, self.d, logits, self.ids,
+                                            self.scoring, out=(self.d_gate, self.d_logits))
+            return
         _call("moe_gate_backward_parts", _p(self.gate_part), _p(self.pair_row), self.rcap, self.d, _p(self.w),
               _p(self.ids), self.T, self.k, self.E, _p(self.d_gate), _p(self.d_logits), _stream())
 
     BWD_STAGES = ("combine_bwd", "dgrad2", "swiglu_bwd", "dgrad1", "unpermute", "wgrad2", "wgrad13", "gate_bwd")
 
-    def backward(self, x, dy, wts, events=None):
+    def backward(self, x, dy, wts, events=None, logits=None):
         """Backward of the last ``forward`` for upstream gradient dy [T, d] bf16;
         wts must hold the transposed weight copies (quantize_weights(transpose=True))
-        when ``self.transpose_weights``."""
+        when ``self.transpose_weights``; logits: the forward's, where the plan has a
+        scoring (its gradient needs the scores)."""
+        if self.scoring is not None:
+            if logits is None:
+                raise ValueError("a plan with a scoring needs the forward's logits")
+            _check(logits, (self.T, self.E), torch.float32, "logits")
         def rec(name, fn, *a):
             if events is not None and name in events:
                 events[name][0].record()
@@ -317,5 +336,5 @@ class TrainPlan(ForwardPlan):
         rec("unpermute", self.unpermute)
         rec("wgrad2", self.wgrad2)
         rec("wgrad13", self.wgrad13)
-        rec("gate_bwd", self.gate_bwd)
+        rec("gate_bwd", self.gate_bwd, logits)
         return self.dx, self.dW13, self.dW2, self.d_logits

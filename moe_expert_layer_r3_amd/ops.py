@@ -618,8 +618,9 @@ def route_scored_backward(d_w, logits, ids, scoring, out=None):
     return out
 
 
-def route_scored_backward_parts(gate_part, pair_row, rcap, d, logits, ids, scoring):
-    """(d_gate [T, k], d_logits [T, E]) from the partials of combine_backward_rows."""
+def route_scored_backward_parts(gate_part, pair_row, rcap, d, logits, ids, scoring, out=None):
+    """(d_gate [T, k], d_logits [T, E]) from the partials of combine_backward_rows;
+    ``out`` receives them without allocating."""
     lt = _logits_type(logits)
     T, E = logits.shape
     dev = _dev(logits)
@@ -628,8 +629,11 @@ def route_scored_backward_parts(gate_part, pair_row, rcap, d, logits, ids, scori
     _dense(ids, (T, k), torch.int32, "ids", dev)
     _dense(pair_row, (T, k), torch.int32, "pair_row", dev)
     _dense(gate_part, (rcap, GATE_PARTS), torch.float32, "gate_part", dev)
-    d_gate = torch.empty((T, k), dtype=torch.float32, device=dev)
-    out = torch.empty_like(logits)
+    if out is None:
+        d_gate, out = torch.empty((T, k), dtype=torch.float32, device=dev), torch.empty_like(logits)
+    else:
+        d_gate = _dense(out[0], (T, k), torch.float32, "d_gate", dev)
+        out = _dense(out[1], (T, E), logits.dtype, "d_logits", dev)
     launch("moe_route_scored_backward_parts", dev, gate_part.data_ptr(), pair_row.data_ptr(), rcap, d, logits.data_ptr(), lt,
            ids.data_ptr(), T, k, E, scoring.code, scoring.renorm, scoring.scale, d_gate.data_ptr(), out.data_ptr())
     return d_gate, out
