@@ -96,7 +96,9 @@ __device__ __forceinline__ Gate gate_of(float x, int act) {
     const float e = expf(-fabsf(x)), q = 1.0f / (1.0f + e);
     return {x >= 0.f ? q : e * q, e * q * q};
 }
-__device__ __forceinline__ float gate_value(float x, int act) { return gate_of(x, act).value; }
+__device__ __forceinline__ float gate_value(float x, int act) {
+    return act == MOE_ACT_SIGMOID ? 1.0f / (1.0f + expf(-x)) : x;
+}
 __device__ __forceinline__ float gate_slope(float x, int act) { return gate_of(x, act).slope; }
 
 // Sum over the workgroup, the same in every thread; `slot` alternates so that one
@@ -110,6 +112,14 @@ __device__ __forceinline__ float block_sum(float v, float (*lds)[NT / 64], int& 
     for (int i = 0; i < NT / 64; ++i) s += lds[slot][i];
     slot ^= 1;
     return s;
+}
+
+// r_out of one element, each operation rounded as it is written: r_out is stored in as few
+// as eight bits, and where it lies next to the border of two of them, the same
+// operations give the same one.
+__device__ __forceinline__ float joined(float r, float y, float rho, float w, float g, float r_scale, float y_scale) {
+#pragma clang fp contract(off)
+    return r_scale * r + y_scale * (g * (y * rho * w));
 }
 
 // eight gate values of row t, columns c ...
@@ -155,10 +165,9 @@ __global__ __launch_bounds__(NT) void join_kernel(JoinArgs a) {
                 gate8(g, a.gate, a.gate_kind, a.gate_f32, t, c, d);
                 if (a.w_post) load8(w, a.w_post, c, a.w_f32);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float n = a.w_post ? v[j] * rho_y * w[j] : v[j];
-                    rv[j] = a.r_scale * rv[j] + a.y_scale * (gate_value(g[j], a.gate_act) * n);
-                }
+                for (int j = 0; j < 8; ++j)
+                    rv[j] = joined(rv[j], v[j], rho_y, a.w_post ? w[j] : 1.0f, gate_value(g[j], a.gate_act), a.r_scale,
+                                   a.y_scale);
                 store8(a.r_out, t * d + c, RF32, rv);
             }
 #pragma unroll
@@ -401,20 +410,15 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a
     int slot = 0;
     const int64_t d = a.d;
     const Team tm = team_of<WAVE>(d, L);
-    float wz[8], wn[8];  // of y: y_scale, the norm's weight, a channel's gate; of the next norm
+    float wp[8], gc[8], wn[8];  // weights of y's norm, a channel's gate, weights of the next norm
 #pragma unroll
-    for (int j = 0; j < 8; ++j) wz[j] = a.y_scale, wn[j] = 0.f;
+    for (int j = 0; j < 8; ++j) wp[j] = gc[j] = 1.0f, wn[j] = 0.f;
     if (tm.on) {
-        float v[8];
-        if (Y && a.w_post) {
-            load8(v, a.w_post, tm.c, a.w_f32);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) wz[j] *= v[j];
-        }
+        if (Y && a.w_post) load8(wp, a.w_post, tm.c, a.w_f32);
         if (Y && a.gate_kind == MOE_GATE_CHANNEL) {
-            load8(v, a.gate, tm.c, a.gate_f32);
+            load8(gc, a.gate, tm.c, a.gate_f32);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) wz[j] *= gate_value(v[j], a.gate_act);
+            for (int j = 0; j < 8; ++j) gc[j] = gate_value(gc[j], a.gate_act);
         }
         if (a.w_pre) load8(wn, a.w_pre, tm.c, a.w_f32);
     }
@@ -438,21 +442,22 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a
         if (t0 + tm.rows < a.T) fetch(t + tm.rows < a.T ? t + tm.rows : last);
         float rv[8];
         if constexpr (Y) {
-            float f = 1.0f;
+            float rho_y = 1.0f;
             if (a.w_post) {
                 float s[1] = {0.f};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[0] += y[j] * y[j];
                 team_sum<WAVE>(s, L, lds, slot);
-                f = 1.0f / sqrtf(s[0] / (float)d + a.eps);
-                if (a.rstd_post && live && tm.c == 0) a.rstd_post[t] = f;
+                rho_y = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+                if (a.rstd_post && live && tm.c == 0) a.rstd_post[t] = rho_y;
             }
-            if (a.gate_kind == MOE_GATE_TOKEN) f *= gate_value(load1(a.gate, live ? t : last, a.gate_f32), a.gate_act);
+            float gt = 1.0f;
+            if (a.gate_kind == MOE_GATE_TOKEN) gt = gate_value(load1(a.gate, live ? t : last, a.gate_f32), a.gate_act);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float z = y[j] * f * wz[j];
-                if constexpr (FULL != FULL_NONE) z *= gate_value(g[j], a.gate_act);
-                rv[j] = stored(a.r_scale * r[j] + z, RF32);
+                float f = FULL != FULL_NONE ? gate_value(g[j], a.gate_act) : gc[j];
+                if (a.gate_kind == MOE_GATE_TOKEN) f = gt;
+                rv[j] = stored(joined(r[j], y[j], rho_y, wp[j], f, a.r_scale, a.y_scale), RF32);
             }
             if (live && tm.on) store8(a.r_out, t * d + tm.c, RF32, rv);
         } else {
