@@ -20,6 +20,16 @@ def _device(device):
     return dv if dv.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _type(dtype, what):
+    if dtype not in ops.SRC_TYPES:
+        raise TypeError(f"{what}: bf16 or fp32, got {dtype}")
+    return ops.SRC_TYPES[dtype]
+
+
 class RoutePlan:
     """The choice of k of E experts for T tokens by ``scoring`` (ops.Scoring), or
     its replay from a record, and the gradient of its weights when ``train``.
@@ -30,48 +40,51 @@ class RoutePlan:
         if logits_dtype not in ops.SRC_TYPES:
             raise TypeError(f"logits_dtype: bf16 or fp32, got {logits_dtype}")
         self.T, self.E, self.k, self.scoring, self.logits_dtype = T, E, k, scoring, logits_dtype
+        self.lt = ops.SRC_TYPES[logits_dtype]
         dv = self.device = _device(device)
         self.ids = torch.empty((T, k), dtype=torch.int32, device=dv)
         self.w = torch.empty((T, k), dtype=F32, device=dv)
         self.status = torch.zeros(1, dtype=torch.int32, device=dv)
         self.d_logits = torch.empty((T, E), dtype=logits_dtype, device=dv) if train else None
-
-    def _logits(self, logits):
-        _dense(logits, (self.T, self.E), self.logits_dtype, "logits", self.device)
+        self._ids, self._w, self._status, self._d_logits = (_ptr(t) for t in (self.ids, self.w, self.status, self.d_logits))
 
     def forward(self, logits, bias=None, load=None, capture=None):
         """(ids, w) of logits [T, E]; bias, load and capture as for ops.route_scored."""
-        self._logits(logits)
-        return ops.route_scored(logits, self.k, self.scoring, bias=bias, load=load, capture=capture, out=(self.ids, self.w))
+        dv, E, c = self.device, self.E, self.scoring
+        _dense(logits, (self.T, E), self.logits_dtype, "logits", dv)
+        if bias is not None:
+            _dense(bias, (E,), F32, "bias", dv)
+        if load is not None:
+            _dense(load, (E,), torch.int32, "load", dv)
+        rec = (None, 0, 0, 0, 0) if capture is None else ops.record_args(*capture, self.k, dv)
+        launch("moe_route_scored", dv, logits.data_ptr(), self.lt, self.T, E, self.k, c.code, _ptr(bias), c.groups,
+               c.top_groups, c.group_top, c.renorm, c.scale, self._ids, self._w, _ptr(load), *rec)
+        return self.ids, self.w
 
     def replay(self, rec, layer, s0, logits):
         """(ids, w) of tokens s0 .. s0 + T - 1 of a record's layer."""
-        self._logits(logits)
-        if rec.shape[1] != self.k:
-            raise ValueError(f"record top_k {rec.shape[1]} differs from the plan's k {self.k}")
-        return ops.replay_scored(rec, layer, s0, logits, self.scoring, status=self.status, out=(self.ids, self.w))
+        dv, c = self.device, self.scoring
+        _dense(logits, (self.T, self.E), self.logits_dtype, "logits", dv)
+        p, NL, S, layer, s0 = ops.record_args(rec, layer, s0, self.k, dv)
+        launch("moe_replay_scored", dv, p, NL, self.k, S, layer, s0, self.T, logits.data_ptr(), self.lt, self.E, c.code,
+               c.renorm, c.scale, self._ids, self._w, self._status)
+        return self.ids, self.w
 
     def backward(self, d_w, logits):
         """d_logits [T, E] of the last call's weights for d_w [T, k]."""
         if self.d_logits is None:
             raise ValueError("the plan was made without train=True")
-        self._logits(logits)
-        return ops.route_scored_backward(d_w, logits, self.ids, self.scoring, out=self.d_logits)
+        dv, c = self.device, self.scoring
+        _dense(logits, (self.T, self.E), self.logits_dtype, "logits", dv)
+        _dense(d_w, (self.T, self.k), F32, "d_w", dv)
+        launch("moe_route_scored_backward", dv, d_w.data_ptr(), logits.data_ptr(), self.lt, self._ids, self.T, self.k, self.E,
+               c.code, c.renorm, c.scale, self._d_logits)
+        return self.d_logits
 
     def capture(self, logits, bias=None, load=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture);
         the warm-up calls count into load too."""
         return capture_graph(lambda: self.forward(logits, bias=bias, load=load), warmup)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _type(dtype, what):
-    if dtype not in ops.SRC_TYPES:
-        raise TypeError(f"{what}: bf16 or fp32, got {dtype}")
-    return ops.SRC_TYPES[dtype]
 
 
 class NormPlan:
@@ -137,6 +150,7 @@ class JoinPlan:
         if gate_act not in ("none", "sigmoid"):
             raise ValueError(f"unknown gate_act {gate_act!r}: none or sigmoid")
         self.T, self.d, self.post, self.pre, self.eps = T, d, post, pre, eps
+        self.shape = (T, d)
         self.r_dtype, self.w_dtype, self.gate_dtype = r_dtype, w_dtype, gate_dtype
         self.rt, self.wt = _type(r_dtype, "r_dtype"), _type(w_dtype, "w_dtype")
         self.gate_shape = dict(none=None, channel=(d,), token=(T,), full=(T, d))[gate]
@@ -145,6 +159,7 @@ class JoinPlan:
         e = lambda shape, dt: torch.empty(shape, dtype=dt, device=dv)
         self.r_out = e((T, d), r_dtype)
         self.h = e((T, d), BF16) if pre else None
+        self._outs = (self.r_out.data_ptr(), _ptr(self.h))
         self.rstd_post = self.rstd_pre = self.dr = self.dy = self.dw_post = self.dw_pre = self.dgate = self.ws = None
         if train:
             with _Device(dv):
@@ -156,15 +171,20 @@ class JoinPlan:
                 self.rstd_pre, self.dw_pre = e(T, F32), e(d, w_dtype)
             if self.gate_shape is not None:
                 self.dgate = e(self.gate_shape, gate_dtype)
+        self._rstd = (_ptr(self.rstd_post), _ptr(self.rstd_pre))
+        self._grads = tuple(_ptr(t) for t in (self.dr, self.dy, self.dw_post, self.dw_pre, self.dgate, self.ws))
+
+    def _weight(self, w, there, name):
+        if (w is not None) != there:
+            raise ValueError(f"{name}: the plan was made {'with' if there else 'without'} this norm")
+        if there:
+            _dense(w, (self.d,), self.w_dtype, name, self.device)
 
     def _operands(self, y, w_post, gate, w_pre):
-        dv, d = self.device, self.d
-        ldy = rows_of(y, (self.T, d), BF16, "y", dv)
-        for t, there, name in ((w_post, self.post, "w_post"), (w_pre, self.pre, "w_pre")):
-            if (t is not None) != there:
-                raise ValueError(f"{name}: the plan was made {'with' if there else 'without'} this norm")
-            if there:
-                _dense(t, (d,), self.w_dtype, name, dv)
+        dv = self.device
+        ldy = rows_of(y, self.shape, BF16, "y", dv)
+        self._weight(w_post, self.post, "w_post")
+        self._weight(w_pre, self.pre, "w_pre")
         if (gate is not None) != (self.gate_shape is not None):
             raise ValueError("gate: not as the plan was made")
         if gate is not None:
@@ -177,8 +197,7 @@ class JoinPlan:
         ldy = self._operands(y, w_post, gate, w_pre)
         ldr = rows_of(r, (T, d), self.r_dtype, "r", dv)
         launch("moe_join", dv, y.data_ptr(), ldy, r.data_ptr(), self.rt, ldr, _ptr(w_post), _ptr(gate), *self.gate_args,
-               _ptr(w_pre), self.wt, T, d, self.eps, self.r_out.data_ptr(), _ptr(self.h), _ptr(self.rstd_post),
-               _ptr(self.rstd_pre))
+               _ptr(w_pre), self.wt, T, d, self.eps, *self._outs, *self._rstd)
         return self.r_out, self.h
 
     def backward(self, d_out, dh, y, w_post=None, gate=None, w_pre=None):
@@ -196,9 +215,8 @@ class JoinPlan:
         if dh is not None:
             _dense(dh, (T, d), BF16, "dh", dv)
         launch("moe_join_backward", dv, _ptr(d_out), _ptr(dh), y.data_ptr(), ldy, self.r_out.data_ptr(), self.rt,
-               _ptr(w_post), _ptr(gate), *self.gate_args, _ptr(w_pre), self.wt, _ptr(self.rstd_post), _ptr(self.rstd_pre),
-               T, d, self.dr.data_ptr(), self.dy.data_ptr(), _ptr(self.dw_post), _ptr(self.dw_pre), _ptr(self.dgate),
-               self.ws.data_ptr(), self.ws.numel())
+               _ptr(w_post), _ptr(gate), *self.gate_args, _ptr(w_pre), self.wt, *self._rstd, T, d, *self._grads,
+               self.ws.numel())
         return dict(dr=self.dr, dy=self.dy, dw_post=self.dw_post, dw_pre=self.dw_pre, dgate=self.dgate)
 
     def capture(self, y, r, w_post=None, gate=None, w_pre=None, warmup=1):

@@ -697,13 +697,13 @@ Shape shape_of(int64_t d) {
     while (L < chunks) L <<= 1;
     return {L, 256, 4 * (64 / L)};
 }
-// workgroups of a backward launch: enough to fill the compute units, but eight rows at
+// workgroups of a backward launch: enough to fill the compute units, but four rows at
 // least to each where there are more rows than units, for the partial sums' sake
 int64_t backward_blocks(int64_t T, int64_t d) {
     const Shape s = shape_of(d);
     const int64_t cus = num_cus(), units = (T + s.per - 1) / s.per;
     int64_t n = cus * (1024 / s.threads);
-    const int64_t most = units / 8 > cus ? units / 8 : cus;
+    const int64_t most = units / 4 > cus ? units / 4 : cus;
     n = n < most ? n : most;
     if (d > MAX_ROW) n = n < (1 << 27) / d ? n : (1 << 27) / d;
     return units < n ? units : n;

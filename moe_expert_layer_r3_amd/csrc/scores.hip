@@ -400,6 +400,13 @@ __device__ __forceinline__ void shift4(float* v, int n) {
     v[2] = n == 1 ? c : v[2];
 }
 
+// fmaxf makes its arguments canonical first; these are
+__device__ __forceinline__ float max_of_numbers(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 // LPR lanes to a row, VPL logits to a lane (4 neighbours in every 4 LPR), k <= KT.
 //
 // The choice is defined by scores that are rounded from 64 bits, but 32 bits decide
@@ -507,16 +514,21 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
             else return exp32(l - m) * s_max;
         };
         if constexpr (BIAS) {
+            auto add_bias = [&](auto masked) {
 #pragma unroll
-            for (int j = 0; j < N4; ++j) {
-                const float4 q = *reinterpret_cast<const float4*>(bias + 4 * LPR * j + 4 * p);
-                const float b[4] = {q.x, q.y, q.z, q.w};
+                for (int j = 0; j < N4; ++j) {
+                    const float4 q = *reinterpret_cast<const float4*>(bias + 4 * LPR * j + 4 * p);
+                    const float b[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float v = __builtin_amdgcn_fmed3f(score32(c[4 * j + i]) + b[i], LOW, -LOW);
-                    c[4 * j + i] = some_masked && c[4 * j + i] == LOW ? LOW : v;
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = __builtin_amdgcn_fmed3f(score32(c[4 * j + i]) + b[i], LOW, -LOW);
+                        if constexpr (masked.value) c[4 * j + i] = c[4 * j + i] == LOW ? LOW : v;
+                        else c[4 * j + i] = v;
+                    }
                 }
-            }
+            };
+            if (some_masked) add_bias(std::true_type{});
+            else add_bias(std::false_type{});
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_fmed3f(c[i], LOW, -LOW) + 0.0f;  // (-0 is 0)
@@ -544,7 +556,7 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
             auto take = [&](float v) {
                 if (scores) v = v == LOW ? LOW : score32(v);
                 t2 = __builtin_amdgcn_fmed3f(t1, t2, v);
-                t1 = __builtin_amdgcn_fmed3f(t1, v, INFINITY);
+                t1 = max_of_numbers(t1, v);
             };
             if (g < a.groups) {
                 const float* q = mine + g * S;
@@ -585,7 +597,7 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
             // (equal logits are equal, and the lower group stays)
             unsure |= !(last - next > far || (!BIAS && !sums && last == next && last > 0.5f * LOW));
             const uint32_t stay = (uint32_t)(__ballot(stays) >> (team * LPR));
-            if (quads) {
+            if (VL < VPL || quads) {
                 // the fours of the groups that stay, in order; which group is the o-th of them, by a table
                 int* table = reinterpret_cast<int*>(mine + a.lds_row - 32);
                 if (stays && sub == 0) table[__popc(stay & ((1u << p) - 1u)) >> shift] = g;

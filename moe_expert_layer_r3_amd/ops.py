@@ -697,12 +697,13 @@ def rows_of(t, shape, dtype, name, dev=None):
     elements, and lives on ``dev``."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+    strides = t.stride()
+    if t.shape != shape or (shape[1] > 1 and strides[1] != 1):
         raise ValueError(f"{name}: expected shape {tuple(shape)} with adjacent row elements, got {tuple(t.shape)} "
-                         f"with strides {tuple(t.stride())}")
-    if not t.is_cuda or (dev is not None and t.device != dev):
+                         f"with strides {tuple(strides)}")
+    if t.device != dev if dev is not None else not t.is_cuda:
         raise ValueError(f"{name}: must live on the GPU{'' if dev is None else f' {dev}'}, got {t.device}")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return strides[0] if shape[0] > 1 else shape[1]
 
 
 def act_save(x, out=None):
