@@ -272,7 +272,7 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int e = lane + 64 * i;
-            if (e < E && !((stay >> ((uint32_t)(e * a.inv_S) >> 22 << shift)) & 1ull)) key[i] = 0.0;
+            if (e < E && !((stay >> ((uint32_t)e * (uint32_t)a.inv_S >> 22 << shift)) & 1ull)) key[i] = 0.0;
         }
         wave_sync();  // the next row's values
     }
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
         for (int i = 0; i < (L4 + 5) / 6; ++i) group_of[i] = 0;
 #pragma unroll
         for (int j = 0; j < L4; ++j)
-            group_of[j / 6] |= ((uint32_t)((4 * LPR * j + 4 * p) * a.inv_S) >> 22 & 31u) << (5 * (j % 6));
+            group_of[j / 6] |= ((uint32_t)(4 * LPR * j + 4 * p) * (uint32_t)a.inv_S >> 22 & 31u) << (5 * (j % 6));
     }
     const int64_t step = (int64_t)gridDim.x * 4 * ROWS;
     float c[VPL];
@@ -625,7 +625,7 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
 #pragma unroll
                 for (int i = 0; i < VL; ++i) {
                     const int e = 4 * LPR * (i >> 2) + 4 * p + (i & 3);
-                    const bool in = (stay >> (((uint32_t)(e * a.inv_S) >> 22) << shift)) & 1u;
+                    const bool in = (stay >> (((uint32_t)e * (uint32_t)a.inv_S >> 22 << shift) & 31u)) & 1u;
                     v_of[i] = in && e < E ? c[i] : LOW;
                 }
             }

@@ -74,6 +74,28 @@ def choice(l, s, kind, k, bias=None, groups=1, top_groups=1, group_top=2):
     return ids
 
 
+def choices(l, s, kind, k, bias=None, groups=1, top_groups=1, group_top=2):
+    """The same for many tokens at once."""
+    T, E = l.shape
+    with np.errstate(invalid="ignore", over="ignore"):
+        c = s.astype(np.float32)
+        if bias is not None:
+            c = c + bias[None, :].astype(np.float32)
+        c = np.where(masked(l, kind), np.float32(-np.inf), c)
+        out = np.zeros((T, E), dtype=bool)
+        if groups > 1 and top_groups < groups:
+            v = np.where(np.isnan(c), np.float32(-np.inf), c).reshape(T, groups, E // groups)
+            v = -np.sort(-v, axis=2)[:, :, :group_top]
+            value = np.where(v > -np.inf, v, np.float32(0)).sum(axis=2, dtype=np.float32)
+            value[v[:, :, 0] == -np.inf] = -np.inf
+            place = np.argsort(np.argsort(-value, axis=1, kind="stable"), axis=1, kind="stable")
+            out = np.repeat(place >= top_groups, E // groups, axis=1)
+        last = np.isnan(c)
+        key = np.where(last, 0.0, -c.astype(np.float64))
+        e = np.broadcast_to(np.arange(E), (T, E))
+        return np.lexsort((e, key, last, out), axis=1)[:, :k].astype(np.int32)
+
+
 def weights(l, s, kind, ids, score, renorm, scale):
     """fp64 (weights, shares) [T, k]."""
     sel = np.take_along_axis(s, ids.astype(np.int64), axis=1)

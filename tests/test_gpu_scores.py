@@ -61,7 +61,9 @@ def check_route(T, E, k, score, kind="f32", special="", bias=False, groups=1, to
     ids, w = plan.forward(lg, bias=b, load=load, capture=(rec, 1, 4))
     l = np64(lg)
     s = R.scores(l, kind, score)
-    ref = R.choice(l, s, kind, k, None if b is None else npi(b), groups, top_groups, group_top)
+    ref = R.choices(l, s, kind, k, None if b is None else npi(b), groups, top_groups, group_top)
+    few = R.choice(l[:64], s[:64], kind, k, None if b is None else npi(b), groups, top_groups, group_top)
+    assert np.array_equal(ref[:64], few), "the two references"
     assert np.array_equal(npi(ids), ref), "ids"
     rw, _ = R.weights(l, s, kind, ref, score, renorm, scale)
     close(w, rw, (R.ROUND["f32"] + R.row_err(E, score, renorm)) * np.abs(rw) + R.TINY["f32"] + 2.0 ** -46 * abs(scale) * (rw != 0), "w")
@@ -107,6 +109,55 @@ def test_route_special(special, score, E, k, groups, top_groups, group_top, bias
                 group_top=group_top, renorm=bias)
 
 
+# more tokens than a wave each is spent on: lanes of a row, groups of every shape, ragged ends
+MANY = [(1, 2, 1, 1, 1, 2), (5, 1, 1, 1, 1, 2), (4, 4, 1, 1, 1, 2), (6, 3, 3, 2, 2, 0), (30, 5, 3, 2, 1, 0), (64, 8, 8, 3, 2, 2),
+        (96, 8, 8, 4, 2, 0), (128, 8, 4, 2, 1, 2), (131, 5, 1, 1, 1, 0), (160, 6, 8, 3, 2, 0), (252, 8, 7, 3, 2, 2),
+        (256, 8, 1, 1, 1, 2), (256, 8, 8, 4, 2, 0), (256, 8, 8, 7, 2, 2), (256, 1, 32, 1, 1, 0), (256, 16, 16, 5, 2, 2),
+        (240, 8, 20, 9, 2, 0), (255, 12, 5, 3, 2, 2), (384, 8, 12, 5, 2, 0), (512, 8, 16, 4, 2, 2), (510, 16, 1, 1, 1, 0),
+        (520, 8, 26, 13, 1, 2), (1024, 8, 32, 8, 2, 0), (1024, 16, 1, 1, 1, 2), (1023, 3, 3, 2, 2, 0), (1000, 8, 40, 11, 2, 2)]
+
+
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top,odd", MANY)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_many(E, k, groups, top_groups, group_top, odd, score, bias):
+    kind = "bf16" if odd else "f32"
+    check_route(1301 + odd, E, min(k, E), score, kind=kind, bias=bias, groups=groups, top_groups=top_groups,
+                group_top=group_top, renorm=bool(odd) != bias, scale=1.5, seed=odd)
+    check_route(1030, E, min(k, E), score, kind="f32" if odd else "bf16", special="masked", bias=bias, groups=groups,
+                top_groups=top_groups, group_top=group_top, renorm=bias)
+
+
+@pytest.mark.parametrize("special", ["ties", "saturated", "masked", "nan", "zeros"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_many_special(special, score, bias):
+    for E, k, groups, top_groups, group_top in ((256, 8, 8, 4, 2), (256, 8, 1, 1, 2), (256, 8, 8, 6, 1), (200, 9, 5, 3, 2)):
+        check_route(1100, E, k, score, special=special, bias=bias, groups=groups, top_groups=top_groups, group_top=group_top,
+                    renorm=not bias, scale=1.5)
+    check_route(1100, 256, 8, score, kind="bf16", special=special, bias=bias, groups=8, top_groups=4, renorm=bias)
+
+
+def test_large_and_odd_biases():
+    """Biases that swamp the scores, that are all equal, negative, infinite for more experts than are chosen."""
+    T, E, k = 1100, 256, 8
+    lg = make(T, E, 55)
+    l = np64(lg)
+    s = R.scores(l, "f32", "sigmoid")
+    rng = np.random.default_rng(8)
+    some = rng.random(E) < 0.1
+    for b in (np.full(E, 1e6), np.full(E, -3.0), rng.standard_normal(E) * 1e4, np.where(some, np.inf, 0.0),
+              np.where(some, -np.inf, 1e-9), np.where(some, np.nan, 0.0), -rng.random(E) * 1e30, np.zeros(E)):
+        b32 = b.astype(np.float32)
+        for groups, top, gt in ((1, 1, 2), (8, 4, 2), (8, 3, 1)):
+            sc = ops.Scoring("sigmoid", groups=groups, top_groups=top, group_top=gt)
+            ids, w = ops.route_scored(lg, k, sc, bias=torch.tensor(b32).to(DEV))
+            ref = R.choices(l, s, "f32", k, b32, groups, top, gt)
+            assert np.array_equal(npi(ids), ref), (b[:3], groups)
+            rw, _ = R.weights(l, s, "f32", ref, "sigmoid", True, 1.0)
+            close(w, rw, R.ROUND["f32"] * np.abs(rw) + R.TINY["f32"], "w")
+
+
 def test_bias_of_infinity_and_nan():
     T, E, k = 20, 64, 8
     lg = make(T, E, 5)
@@ -123,7 +174,7 @@ def test_bias_of_infinity_and_nan():
 
 def test_close_scores_are_ordered_as_rounded():
     """Logits a few ulps apart: scores that round to the same value tie by id, others do not."""
-    E, T, k = 256, 64, 8
+    E, T, k = 256, 1200, 8
     rng = np.random.default_rng(3)
     l = np.float32(1.0) + rng.integers(0, 40, size=(T, E)).astype(np.float32) * np.float32(2.0 ** -23)
     lg = torch.tensor(l).to(DEV)
@@ -134,8 +185,10 @@ def test_close_scores_are_ordered_as_rounded():
             for bias in (None, b):
                 ids, _ = ops.route_scored(lg, k, sc, bias=bias)
                 s = R.scores(l.astype(np.float64), "f32", score)
-                ref = R.choice(l.astype(np.float64), s, "f32", k, None if bias is None else npi(b), groups, top, 2)
+                ref = R.choices(l.astype(np.float64), s, "f32", k, None if bias is None else npi(b), groups, top, 2)
                 assert np.array_equal(npi(ids), ref), (score, groups, bias is None)
+                ids, _ = ops.route_scored(lg[:64].contiguous(), k, sc, bias=bias)
+                assert np.array_equal(npi(ids), ref[:64]), (score, groups, bias is None)
 
 
 def test_many_tokens():

@@ -100,3 +100,22 @@ def test_python_refusals():
         ops.record_args(torch.zeros(2, 3, 4, dtype=torch.int32), 0, 0, 2, torch.device("cpu"))
     with pytest.raises(ValueError):
         ops.record_args(torch.zeros(2, 2, 4, dtype=torch.int64), 0, 0, 2, torch.device("cpu"))
+
+
+def test_the_references_agree():
+    """The reference for many tokens at once against the one that goes token by token."""
+    import numpy as np
+
+    import scores_ref as R
+    rng = np.random.default_rng(5)
+    for E, k, groups, top, gt in ((16, 4, 4, 2, 2), (24, 6, 3, 2, 1), (9, 9, 1, 1, 2), (32, 3, 16, 3, 2)):
+        l = np.round(rng.standard_normal((60, E)) * 2) / 2
+        l[rng.random((60, E)) < 0.3] = -np.inf
+        l[rng.random((60, E)) < 0.1] = R.LOWEST["f32"]
+        l[rng.random((60, E)) < 0.05] = np.nan
+        l[::7] = -np.inf
+        for score in ("sigmoid", "softmax"):
+            s = R.scores(l, "f32", score)
+            for bias in (None, np.round(rng.standard_normal(E), 1)):
+                a = (l, s, "f32", k, bias, groups, top, gt)
+                assert np.array_equal(R.choice(*a), R.choices(*a))
