@@ -6,7 +6,8 @@
  * block-scaled FP8 e4m3 quantisation, an MFMA FP8 grouped GEMM with a fused
  * SwiGLU epilogue, the weighted combine, and the training backward.  Around the
  * routed experts: bf16 products with fused epilogues (the router's projection, a
- * shared expert) with their gradients, and activations kept in 8 bits.
+ * shared expert) with their gradients, activations kept in 8 bits, routing by scores
+ * and the norms in front of and behind the layer.
  *
  * Sources (cited by page and section):
  *   [R3]  "RL at 1T scale: a deep dive into prime-rl performance", section
