@@ -89,13 +89,17 @@ __device__ __forceinline__ void store1(void* p, int64_t i, bool f32, float v) {
 // Gate and its slope, for the gradients. The exponential of -|x| serves both, without
 // cancellation: e / (1 + e)^2 is the slope on either side. exp2 and reciprocal of the
 // hardware, the product's rounding and a Newton step made good: 4 roundings' worth off,
-// half the instructions of expf and a division.
+// half the instructions of expf and a division. Beyond |x| = 128 e is 0, as it is from 88 on
+// (exp2 gives no values below 2^-126); stopped there, the product's rounding stays a number
+// for infinite x too. A NaN goes through.
 struct Gate {
     float value, slope;
 };
 __device__ __forceinline__ Gate gate_of(float x, int act) {
     if (act != MOE_ACT_SIGMOID) return {x, 1.0f};
-    const float n = -fabsf(x), t = n * 1.4426950408889634f;
+    float n = -fabsf(x);
+    n = n < -128.f ? -128.f : n;
+    const float t = n * 1.4426950408889634f;
     const float lost = fmaf(n, 1.4426950408889634f, -t) + n * 1.9259629911266175e-8f;  // of the product, and of log2 e
     const float e0 = __builtin_amdgcn_exp2f(t), e = fmaf(e0, lost * 0.6931471805599453f, e0);
     const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d), q = fmaf(fmaf(-d, r, 1.0f), r, r);

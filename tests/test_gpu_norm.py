@@ -84,9 +84,9 @@ def test_norm_special_rows():
 
 
 def check_join(T, d, r_type="bf16", w_type="bf16", post=True, pre=True, gate="none", gate_type="bf16", act="none",
-               r_scale=1.0, y_scale=1.0, pad=0, with_d_out=True, seed=0):
+               r_scale=1.0, y_scale=1.0, pad=0, with_d_out=True, seed=0, far=False):
     say(f"join T={T} d={d} r={r_type} w={w_type} post={post} pre={pre} gate={gate} {gate_type} {act} scales={r_scale},{y_scale} "
-        f"pad={pad} d_out={with_d_out}")
+        f"pad={pad} d_out={with_d_out} far={far}")
     rt, wt, gt = T_OF[r_type], T_OF[w_type], T_OF[gate_type]
     y = normal((T, d), 11 + seed, 0.7, pad=pad, rows=True)
     r = normal((T, d), 12 + seed, 2.0, rt, pad=pad, rows=True)
@@ -94,6 +94,8 @@ def check_join(T, d, r_type="bf16", w_type="bf16", post=True, pre=True, gate="no
     wn = normal((d,), 14, 0.3, wt, 1.0) if pre else None
     shape = dict(none=None, channel=(d,), token=(T,), full=(T, d))[gate]
     gv = None if shape is None else normal(shape, 15, 0.8, gt, 0.2).contiguous()
+    if far:
+        gv.view(-1)[:len(FAR)] = torch.tensor(FAR, device=DEV).to(gt)[:gv.numel()]
     p = JoinPlan(T, d, r_dtype=rt, w_dtype=wt, post=post, pre=pre, gate=gate, gate_dtype=gt, gate_act=act, r_scale=r_scale,
                  y_scale=y_scale, eps=EPS, train=True, device=DEV)
     r_out, h = p.forward(y, r, w_post=wp, gate=gv, w_pre=wn)
@@ -106,7 +108,9 @@ def check_join(T, d, r_type="bf16", w_type="bf16", post=True, pre=True, gate="no
     else:
         n, en, rho_y = Y, 0 * Y, torch.ones(1, 1, dtype=torch.float64)
     g, slope = R.gate_of(gv, gate, act, T, d)
-    eg = 8 * u * g.abs()               # exp, a sum and a division; 0 without an activation
+    # exp, a sum and a division; 0 without an activation. Below the normal range a gate and its slope may be 0
+    tiny = 2.0 ** -126 if far else 0.0
+    eg = 8 * u * g.abs() + tiny
     z, ez = g * n, g.abs() * en + eg * (n.abs() + en)
     ref = rs * X + ys * z
     R.close(r_out, ref, abs(ys) * ez + 3 * u * ((rs * X).abs() + (ys * z).abs()), "r_out")
@@ -131,7 +135,7 @@ def check_join(T, d, r_type="bf16", w_type="bf16", post=True, pre=True, gate="no
     R.close(got["dr"], rs * D, abs(rs) * eD + u * (rs * D).abs(), "dr")
     dz, edz = ys * D, abs(ys) * eD + u * (ys * D).abs()
     if gate != "none":
-        t, et = dz * n * slope, (edz * (n.abs() + en) + dz.abs() * en + 20 * u * (dz * n).abs()) * slope.abs()
+        t, et = dz * n * slope, (edz * (n.abs() + en) + dz.abs() * en + 20 * u * (dz * n).abs()) * slope.abs() + tiny * (dz * n).abs()
         if gate == "channel":
             t, et = R.column(t, et, T)
         elif gate == "token":
@@ -164,6 +168,21 @@ def test_join_forms(gate, act, post, pre, types):
 def test_join_sizes(T, d, gate, r_type):
     check_join(T, d, r_type, "bf16" if d % 3 else "f32", gate=gate, act="sigmoid", gate_type="f32" if d % 5 else "bf16",
                r_scale=0.5, y_scale=1.5, pad=16 * (T % 2), with_d_out=T % 4 != 1)
+
+
+# gates far out, where the exponential leaves its range on either side
+FAR = [float("inf"), -float("inf"), 3e38, -3e38, 1e30, -1e30, 129.0, -129.0, 104.0, -104.0, 90.0, -90.0, 87.0, -87.0, 50.0, -50.0,
+       0.0, -0.0]
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("T,d", [(45, 264), (40, 5000), (21, 8200)])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+def test_join_far_gates(gate, T, d, types):
+    """Sigmoid gates up to infinity: 0 or 1, without a slope."""
+    p, (_, _, _, gv, *_) = check_join(T, d, types[0], gate=gate, gate_type=types[1], act="sigmoid", far=True)
+    assert bool(p.dgate.isfinite().all()) and bool((p.dgate.view(-1)[:8] == 0).all())
+    assert all(bool(t.isfinite().all()) for t in (p.r_out, p.h, p.dr, p.dy, p.dw_post, p.dw_pre))
 
 
 def test_many_rows():
