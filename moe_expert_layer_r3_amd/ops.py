@@ -546,9 +546,9 @@ class Scoring:
         return self.groups, self.top_groups, self.group_top, self.renorm, self.scale
 
 
-def _logits_type(t, what="logits"):
+def _logits_type(t):
     if t.dtype not in SRC_TYPES:
-        raise TypeError(f"{what}: bf16 or fp32, got {t.dtype}")
+        raise TypeError(f"logits: bf16 or fp32, got {t.dtype}")
     return SRC_TYPES[t.dtype]
 
 
