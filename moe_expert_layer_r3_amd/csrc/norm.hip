@@ -142,7 +142,9 @@ __device__ __forceinline__ void gate8(float (&g)[8], const void* gate, int kind,
     }
 }
 
-// One workgroup per row, the row read again for each sum.
+// Rows of more than 16384 columns: one workgroup per row, the row read again for each
+// sum, from the caches. 4096 rows of 16400, gate per channel: 191 us, of 107 at the rate of
+// a large copy; what a thread does in turn between barriers bounds it.
 template <bool RF32>
 __global__ __launch_bounds__(NT) void join_kernel(JoinArgs a) {
     __shared__ float lds[2][NT / 64];
@@ -200,8 +202,8 @@ __global__ __launch_bounds__(NT) void join_kernel(JoinArgs a) {
     }
 }
 
-// One workgroup per row, the row read again for each sum; what is summed over the
-// tokens goes into the workgroup's own row of the partial sums.
+// Their gradients; what is summed over the tokens goes into the workgroup's own row of
+// the partial sums, in memory: 542 us where the copy rate allows 161.
 template <bool RF32>
 __global__ __launch_bounds__(NT) void join_backward_kernel(JoinGradArgs a) {
     __shared__ float lds[2][NT / 64];
@@ -316,7 +318,14 @@ __global__ __launch_bounds__(NT) void join_backward_kernel(JoinGradArgs a) {
 // every row, so that weights and column sums stay in its registers. Rows of up to
 // 512 columns: teams of L lanes (a power of two) of a wave, no barriers; longer
 // ones: a workgroup of up to 1024 threads, one barrier per sum. The next row's loads
-// go out before this row's sums are waited for.
+// go out before this row's sums are waited for. (512 columns in a workgroup of one wave
+// instead: gradients of 16384 rows 32.1 against 32.8 us, of 1237 rows of 320 12.4 against 11.7;
+// 256 columns, 16384 rows: forward 14.4 against 10.9, gradients 27.8 against 22.3.)
+//
+// Bound by memory where there are many rows: 16384 rows of 7168, y, r and both outputs in
+// bf16, take 190 us (4.9 TB/s; a large copy reaches 5.0), a norm alone of 4096 rows 19 us.
+// Few rows are bound by the latency of a row's chain of load, sum, barrier, store: 64 rows
+// of 8192 6.4 us.
 
 // Sum over aligned groups of L lanes (a power of two up to 64), in every lane.
 template <int CTRL>
@@ -379,6 +388,13 @@ struct Chunk {
     __device__ __forceinline__ void pin() {
 #pragma unroll
         for (int k = 0; k < (F32 ? 2 : 1); ++k) asm volatile("" : "+v"(q[k]));
+    }
+    __device__ __forceinline__ void put(const float (&v)[8]) {  // values that are of the type
+#pragma unroll
+        for (int j = 0; j < (F32 ? 8 : 4); ++j) {
+            if constexpr (F32) q[j >> 2][j & 3] = __float_as_uint(v[j]);
+            else q[0][j] = cvt_bf16x2(v[2 * j], v[2 * j + 1]);
+        }
     }
     __device__ __forceinline__ float operator[](int j) const {
         if constexpr (F32) return __uint_as_float(q[j >> 2][j & 3]);
@@ -495,6 +511,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a
 // them, is put in at the end).
 // MOST: threads of a workgroup at most. With a gate per element the next row's chunks fit
 // the registers up to 512.
+// 16384 rows of 7168, bf16: 263 us of reading and writing six operands (5.4 TB/s), memory-bound;
+// four sums in four rounds would add three barriers to every row.
 template <bool RF32, bool Y, int FULL, bool WAVE, int MOST>
 __global__ __launch_bounds__(MOST) void join_rows_backward_kernel(JoinGradArgs a, int L) {
     constexpr bool AHEAD = FULL == FULL_NONE || MOST <= 512;
@@ -623,6 +641,251 @@ __global__ __launch_bounds__(MOST) void join_rows_backward_kernel(JoinGradArgs a
     if (Y && a.part_y) store8(a.part_y, part * d + tm.c, true, acc_y);
 }
 
+// Rows of 8200 to 16384 columns: a workgroup of 1024 threads, two chunks to a thread,
+// 8192 columns apart. What else would need registers lies in LDS, a thread's own values in
+// places of its own (no barriers): a channel's gate; for the gradients y's weights and one
+// of the column sums. The other weights come from the caches for each row. 4096 rows of
+// 16384, gate per channel: forward 115 us, gradients 175 (copy rate 107 and 161); 8200 columns
+// 65 and 97, by the re-reading kernels 80 and 257.
+constexpr int LONG = 2, LONG_STEP = 8192;
+// a thread's own eight values in LDS
+typedef f4 Own8[2][1024];
+__device__ __forceinline__ void put_own(Own8& p, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p[i][threadIdx.x] = f4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+}
+__device__ __forceinline__ void get_own(float (&v)[8], const Own8& p) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[j >> 2][threadIdx.x][j & 3];
+}
+template <bool RF32, bool Y, int FULL>
+__global__ __launch_bounds__(1024) void join_long_kernel(JoinArgs a) {
+    __shared__ float lds[2][16][4];
+    int slot = 0;
+    const int64_t d = a.d, c0 = (int64_t)threadIdx.x * 8;
+    __shared__ Own8 channel[Y && FULL == FULL_NONE ? LONG : 1];  // a channel's gate
+    if (Y && FULL == FULL_NONE && a.gate_kind != MOE_GATE_TOKEN) {
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            if (c >= d) continue;
+            float v[8];
+            gate8(v, a.gate, a.gate_kind, a.gate_f32, 0, c, d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = gate_value(v[j], a.gate_act);
+            put_own(channel[k], v);
+        }
+    }
+    Chunk<false> y[LONG], y1[LONG];
+    Chunk<RF32> r[LONG], r1[LONG];
+    Chunk<FULL == FULL_F32> g[LONG], g1[LONG];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            if (c >= d) continue;
+            if constexpr (Y) y1[k].load(a.y, t * a.ldy + c);
+            r1[k].load(a.r, t * a.ldr + c);
+            if constexpr (FULL != FULL_NONE) g1[k].load(a.gate, t * d + c);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < LONG; ++k) y1[k].zero(), r1[k].zero(), g1[k].zero();
+    if (blockIdx.x < a.T) fetch(blockIdx.x);
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) y[k] = y1[k], r[k] = r1[k], g[k] = g1[k];
+        if (t + gridDim.x < a.T) fetch(t + gridDim.x);
+        if constexpr (Y) {
+            float rho_y = 1.0f;
+            if (a.w_post) {
+                float s[1] = {0.f};
+#pragma unroll
+                for (int k = 0; k < LONG; ++k)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s[0] += y[k][j] * y[k][j];
+                team_sum<false>(s, 64, lds, slot);
+                rho_y = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+                if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rho_y;
+            }
+            float gt = 1.0f;
+            if (a.gate_kind == MOE_GATE_TOKEN) gt = gate_value(load1(a.gate, t, a.gate_f32), a.gate_act);
+#pragma unroll
+            for (int k = 0; k < LONG; ++k) {
+                const int64_t c = c0 + k * LONG_STEP;
+                if (c >= d) continue;
+                float w[8], f[8], rv[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+                if (a.w_post) load8(w, a.w_post, c, a.w_f32);
+                if (FULL == FULL_NONE && a.gate_kind != MOE_GATE_TOKEN) get_own(f, channel[k]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = FULL != FULL_NONE ? gate_value(g[k][j], a.gate_act) : gt;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    rv[j] = stored(joined(r[k][j], y[k][j], rho_y, w[j], f[j], a.r_scale, a.y_scale), RF32);
+                store8(a.r_out, t * d + c, RF32, rv);
+                r[k].put(rv);
+            }
+        }
+        if (!a.w_pre) continue;
+        float s[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < LONG; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[0] += r[k][j] * r[k][j];
+        team_sum<false>(s, 64, lds, slot);
+        const float rho = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+        if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rho;
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            if (c >= d) continue;
+            float w[8];
+            load8(w, a.w_pre, c, a.w_f32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = r[k][j] * rho * w[j];
+            store8(a.h, t * d + c, false, w);
+        }
+    }
+}
+
+// Their gradients, with the sums of join_rows_backward_kernel.
+template <bool RF32, bool Y, int FULL>
+__global__ __launch_bounds__(1024) void join_long_backward_kernel(JoinGradArgs a) {
+    __shared__ float lds[2][16][4];
+    int slot = 0;
+    const int64_t d = a.d, c0 = (int64_t)threadIdx.x * 8;
+    // a thread's column sums: dh rh, and D g yh; of y: the norm's weights, a channel's gate
+    float acc_n[LONG][8];
+    __shared__ Own8 acc_y[Y ? LONG : 1], of_y[Y ? LONG : 1];
+#pragma unroll
+    for (int k = 0; k < LONG; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc_n[k][j] = 0.f;
+        if constexpr (Y) {
+            const int64_t c = c0 + k * LONG_STEP;
+            put_own(acc_y[k], acc_n[k]);
+            if (c >= d) continue;
+            float w[8], v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = v[j] = 1.0f;
+            if (a.w_post) load8(w, a.w_post, c, a.w_f32);
+            if (FULL == FULL_NONE && a.gate_kind == MOE_GATE_CHANNEL) load8(v, a.gate, c, a.gate_f32);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] *= a.gate_kind == MOE_GATE_CHANNEL ? gate_of(v[j], a.gate_act).value : 1.0f;
+            put_own(of_y[k], w);
+        }
+    }
+    Chunk<false> y[LONG], h[LONG];
+    Chunk<RF32> r[LONG], o[LONG];
+    Chunk<FULL == FULL_F32> g[LONG];
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            y[k].zero(), h[k].zero(), r[k].zero(), o[k].zero(), g[k].zero();
+            if (c >= d) continue;
+            if (a.w_pre) {
+                h[k].load(a.dh, t * d + c);
+                r[k].load(a.r_out, t * a.ldr + c);
+            }
+            if (a.d_out) o[k].load(a.d_out, t * d + c);
+            if constexpr (Y) y[k].load(a.y, t * a.ldy + c);
+            if constexpr (FULL != FULL_NONE) g[k].load(a.gate, t * d + c);
+        }
+        const float rho = a.w_pre ? a.rstd_pre[t] : 0.f;
+        const float rho_y = Y && a.w_post ? a.rstd_post[t] : 1.f;
+        Gate gt = {1.f, 0.f};
+        if (Y && a.gate_kind == MOE_GATE_TOKEN) gt = gate_of(load1(a.gate, t, a.gate_f32), a.gate_act);
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            if (c >= d) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            float wn[8], wz[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wn[j] = 0.f;
+            if (a.w_pre) load8(wn, a.w_pre, c, a.w_f32);
+            if constexpr (Y) get_own(wz, of_y[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float aj = h[k][j] * wn[j], rh = r[k][j] * rho;
+                s[0] += aj * rh;
+                if constexpr (Y) {
+                    float z = y[k][j] * rho_y * wz[j];
+                    if constexpr (FULL != FULL_NONE) z *= gate_of(g[k][j], a.gate_act).value;
+                    s[1] += o[k][j] * z;
+                    s[2] += aj * z;
+                    s[3] += rh * z;
+                }
+                two_at_a_time(j);
+            }
+        }
+        team_sum<false>(s, 64, lds, slot);
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) y[k].pin(), h[k].pin(), r[k].pin(), o[k].pin(), g[k].pin();
+        const float mean = s[0] / (float)d;
+        float sn = 0.f;
+        if constexpr (Y) {
+            const float sum = a.y_scale * (s[1] + rho * (s[2] - mean * s[3]));
+            if (a.gate_kind == MOE_GATE_TOKEN && a.dgate && threadIdx.x == 0) store1(a.dgate, t, a.gate_f32, sum * gt.slope);
+            sn = sum * gt.value / (float)d;
+        }
+#pragma unroll
+        for (int k = 0; k < LONG; ++k) {
+            const int64_t c = c0 + k * LONG_STEP;
+            if (c >= d) continue;
+            __builtin_amdgcn_sched_barrier(0);
+            float wn[8], wz[8], dr[8], dy[8], dg[8], ey[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) wn[j] = 0.f;
+            if (a.w_pre) load8(wn, a.w_pre, c, a.w_f32);
+            if constexpr (Y) get_own(wz, of_y[k]), get_own(ey, acc_y[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float rh = r[k][j] * rho, D = o[k][j] + rho * (h[k][j] * wn[j] - rh * mean);
+                acc_n[k][j] += h[k][j] * rh;
+                dr[j] = a.r_scale * D;
+                if constexpr (Y) {
+                    const float yh = y[k][j] * rho_y, dz = a.y_scale * D;
+                    float q = dz * gt.value;
+                    if constexpr (FULL != FULL_NONE) {
+                        const Gate f = gate_of(g[k][j], a.gate_act);
+                        q *= f.value;
+                        dg[j] = dz * (yh * wz[j]) * f.slope;
+                    }
+                    ey[j] += q * yh;
+                    dy[j] = a.w_post ? rho_y * (q * wz[j] - yh * sn) : q * wz[j];
+                }
+                two_at_a_time(j);
+            }
+            if constexpr (Y) put_own(acc_y[k], ey);
+            if (a.dr) store8(a.dr, t * d + c, RF32, dr);
+            if constexpr (Y) {
+                if (a.dy) store8(a.dy, t * d + c, false, dy);
+                if constexpr (FULL != FULL_NONE)
+                    if (a.dgate) store8(a.dgate, t * d + c, FULL == FULL_F32, dg);
+            }
+        }
+    }
+    const int64_t part = blockIdx.x;
+#pragma unroll
+    for (int k = 0; k < LONG; ++k) {
+        const int64_t c = c0 + k * LONG_STEP;
+        if (c >= d) continue;
+        if (a.part_pre) store8(a.part_pre, part * d + c, true, acc_n[k]);
+        if constexpr (Y) {
+            float v[8];
+            get_own(v, acc_y[k]);
+            if (a.part_y) store8(a.part_y, part * d + c, true, v);
+        }
+    }
+}
+
 // The columns' sums over the partial rows, in a fixed order; then dw_pre, or dw_post and
 // a channel's dgate, which share one sum q: dw_post = g q, dgate = w_post slope(gate) q.
 // COLS columns to a workgroup of 1024 threads, the others over the rows: 64, or 16
@@ -700,13 +963,14 @@ int check_gate(const char* what, int32_t kind, int32_t type, int32_t act, const 
 }
 
 // How a launch takes rows of d columns: in registers up to 8192 (a chunk of eight to
-// each of up to 1024 threads), read again for each sum beyond.
-constexpr int64_t MAX_ROW = 8192;
+// each of up to 1024 threads) and 16384 (two chunks), read again for each sum beyond.
+// (4096 rows of 8192: forward 52 us in registers, 72 read again; gradients 88 and 227.)
+constexpr int64_t MAX_ROW = 8192, MAX_LONG = LONG * LONG_STEP;
 struct Shape {
     int L, threads, per;  // lanes of a team in a wave (0: a workgroup to a row); rows of a workgroup at a time
 };
 Shape shape_of(int64_t d) {
-    if (d > MAX_ROW) return {0, NT, 1};
+    if (d > MAX_ROW) return {0, d > MAX_LONG ? NT : 1024, 1};
     const int chunks = (int)(d / 8);
     if (chunks > 64) return {0, (chunks + 63) / 64 * 64, 1};
     int L = 1;
@@ -715,13 +979,14 @@ Shape shape_of(int64_t d) {
 }
 // workgroups of a backward launch: enough to fill the compute units, but four rows at
 // least to each where there are more rows than units, for the partial sums' sake
+// (2048 x 2048: 21.2 us, one row at least 22.8, sixteen 22.5; a norm's 12.4, 16.3, 13.5)
 int64_t backward_blocks(int64_t T, int64_t d) {
     const Shape s = shape_of(d);
     const int64_t cus = num_cus(), units = (T + s.per - 1) / s.per;
     int64_t n = cus * (1024 / s.threads);
     const int64_t most = units / 4 > cus ? units / 4 : cus;
     n = n < most ? n : most;
-    if (d > MAX_ROW) n = n < (1 << 27) / d ? n : (1 << 27) / d;
+    if (d > MAX_LONG) n = n < (1 << 27) / d ? n : (1 << 27) / d;
     return units < n ? units : n;
 }
 int64_t partial_rows(int64_t T, int64_t d) { return backward_blocks(T, d) * (shape_of(d).L ? 4 : 1); }
@@ -741,12 +1006,13 @@ void launch_join(const JoinArgs& a, hipStream_t stream) {
     const Shape s = shape_of(a.d);
     const int64_t units = (a.T + s.per - 1) / s.per, most = (int64_t)num_cus() * (2048 / s.threads);
     const dim3 grid((unsigned)(units < most ? units : most)), block(s.threads);
-    if (a.d > MAX_ROW) {
+    if (a.d > MAX_LONG) {
         join_kernel<RF32><<<grid, block, 0, stream>>>(a);
         return;
     }
     with_gate(a.y != nullptr, a.gate_kind, a.gate_f32, [&](auto y, auto full) {
-        if (s.L) join_rows_kernel<RF32, y.value, full.value, true><<<grid, block, 0, stream>>>(a, s.L);
+        if (a.d > MAX_ROW) join_long_kernel<RF32, y.value, full.value><<<grid, block, 0, stream>>>(a);
+        else if (s.L) join_rows_kernel<RF32, y.value, full.value, true><<<grid, block, 0, stream>>>(a, s.L);
         else join_rows_kernel<RF32, y.value, full.value, false><<<grid, block, 0, stream>>>(a, s.L);
     });
 }
@@ -754,11 +1020,15 @@ template <bool RF32>
 void launch_join_backward(const JoinGradArgs& a, hipStream_t stream) {
     const Shape s = shape_of(a.d);
     const dim3 grid((unsigned)backward_blocks(a.T, a.d)), block(s.threads);
-    if (a.d > MAX_ROW) {
+    if (a.d > MAX_LONG) {
         join_backward_kernel<RF32><<<grid, block, 0, stream>>>(a);
         return;
     }
     with_gate(a.y != nullptr, a.gate_kind, a.gate_f32, [&](auto y, auto full) {
+        if (a.d > MAX_ROW) {
+            join_long_backward_kernel<RF32, y.value, full.value><<<grid, block, 0, stream>>>(a);
+            return;
+        }
         if (s.L) {
             join_rows_backward_kernel<RF32, y.value, full.value, true, 256><<<grid, block, 0, stream>>>(a, s.L);
             return;

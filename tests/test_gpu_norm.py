@@ -161,6 +161,7 @@ def check_join(T, d, r_type="bf16", w_type="bf16", post=True, pre=True, gate="no
 def test_join_forms(gate, act, post, pre, types):
     check_join(45, 264, *types[:2], post, pre, gate, types[2], act, 0.75, 0.5, pad=8)
     check_join(6, 1544, *types[:2], post, pre, gate, types[2], act, 1.0, -2.0)
+    check_join(5, 10008, *types[:2], post, pre, gate, types[2], act, 1.0, 0.5, pad=16)
 
 
 @pytest.mark.parametrize("T,d", NORM_SIZES)
@@ -176,7 +177,7 @@ FAR = [float("inf"), -float("inf"), 3e38, -3e38, 1e30, -1e30, 129.0, -129.0, 104
 
 
 @pytest.mark.parametrize("gate", ["channel", "token", "full"])
-@pytest.mark.parametrize("T,d", [(45, 264), (40, 5000), (21, 8200)])
+@pytest.mark.parametrize("T,d", [(45, 264), (40, 5000), (21, 8200), (18, 16400)])
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
 def test_join_far_gates(gate, T, d, types):
     """Sigmoid gates up to infinity: 0 or 1, without a slope."""
@@ -187,7 +188,7 @@ def test_join_far_gates(gate, T, d, types):
 
 def test_many_rows():
     """More rows than workgroups: every partial sum, the tails, and unequal shares of rows."""
-    for T, d in ((4099, 64), (1500, 1032), (1027, 7168)):
+    for T, d in ((4099, 64), (1500, 1032), (1027, 7168), (600, 12296)):
         check_join(T, d, gate="channel", act="sigmoid", y_scale=0.5)
         check_norm(T, d, "f32", "f32", add=True)
 
