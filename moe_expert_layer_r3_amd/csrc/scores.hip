@@ -208,7 +208,8 @@ __device__ __forceinline__ double wave_kmax(double v) {
 // One row by a whole wave, as it is defined: scores in 64 bits, rounded. Lane l holds
 // experts l, l + 64, ...; k rounds of a wave-wide maximum over the keys of the groups
 // that stay, as doubles (route_dkey). lds: E floats of this wave. Rare where the kernel below calls it, and a
-// function of its own so that its registers are not the caller's.
+// function of its own so that its registers are not the caller's. Bound by its chain: k
+// rounds of a maximum over 64 lanes, 64-bit exponentials in front: 5.3 us for one row of 256.
 typedef const __attribute__((address_space(4))) ScoreArgs* KernelArgs;
 typedef __attribute__((address_space(3))) float* LdsFloats;
 __device__ __forceinline__ uint64_t uniform(uint64_t v) {
@@ -421,6 +422,11 @@ __device__ __forceinline__ float max_of_numbers(float a, float b) {
 // zero. VL of a lane's values come to that: all, or, where the groups that stay hold at
 // most half the experts, those of them alone. A lane passes on its 8 largest; one
 // whose last passed key comes near the last pick makes the row uncertain.
+//
+// Bound by vector instructions (80% of the cycles), not by memory: 131072 rows of 256, sigmoid,
+// bias, 4 of 8 groups, take 45 us, of which reading 128 MiB needs 27; one wave per row and
+// 64-bit scores took 228. Lanes of a row: as few as hold its groups and logits, since every
+// step of the merge is done by all of them.
 template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int VL, int KT>
 __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
@@ -785,7 +791,8 @@ __global__ __launch_bounds__(1024) void score_load_kernel(const int32_t* ids, in
 
 // ---------------------------------------------------------------- replay
 
-// 16 lanes per token where the chosen logits alone decide its weights.
+// 16 lanes per token where the chosen logits alone decide its weights: k of a row's logits
+// are read, scattered. Bound by 64-bit exponentials and latency: 16384 tokens, k = 8: 5.1 us.
 template <bool F32, bool SIGMOID, bool RENORM>
 __global__ __launch_bounds__(256) void score_replay_kernel(ScoreArgs a, int32_t* status) {
     const int lane = threadIdx.x & 15, E = a.E, k = a.k;
@@ -850,7 +857,8 @@ struct Row16 {
     }
 };
 
-// 16 lanes per token where the whole row does (softmax without renorm).
+// 16 lanes per token where the whole row does (softmax without renorm). Bound by reading
+// the rows: 16384 tokens of 256 experts (16 MiB) 7.0 us.
 template <bool F32, int VPL>
 __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int32_t* status) {
     const int lane = threadIdx.x & 15, E = a.E, k = a.k;
@@ -897,7 +905,8 @@ struct ScoreGradArgs {
 
 // 16 lanes per token, four tokens to a wave: lane j < k has slot j; the slots' values go
 // into the rows' place in LDS, from which whole rows are written. Bound by writing
-// [T, E] (and reading it, where every logit has a gradient).
+// [T, E] (and reading it, where every logit has a gradient): 16384 tokens of 256 experts, fp32,
+// 7.2 us, and 8.9 with the whole row's gradient.
 template <bool F32, bool SIGMOID, bool RENORM, bool PARTS, int VPL>
 __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
     constexpr bool WHOLE = !SIGMOID && !RENORM;
@@ -1007,6 +1016,8 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
 
 // ---------------------------------------------------------------- bias
 
+// bias + step sign(mean - load), the mean as an exact comparison of integers:
+// total against load E. One workgroup, bound by a launch's latency (1.9 us).
 __global__ __launch_bounds__(1024) void balance_bias_kernel(int32_t* load, const float* bias, int E, float step, int clear,
                                                             float* out) {
     __shared__ int64_t part[16];
