@@ -299,7 +299,8 @@ __device__ __attribute__((noinline)) void choose_exactly(KernelArgs args, int64_
 
 __device__ __forceinline__ KernelArgs kernel_args() { return (KernelArgs)__builtin_amdgcn_kernarg_segment_ptr(); }
 
-// Every row exactly: more groups that count than 32 lanes hold, less than four experts, or few rows.
+// Every row exactly: more groups that count than 32 lanes hold, less than four experts, or few rows
+// of many picks or groups.
 template <bool F32, bool SIGMOID, int VPL>
 __global__ __launch_bounds__(256) void score_topk_exact_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
@@ -1122,22 +1123,29 @@ void launch_choice_of(ScoreArgs a, hipStream_t stream) {
     while ((1 << a.group_bits) < G) ++a.group_bits;
     // groups a multiple of 32 floats apart would read the same banks
     a.spread = S % 32 == 0;
-    // A whole wave to a row has the least to do in turn: one token of 256 experts 5.3 us against
-    // 5.9 (1024 tokens 6.0 against 6.5) with the rest of the chip idle, 4096 tokens 9.1 against 7.9;
-    // 64 and 512 experts are faster below (one token 3.5 against 3.5 us and 7.4 against 5.1).
-    if (G > 32 || E < 4 || (E > 128 && E <= 256 && a.T <= 1024)) {
+    // A whole wave to a row, and to all of it exactly, where that is no slower than 16 lanes or 32:
+    // up to 1024 rows of 129 to 256 experts that need 16 picks or more than 8 groups (1024 rows, k = 16:
+    // 6.0 us against 7.8, 32 groups 7.1 against 8.5; one row 5.4 against 4.6).
+    const bool few_lanes = G <= 8 && a.k <= 8;
+    // Up to 32 rows for each compute unit lanes are plenty, and twice as many to a row shorten what
+    // they do in turn (one row of 256 experts, no groups, 5.9 -> 4.0 us; 2048 rows 6.4 -> 4.5; 8192 7.3 -> 5.8;
+    // 512 experts 5.2 -> 4.0, 6.9 -> 4.7, 10.1 -> 8.6); more rows lose by it (32768: 14 -> 17 us, 31 -> 36).
+    const bool wide = a.T <= 32 * (int64_t)num_cus();
+    if (G > 32 || E < 4 || (E > 128 && E <= 256 && a.T <= 1024 && !few_lanes)) {
         a.lds_wave = E;
         with_vpl(E, [&](auto v) {
             score_topk_exact_kernel<F32, SIGMOID, v.value>
                 <<<row_blocks(a.T, 4), 256, (size_t)a.lds_wave * 4 * sizeof(float), stream>>>(a);
         });
-    } else if (G <= 8 && a.k <= 8 && E <= 256) {
+    } else if (few_lanes && E <= 256) {
         if (E <= 64) launch_topk<F32, SIGMOID, 8, 8, 8>(a, stream);
         else if (E <= 128) launch_topk<F32, SIGMOID, 8, 16, 8>(a, stream);
+        else if (wide) launch_topk<F32, SIGMOID, 16, 16, 8>(a, stream);
         else launch_topk<F32, SIGMOID, 8, 32, 8>(a, stream);
     } else if (G <= 16 && E <= 512) {
         if (E <= 128) launch_topk<F32, SIGMOID, 16, 8, 16>(a, stream);
         else if (E <= 256) launch_topk<F32, SIGMOID, 16, 16, 16>(a, stream);
+        else if (a.k <= 8 && wide) launch_topk<F32, SIGMOID, 32, 16, 8>(a, stream);
         else if (a.k <= 8) launch_topk<F32, SIGMOID, 16, 32, 8>(a, stream);
         else launch_topk<F32, SIGMOID, 16, 32, 16>(a, stream);
     } else {

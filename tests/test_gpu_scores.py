@@ -138,6 +138,34 @@ def test_route_many_special(special, score, bias):
     check_route(1100, 256, 8, score, kind="bf16", special=special, bias=bias, groups=8, top_groups=4, renorm=bias)
 
 
+# batches that fill the chip: fewer lanes to a row
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top,odd", [
+    (160, 6, 8, 3, 2, 0), (252, 8, 7, 3, 2, 2), (131, 5, 1, 1, 1, 0), (256, 8, 1, 1, 1, 2), (256, 8, 8, 4, 2, 0),
+    (256, 8, 8, 7, 2, 2), (384, 8, 12, 5, 2, 0), (384, 8, 1, 1, 1, 2), (512, 8, 16, 4, 2, 2), (510, 7, 1, 1, 1, 0)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_large_batch(E, k, groups, top_groups, group_top, odd, score, bias):
+    check_route(8197 + odd, E, k, score, kind="bf16" if odd else "f32", bias=bias, groups=groups, top_groups=top_groups,
+                group_top=group_top, renorm=bool(odd) != bias, scale=1.5, seed=odd)
+
+
+@pytest.mark.parametrize("special", ["ties", "saturated", "masked", "nan", "zeros"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+def test_special_large_batch(special, score, bias):
+    for E, groups, top_groups in ((256, 8, 4), (200, 1, 1), (512, 16, 4)):
+        check_route(8200, E, 8, score, special=special, bias=bias, groups=groups, top_groups=top_groups, renorm=not bias,
+                    scale=1.5)
+
+
+@pytest.mark.parametrize("T", [1, 48, 1024])
+@pytest.mark.parametrize("E,k,groups,top_groups", [(512, 8, 16, 4), (384, 8, 1, 1), (510, 7, 5, 2), (256, 16, 1, 1), (256, 8, 32, 9)])
+def test_few_rows(T, E, k, groups, top_groups):
+    for score in ("softmax", "sigmoid"):
+        check_route(T, E, k, score, bias=score == "sigmoid", groups=groups, top_groups=top_groups, special="masked")
+        check_route(T, E, k, score, kind="bf16", bias=score == "softmax", groups=groups, top_groups=top_groups, renorm=False)
+
+
 def test_large_and_odd_biases():
     """Biases that swamp the scores, that are all equal, negative, infinite for more experts than are chosen."""
     T, E, k = 1100, 256, 8
