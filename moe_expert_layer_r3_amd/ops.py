@@ -587,7 +587,7 @@ def replay_scored(rec, layer, s0, logits, scoring, status=None, out=None):
     T, E = logits.shape
     dev = _dev(logits)
     _dense(logits, (T, E), logits.dtype, "logits", dev)
-    k = rec.shape[1]
+    k = rec.shape[1] if rec.dim() == 3 else 0
     p, NL, S, layer, s0 = record_args(rec, layer, s0, k, dev)
     if status is not None:
         _dense(status, (1,), torch.int32, "status", dev)
@@ -609,7 +609,7 @@ def route_scored_backward(d_w, logits, ids, scoring, out=None):
     T, E = logits.shape
     dev = _dev(logits)
     _dense(logits, (T, E), logits.dtype, "logits", dev)
-    k = ids.shape[1]
+    k = ids.shape[1] if ids.dim() == 2 else 0
     _dense(ids, (T, k), torch.int32, "ids", dev)
     _dense(d_w, (T, k), torch.float32, "d_w", dev)
     out = torch.empty_like(logits) if out is None else _dense(out, (T, E), logits.dtype, "d_logits", dev)
@@ -625,7 +625,7 @@ def route_scored_backward_parts(gate_part, pair_row, rcap, d, logits, ids, scori
     T, E = logits.shape
     dev = _dev(logits)
     _dense(logits, (T, E), logits.dtype, "logits", dev)
-    k = ids.shape[1]
+    k = ids.shape[1] if ids.dim() == 2 else 0
     _dense(ids, (T, k), torch.int32, "ids", dev)
     _dense(pair_row, (T, k), torch.int32, "pair_row", dev)
     _dense(gate_part, (rcap, GATE_PARTS), torch.float32, "gate_part", dev)

@@ -347,3 +347,51 @@ def test_graph_and_streams():
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d", [264, 1032, 7168, 12296])
+def test_two_streams_at_once(d):
+    """Plans of their own on two streams, calls in flight on both: each gives what it gives alone."""
+    T = 900
+    y, r, d_out, dh = (normal((T, d), 20 + i) for i in range(4))
+    wp, wn, g = (normal((d,), 30 + i, 0.3, BF, 1.0) for i in range(3))
+    plans = [JoinPlan(T, d, gate="channel", gate_act=act, train=True, device=DEV) for act in ("none", "sigmoid")]
+
+    def step(p):
+        p.forward(y, r, w_post=wp, gate=g, w_pre=wn)
+        p.backward(d_out, dh, y, w_post=wp, gate=g, w_pre=wn)
+        return p.r_out, p.h, p.dr, p.dy, p.dw_post, p.dw_pre, p.dgate
+    want = [[t.clone() for t in step(p)] for p in plans]
+    sides = [torch.cuda.Stream() for _ in plans]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for p, s in zip(plans, sides):
+            with torch.cuda.stream(s):
+                step(p)
+    for s in sides:
+        s.synchronize()
+    for p, w in zip(plans, want):
+        for a, b in zip((p.r_out, p.h, p.dr, p.dy, p.dw_post, p.dw_pre, p.dgate), w):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,d", [(40, 264), (12, 5000), (5, 8200), (4, 16400)])
+@pytest.mark.parametrize("act", ["none", "sigmoid"])
+def test_nan_gate_stays_in_its_row(T, d, act):
+    """A gate of NaN makes its own row NaN, forward and back, and no other."""
+    y, r, d_out, dh, g = (normal((T, d), 40 + i) for i in range(5))
+    wp, wn = (normal((d,), 50 + i, 0.3, BF, 1.0) for i in range(2))
+    p = JoinPlan(T, d, gate="full", gate_act=act, train=True, device=DEV)
+
+    def step():
+        p.forward(y, r, w_post=wp, gate=g, w_pre=wn)
+        p.backward(d_out, dh, y, w_post=wp, gate=g, w_pre=wn)
+        return [t.clone() for t in (p.r_out, p.h, p.dr, p.dy, p.dgate)]
+    want = step()
+    g[2, 17] = float("nan")
+    got = step()
+    keep = torch.arange(T, device=DEV) != 2
+    for a, b in zip(got, want):
+        assert torch.equal(a[keep], b[keep])
+    assert bool(got[0][2, 17].isnan()) and all(bool(t[2].isnan().all()) for t in got[1:4])

@@ -392,3 +392,42 @@ def test_graph_and_streams():
         a = other.forward(lg, bias=bias)
     side.synchronize()
     assert torch.equal(a[0], plan.ids) and torch.equal(a[1], plan.w)
+
+
+def test_two_streams_at_once():
+    """Plans of their own on two streams, calls in flight on both: each gives what it gives alone."""
+    T, E, k = 9000, 256, 8
+    forms = (ops.Scoring("sigmoid", groups=8, top_groups=4, scale=2.5), ops.Scoring("softmax", renorm=False))
+    lg = [make(T, E, 61 + i) for i in range(2)]
+    rec = [torch.zeros((1, k, T), dtype=torch.int32, device=DEV) for _ in range(2)]
+    d_w = [torch.randn((T, k), device=DEV, generator=torch.Generator(DEV).manual_seed(i)) for i in range(2)]
+
+    def step(p, i):
+        p.forward(lg[i], capture=(rec[i], 0, 0))
+        p.backward(d_w[i], lg[i])
+        p.replay(rec[i], 0, 0, lg[i])
+        return p.ids, p.w, p.d_logits
+    plans = [RoutePlan(T, E, k, sc, train=True, device=DEV) for sc in forms]
+    want = [[t.clone() for t in step(p, i)] for i, p in enumerate(plans)]
+    sides = [torch.cuda.Stream() for _ in plans]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for i, (p, s) in enumerate(zip(plans, sides)):
+            with torch.cuda.stream(s):
+                got = step(p, i)
+    for s in sides:
+        s.synchronize()
+    for i, p in enumerate(plans):
+        for a, b in zip((p.ids, p.w, p.d_logits), want[i]):
+            assert torch.equal(a, b)
+
+
+def test_ranks_of_operands():
+    """Records and ids of another number of dimensions are refused."""
+    lg = make(8, 16, 3)
+    sc = ops.Scoring()
+    with pytest.raises(ValueError):
+        ops.replay_scored(torch.zeros(16, dtype=torch.int32, device=DEV), 0, 0, lg, sc)
+    with pytest.raises(ValueError):
+        ops.route_scored_backward(torch.zeros(8, device=DEV), lg, torch.zeros(8, dtype=torch.int32, device=DEV), sc)
