@@ -43,21 +43,23 @@ __device__ __forceinline__ bool is_masked(float l) {
 }
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// For weights and gradients, which are rounded to 32 bits: exp(x) from the Taylor
-// polynomial of degree 10 on [-ln 2 / 2, ln 2 / 2] (its remainder 2^-42), a reciprocal from the
-// hardware's and two Newton steps (2^-50): a third of the instructions of the exact ones.
+// For weights and gradients, which are rounded to 32 bits: exp(x) from a polynomial of
+// degree 10, 1 + r + r^2 g(r) with g interpolated at the Chebyshev nodes of
+// [-ln 2 / 2, ln 2 / 2] (off by 2^-49 of itself; Taylor's of that degree would be by 2^-41, which
+// shows where a gradient is a difference), a reciprocal from the hardware's and two Newton
+// steps (2^-50): a third of the instructions of the exact ones.
 __device__ __forceinline__ double exp_near(double x) {
     x = x > 1000.0 ? 1000.0 : x < -1000.0 ? -1000.0 : x;
     const double n = __builtin_rint(x * 1.4426950408889634);
     const double r = __builtin_fma(-n, 2.319046813846300e-17, __builtin_fma(-n, 0.6931471805599453, x));
-    double p = 1.0 / 3628800;
-    p = __builtin_fma(p, r, 1.0 / 362880);
-    p = __builtin_fma(p, r, 1.0 / 40320);
-    p = __builtin_fma(p, r, 1.0 / 5040);
-    p = __builtin_fma(p, r, 1.0 / 720);
-    p = __builtin_fma(p, r, 1.0 / 120);
-    p = __builtin_fma(p, r, 1.0 / 24);
-    p = __builtin_fma(p, r, 1.0 / 6);
+    double p = 2.761379556582631e-07;
+    p = __builtin_fma(p, r, 2.7625102018960324e-06);
+    p = __builtin_fma(p, r, 2.4801536409043718e-05);
+    p = __builtin_fma(p, r, 0.0001984120875696787);
+    p = __builtin_fma(p, r, 0.0013888888905871355);
+    p = __builtin_fma(p, r, 0.008333333353717168);
+    p = __builtin_fma(p, r, 0.041666666666651364);
+    p = __builtin_fma(p, r, 0.16666666666648303);
     p = __builtin_fma(p, r, 0.5);
     p = __builtin_fma(p, r, 1.0);
     p = __builtin_fma(p, r, 1.0);

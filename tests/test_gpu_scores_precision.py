@@ -1,0 +1,38 @@
+"""The 64 bits of scored routing's weights and gradients on the GPU, where fewer would
+show: bounds of their own, next to those of scores_ref.
+
+u = 2^-24. What is rounded once from 64 bits is off by u of itself (2^-8 in bf16,
+and u for the way through fp32), or half the smallest step. In front of that
+rounding stand some 20 operations of 2^-53 each, an exponential good to 2^-49 and a
+reciprocal good to 2^-50: 2^-46 of the terms that a difference is taken of."""
+
+import numpy as np
+import pytest
+import torch
+
+import scores_ref as R
+from gpu_util import DEV, np64, say
+from moe_expert_layer_r3_amd import ops
+from test_gpu_scores import close
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_balanced_gradients(score):
+    """d_w of the last pick next to the mean of all, so that its gradient is some 2^-24
+    of the terms it is a difference of."""
+    T, E, k = 8192, 32, 3
+    say(f"balanced gradients {score}")
+    rng = np.random.default_rng(41)
+    lg = torch.tensor(rng.standard_normal((T, E)) * 1.5).float().to(DEV)
+    ids = np.ascontiguousarray(np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32))
+    l = np64(lg)
+    s = R.scores(l, "f32", score)
+    _, share = R.weights(l, s, "f32", ids, score, True, 1.0)
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    d_w[:, 2] = (share[:, :2] * d_w[:, :2]).sum(axis=1) / share[:, :2].sum(axis=1)
+    got = ops.route_scored_backward(torch.tensor(d_w).to(DEV), lg, torch.tensor(ids).to(DEV), ops.Scoring(score))
+    g, size = R.gradient(l, s, "f32", ids, d_w.astype(np.float64), score, True, 1.0)
+    close(got, g, R.ROUND["f32"] * np.abs(g) + R.TINY["f32"] + 2.0 ** -46 * size, "d_logits")
