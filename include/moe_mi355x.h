@@ -122,7 +122,8 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 /* Rules of the functions below.  logits [T, E] dense, fp32 (MOE_SRC_F32) or bf16
  * (MOE_SRC_BF16). Scores of a token's logits l:
  *     s_e = 1 / (1 + exp(-l_e))   or   exp(l_e) / sum over the row
- * evaluated in 64 bits.  A logit of -inf or of its type's lowest value masks its
+ * evaluated in 64 bits (a sigmoid score is 0 where exp(-l_e) passes their range, for
+ * l_e below -709.78).  A logit of -inf or of its type's lowest value masks its
  * expert: s_e = 0, and it counts in no sum.  A NaN or +inf makes its own sigmoid
  * score NaN or 1, and every softmax score of its row NaN.
  * Weights of the chosen experts id_j:

@@ -43,13 +43,13 @@ __device__ __forceinline__ bool is_masked(float l) {
 }
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// For weights and gradients, which are rounded to 32 bits: exp(x) from a polynomial of
+// For weights and gradients, which are rounded to 32 bits: exp(x), x <= 0, from a polynomial of
 // degree 10, 1 + r + r^2 g(r) with g interpolated at the Chebyshev nodes of
 // [-ln 2 / 2, ln 2 / 2] (off by 2^-49 of itself; Taylor's of that degree would be by 2^-41, which
 // shows where a gradient is a difference), a reciprocal from the hardware's and two Newton
 // steps (2^-50): a third of the instructions of the exact ones.
 __device__ __forceinline__ double exp_near(double x) {
-    x = x > 1000.0 ? 1000.0 : x < -1000.0 ? -1000.0 : x;
+    x = x < -1000.0 ? -1000.0 : x;
     const double n = __builtin_rint(x * 1.4426950408889634);
     const double r = __builtin_fma(-n, 2.319046813846300e-17, __builtin_fma(-n, 0.6931471805599453, x));
     double p = 2.761379556582631e-07;
@@ -65,13 +65,16 @@ __device__ __forceinline__ double exp_near(double x) {
     p = __builtin_fma(p, r, 1.0);
     return __builtin_amdgcn_ldexp(p, (int)n);
 }
-__device__ __forceinline__ double inverse_near(double x) {  // of a positive finite number below 2^1000
+__device__ __forceinline__ double inverse_near(double x) {  // of a number from 1 to 2^1000
     double y = __builtin_amdgcn_rcp(x);
     y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
     return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
 }
+// From exp(-|l|), so that no reciprocal leaves the normal range; 0 where exp(-l) passes the
+// largest double, as it makes 1 / (1 + exp(-l)) in 64 bits.
 __device__ __forceinline__ double sigmoid_near(double l) {
-    return l < -709.0 ? 0.0 : inverse_near(1.0 + exp_near(-l));  // (0 where sigmoid64 is below 2^-1022)
+    const double e = exp_near(-__builtin_fabs(l)), q = inverse_near(1.0 + e);
+    return l < -709.782712893384 ? 0.0 : l < 0.0 ? e * q : q;
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {

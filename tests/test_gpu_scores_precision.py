@@ -36,3 +36,23 @@ def test_balanced_gradients(score):
     got = ops.route_scored_backward(torch.tensor(d_w).to(DEV), lg, torch.tensor(ids).to(DEV), ops.Scoring(score))
     g, size = R.gradient(l, s, "f32", ids, d_w.astype(np.float64), score, True, 1.0)
     close(got, g, R.ROUND["f32"] * np.abs(g) + R.TINY["f32"] + 2.0 ** -46 * size, "d_logits")
+
+
+def test_sigmoid_scores_at_the_end_of_64_bits():
+    """Logits from -706 to the border below which scores are 0: weights of equal ones are 1 / k,
+    those of others their exponentials' shares."""
+    border = 709.782712893384
+    l = -np.concatenate([np.arange(706.0, 712.0, 0.01), [708.39, 708.4, 709.0, 709.01, 709.78, 709.79]]).astype(np.float32)
+    T, E, k = len(l), 8, 4
+    lg = np.repeat(l[:, None], E, axis=1)
+    lg[:, 1] = lg[:, 0] + np.float32(1.0)
+    x = lg.astype(np.float64)
+    ids = np.tile(np.arange(k, dtype=np.int32), (T, 1))
+    there = x[:, :k] >= -border
+    e = np.where(there, np.exp(x[:, :k] - x[:, 1:2]), 0.0)       # sigmoid(l) = exp(l) (1 - 2^-1000)
+    total = e.sum(axis=1, keepdims=True)
+    want = np.where(total == 0, 0.0, e / np.where(total == 0, 1.0, total))
+    rec = torch.tensor(np.ascontiguousarray(ids.T[None])).to(DEV)
+    _, w = ops.replay_scored(rec, 0, 0, torch.tensor(lg).to(DEV), ops.Scoring("sigmoid"))
+    # scores down to 2^-1024 are subnormal: off by half a step of 2^-1074, 2^-51 of them and less
+    close(w, want, (R.ROUND["f32"] + 2.0 ** -46) * want, "w")
