@@ -48,10 +48,7 @@ __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(
 // [-ln 2 / 2, ln 2 / 2] (off by 2^-49 of itself; Taylor's of that degree would be by 2^-41, which
 // shows where a gradient is a difference), a reciprocal from the hardware's and two Newton
 // steps (2^-50): a third of the instructions of the exact ones.
-__device__ __forceinline__ double exp_near(double x) {
-    x = x < -1000.0 ? -1000.0 : x;
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    const double r = __builtin_fma(-n, 2.319046813846300e-17, __builtin_fma(-n, 0.6931471805599453, x));
+__device__ __forceinline__ double exp_poly(double r) {
     double p = 2.761379556582631e-07;
     p = __builtin_fma(p, r, 2.7625102018960324e-06);
     p = __builtin_fma(p, r, 2.4801536409043718e-05);
@@ -62,19 +59,36 @@ __device__ __forceinline__ double exp_near(double x) {
     p = __builtin_fma(p, r, 0.16666666666648303);
     p = __builtin_fma(p, r, 0.5);
     p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, (int)n);
+    return __builtin_fma(p, r, 1.0);
 }
-__device__ __forceinline__ double inverse_near(double x) {  // of a number from 1 to 2^1000
+__device__ __forceinline__ double exp_near(double x) {
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(-n, 2.319046813846300e-17, __builtin_fma(-n, 0.6931471805599453, x));
+    // (a far x: r is up to 2^-53 |x|, the polynomial below 2^760, and the result 0)
+    return __builtin_amdgcn_ldexp(exp_poly(r), (int)__builtin_fmax(n, -2000.0));
+}
+// The same for a row's sum, in three operations less: the whole number comes from adding 1.5 2^52
+// (in its lowest bits), ln 2 is one constant (off by 2^-55 of itself, 2^-50 of a term at x = -30),
+// and x stops at -800, where terms are 0 next to the largest one's 1. For rows of
+// finite or masked logits alone: a NaN does not go through.
+__device__ __forceinline__ double exp_term(double x) {
+    constexpr double whole = 6755399441055744.0;
+    x = __builtin_fmax(x, -800.0);
+    const double t = __builtin_fma(x, 1.4426950408889634, whole);
+    const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
+    return __builtin_amdgcn_ldexp(exp_poly(__builtin_fma(whole - t, 0.6931471805599453, x)), n);
+}
+__device__ __forceinline__ double inverse_near(double x) {  // of a number from 1 to 2
     double y = __builtin_amdgcn_rcp(x);
     y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
     return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
 }
 // From exp(-|l|), so that no reciprocal leaves the normal range; 0 where exp(-l) passes the
-// largest double, as it makes 1 / (1 + exp(-l)) in 64 bits.
-__device__ __forceinline__ double sigmoid_near(double l) {
-    const double e = exp_near(-__builtin_fabs(l)), q = inverse_near(1.0 + e);
-    return l < -709.782712893384 ? 0.0 : l < 0.0 ? e * q : q;
+// largest double (at 709.7827 as a float), as it makes 1 / (1 + exp(-l)) in 64 bits.
+__device__ __forceinline__ double sigmoid_near(float l) {
+    const float far = fabsf(l);
+    const double e = exp_near((double)(far >= 709.7827f ? -1000.f : -far)), q = inverse_near(1.0 + e);
+    return (l < 0.f ? e : 1.0) * q;
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {
@@ -126,10 +140,10 @@ __device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(
 
 // Maximum and sum of exponentials of a row that a wave holds, masked experts left
 // out. A NaN anywhere makes the sum NaN (fmaxf passes over it, exp does not).
-// EXACT: in 64 bits, for the choice. Otherwise the terms are exp32's, added in 64 bits,
-// for weights and gradients: the sum is off by (2 ln E + 3) 2^-24 of itself (the mean
-// |x| weighted by exp(x) is ln E at most), the same in every kernel, whatever the order
-// of its terms.
+// EXACT: for the choice, which is defined by these values. Otherwise the terms are
+// exp_near's, for weights and gradients: the same terms in every kernel, added in 64 bits in an
+// order that goes by the lanes that hold a row, so that a weight made by two kernels can
+// differ where it lies next to the border of two fp32 values.
 struct RowStat {
     double m, inv;
 };
@@ -145,7 +159,7 @@ __device__ __forceinline__ RowStat row_stat(const float (&l)[VPL], int lane, int
     for (int i = 0; i < VPL; ++i)
         if (lane + 64 * i < E && !is_masked<F32>(l[i])) {
             if constexpr (EXACT) sum += exp((double)l[i] - (double)m);
-            else sum += (double)exp32(l[i] - m);
+            else sum += exp_near((double)l[i] - (double)m);
         }
     sum = wave_sum64(sum);
     return {(double)m, sum == 0.0 ? 0.0 : 1.0 / sum};
@@ -500,25 +514,34 @@ __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(Scor
         float m = 0.f, s_max = 1.f;
         double sum = 1.0;
         if constexpr (!SIGMOID) {
-            m = LOW;
+            m = c[0];
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) m = fmaxf(m, c[i]);
-            m = team_max<LPR>(m);
-            if (BIAS || !a.renorm) {
+            for (int i = 1; i < VPL; ++i) m = __builtin_elementwise_maximum(m, c[i]);
+            m = team_reduce<LPR>(m, [](float x, float y) { return __builtin_elementwise_maximum(x, y); });
+            // one NaN or infinity is in every score of its row
+            unsure = !(m < INFINITY);
+            m = unsure ? 0.f : m;
+            if (!a.renorm) {
+                // the weights' sum too (a row with nothing left: all terms 0)
+                const double top = m == LOW ? 0.0 : (double)m;
+                sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    sum += exp_term((double)c[i] - top);
+                    if (i % 8 == 7) __builtin_amdgcn_sched_barrier(0);
+                }
+            } else if (BIAS) {
                 sum = 0.0;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i) {
                     sum += c[i] == LOW ? 0.0 : (double)exp32(c[i] - m);
                     if (i % 8 == 7) __builtin_amdgcn_sched_barrier(0);
                 }
+            }
+            if (BIAS || !a.renorm) {
                 sum = team_sum<LPR>(sum);
                 s_max = sum == 0.0 ? 0.f : 1.0f / (float)sum;
             }
-            // one NaN is in every score of its row
-            bool nan = false;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) nan |= c[i] != c[i];
-            unsure = nan;
         }
         // score of a logit, 0 of LOW
         auto score32 = [&](float l) {
@@ -834,32 +857,50 @@ struct Row16 {
     float l[VPL];
     RowStat st;
     float m;
-    __device__ __forceinline__ void load(const void* logits, int64_t row, int E, int p) {
+    __device__ __forceinline__ void fetch(const void* logits, int64_t row, int E, int p) {
         const char* src = static_cast<const char*>(logits) + row * E * (F32 ? 4 : 2);
-        if (E >= 4) {
+        if (VPL > 4 || E >= 4) {
 #pragma unroll
             for (int j = 0; j < VPL / 4; ++j)
                 load4<F32>(l + 4 * j, src + (uint32_t)min(64 * j + 4 * p, E - 4) * (F32 ? 4u : 2u));
-            if (E & 3) {
-#pragma unroll
-                for (int j = 0; j < VPL / 4; ++j) shift4(l + 4 * j, 64 * j + 4 * p - (E - 4));
-            }
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) l[i] = logit<F32>(src, min(64 * (i >> 2) + 4 * p + (i & 3), E - 1));
         }
+    }
+    __device__ __forceinline__ void sums(int E, int p) {
+        if ((VPL > 4 || E >= 4) && (E & 3)) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            l[i] = 64 * (i >> 2) + 4 * p + (i & 3) < E && !is_masked<F32>(l[i]) ? l[i] : LOW;
-        m = LOW;
+            for (int j = 0; j < VPL / 4; ++j) shift4(l + 4 * j, 64 * j + 4 * p - (E - 4));
+        }
+        if (E < 16 * VPL) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
-        m = team_max<16>(m);
+            for (int i = 0; i < VPL; ++i) l[i] = 64 * (i >> 2) + 4 * p + (i & 3) < E ? l[i] : LOW;
+        }
+        // LOW for masked experts; m is NaN where a logit is
+        float least = l[0];
+        m = l[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) {
+            least = fminf(least, l[i]);
+            m = __builtin_elementwise_maximum(m, l[i]);
+        }
+        m = team_reduce<16>(m, [](float x, float y) { return __builtin_elementwise_maximum(x, y); });
+        if (__ballot(is_masked<F32>(least))) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) l[i] = is_masked<F32>(l[i]) ? LOW : l[i];
+            m = is_masked<F32>(m) ? LOW : m;
+        }
+        const double top = m == LOW ? 0.0 : (double)m;  // (a row with nothing left: all terms 0)
         double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) sum += l[i] == LOW ? 0.0 : (double)exp32(l[i] - m);
+        for (int i = 0; i < VPL; ++i) {
+            sum += exp_term((double)l[i] - top);
+            if (VPL > 32 && i % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // (more would not fit the registers)
+        }
         sum = team_sum<16>(sum);
-        st = {(double)m, sum == 0.0 ? 0.0 : 1.0 / sum};
+        if (!(m < INFINITY)) sum = NAN;
+        st = {(double)m, m == LOW ? 0.0 : 1.0 / sum};
     }
 };
 
@@ -872,9 +913,11 @@ __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int3
         const int64_t row = row0 + (threadIdx.x >> 4);
         const bool live = row < a.T;
         const int64_t t = live ? row : row0;
-        const int id = lane < k ? a.rec[(int64_t)lane * a.rec_stride + t] : 0;
+        int p = lane;
+        asm volatile("" : "+v"(p));  // (what follows from it is made where it is used: most waves have one round)
         Row16<F32, VPL> r;
-        r.load(a.logits, t, E, lane);
+        r.fetch(a.logits, t, E, p);
+        const int id = lane < k ? a.rec[(int64_t)lane * a.rec_stride + t] : 0;
         int bad = lane < k && (id < 0 || id >= E), dup = 0;
         for (int j = 0; j < k; ++j) {
             const int o = __shfl(id, j, 16);
@@ -882,7 +925,8 @@ __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int3
         }
         bad = ((__ballot(bad) >> (threadIdx.x & 48)) & 0xFFFF) != 0;
         dup = ((__ballot(dup) >> (threadIdx.x & 48)) & 0xFFFF) != 0;
-        const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));
+        const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));  // on its way during the sums
+        r.sums(E, p);
         if (live && lane < k) {
             a.ids[row * k + lane] = id;
             a.w[row * k + lane] = bad ? 0.f : (float)((double)a.scale * score<F32, false>(ls, r.st));
@@ -917,7 +961,8 @@ template <bool F32, bool SIGMOID, bool RENORM, bool PARTS, int VPL>
 __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
     constexpr bool WHOLE = !SIGMOID && !RENORM;
     extern __shared__ float lds_all[];
-    const int lane = threadIdx.x & 63, p = lane & 15, team = lane >> 4, E = a.E, k = a.k;
+    const int lane = threadIdx.x & 63, team = lane >> 4, E = a.E, k = a.k;
+    int p = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int EP = WHOLE ? (E + 3) & ~3 : E;  // a row's floats in LDS
     float* lds = lds_all + wave * a.lds_wave;
@@ -927,6 +972,12 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
         const int64_t row = row0 + team;
         const bool live = row < a.T;
         const int64_t t = live ? row : row0;
+        Row16<F32, VPL> r;
+        r.st = {0.0, 0.0};
+        if constexpr (WHOLE) {
+            asm volatile("" : "+v"(p));  // (what follows from it is made where it is used: most waves have one round)
+            r.fetch(a.logits, t, E, p);
+        }
         const int id = p < k ? a.ids[t * k + p] : 0;
         float dw = 0.f;
         if constexpr (PARTS) {
@@ -945,17 +996,15 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
         for (int i = 4 * lane; i < 4 * EP; i += 256) *reinterpret_cast<float4*>(lds + i) = float4{0.f, 0.f, 0.f, 0.f};
         const bool outside = p < k && (id < 0 || id >= E);
         const bool bad = ((__ballot(outside) >> (16 * team)) & 0xFFFF) != 0;
-        Row16<F32, VPL> r;
-        r.st = {0.0, 0.0};
-        if constexpr (WHOLE) r.load(a.logits, t, E, p);
         const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));
+        if constexpr (WHOLE) r.sums(E, p);
         const double s = score<F32, SIGMOID>(ls, r.st);
         const double h = share<F32, SIGMOID, 16>(ls, s, p, k, RENORM);
         double dot = 0.0;
         if constexpr (RENORM || WHOLE) dot = team_sum<16>(p < k ? h * (double)dw : 0.0);
         // the slot's gradient of its own logit; WHOLE: of its score
         double c = WHOLE ? (double)a.scale * (double)dw : (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
-        if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-(double)ls);
+        if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-ls);
         wave_sync();
         const bool on = p < k && !bad;
         if (on) reinterpret_cast<int*>(mine)[id] = p;

@@ -56,3 +56,37 @@ def test_sigmoid_scores_at_the_end_of_64_bits():
     _, w = ops.replay_scored(rec, 0, 0, torch.tensor(lg).to(DEV), ops.Scoring("sigmoid"))
     # scores down to 2^-1024 are subnormal: off by half a step of 2^-1074, 2^-51 of them and less
     close(w, want, (R.ROUND["f32"] + 2.0 ** -46) * want, "w")
+
+
+def softmax_rows(T, E, seed):
+    """Rows of which a third are normal, a third have one logit in front and all others equal
+    (their exponentials' errors have one sign), a third one logit far in front."""
+    rng = np.random.default_rng(seed)
+    l = rng.standard_normal((T, E)) * 1.5
+    flat = l[1::3]
+    flat[:] = rng.uniform(-6.0, 0.0, size=(len(flat), 1))
+    flat[np.arange(len(flat)), rng.integers(0, E, size=len(flat))] = 0.3
+    far = l[2::3]
+    far[np.arange(len(far)), rng.integers(0, E, size=len(far))] += rng.uniform(8.0, 25.0, size=len(far))
+    return l
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,groups,top_groups", [
+    (1200, 3, 2, 1, 1), (1200, 16, 2, 1, 1), (9000, 60, 6, 5, 2), (1200, 128, 8, 1, 1), (9000, 256, 8, 8, 4), (9000, 256, 8, 1, 1),
+    (600, 256, 16, 1, 1), (1200, 256, 16, 16, 5), (1200, 512, 8, 16, 4), (9000, 510, 8, 1, 1), (600, 1024, 16, 1, 1),
+    (600, 1000, 8, 40, 11), (1, 256, 8, 8, 4)])
+def test_softmax_weights_are_rounded_once(kind, T, E, k, groups, top_groups):
+    """Weights that are not renormalised: scores of the whole row, rounded once from 64 bits."""
+    say(f"softmax weights T={T} E={E} k={k} {kind}")
+    lg = torch.tensor(softmax_rows(T, E, 42)).to(dict(f32=torch.float32, bf16=torch.bfloat16)[kind]).to(DEV)
+    l = np64(lg)
+    s = R.scores(l, kind, "softmax")
+    rec = torch.zeros((1, k, T), dtype=torch.int32, device=DEV)
+    for bias in (None, torch.tensor(np.random.default_rng(43).standard_normal(E).astype(np.float32) * 0.05).to(DEV)):
+        sc = ops.Scoring("softmax", groups=groups, top_groups=top_groups, renorm=False, scale=1.5)
+        ids, w = ops.route_scored(lg, k, sc, bias=bias, capture=(rec, 0, 0))
+        want, _ = R.weights(l, s, kind, ids.cpu().numpy(), "softmax", False, 1.5)
+        tol = (R.ROUND["f32"] + 2.0 ** -46) * want + R.TINY["f32"]
+        close(w, want, tol, "w")
+        close(ops.replay_scored(rec, 0, 0, lg, sc)[1], want, tol, "replayed w")
