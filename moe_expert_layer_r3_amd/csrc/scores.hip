@@ -70,9 +70,11 @@ __device__ __forceinline__ double exp_near(double x) {
 // The same for a row's sum, in three operations less: the whole number comes from adding 1.5 2^52
 // (in its lowest bits), ln 2 is one constant (off by 2^-55 of itself, 2^-50 of a term at x = -30),
 // and x stops at -800, where terms are 0 next to the largest one's 1. For rows of
-// finite or masked logits alone: a NaN does not go through.
+// finite or masked logits alone: a NaN does not go through. Times 2^UP, whose exponent comes with
+// the whole number.
+template <int UP = 0>
 __device__ __forceinline__ double exp_term(double x) {
-    constexpr double whole = 6755399441055744.0;
+    constexpr double whole = 6755399441055744.0 + UP;
     x = __builtin_fmax(x, -800.0);
     const double t = __builtin_fma(x, 1.4426950408889634, whole);
     const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
@@ -851,12 +853,16 @@ __global__ __launch_bounds__(256) void score_replay_kernel(ScoreArgs a, int32_t*
     }
 }
 
-// A row that 16 lanes hold: lane p the logits 64 j + 4 p + i, and its softmax.
-template <bool F32, int VPL>
+// A row that 16 lanes hold: lane p the logits 64 j + 4 p + i, and its softmax. KEEP: l is
+// afterwards 2^UP exp(l - m), rounded once to 32 bits, in which 2^UP keeps the normal range down to
+// scores of 2^-150 (and a gradient made from it has room for values up to 2^104).
+template <bool F32, int VPL, bool KEEP = false>
 struct Row16 {
+    static constexpr int UP = KEEP ? 24 : 0;
     float l[VPL];
     RowStat st;
-    float m;
+    bool odd;        // a NaN or infinity is in every score that is not masked: KEEP says which of the lane's
+    uint64_t there;  // are not, and l is 0
     __device__ __forceinline__ void fetch(const void* logits, int64_t row, int E, int p) {
         const char* src = static_cast<const char*>(logits) + row * E * (F32 ? 4 : 2);
         if (VPL > 4 || E >= 4) {
@@ -878,8 +884,7 @@ struct Row16 {
             for (int i = 0; i < VPL; ++i) l[i] = 64 * (i >> 2) + 4 * p + (i & 3) < E ? l[i] : LOW;
         }
         // LOW for masked experts; m is NaN where a logit is
-        float least = l[0];
-        m = l[0];
+        float least = l[0], m = l[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) {
             least = fminf(least, l[i]);
@@ -892,15 +897,26 @@ struct Row16 {
             m = is_masked<F32>(m) ? LOW : m;
         }
         const double top = m == LOW ? 0.0 : (double)m;  // (a row with nothing left: all terms 0)
+        odd = !(m < INFINITY);
+        if (KEEP && __ballot(odd)) {
+            there = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) there |= (uint64_t)(l[i] != LOW) << i;
+        }
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            sum += exp_term((double)l[i] - top);
-            if (VPL > 32 && i % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // (more would not fit the registers)
+            const double e = exp_term<UP>((double)l[i] - top);
+            sum += e;
+            if constexpr (KEEP) {
+                l[i] = (float)e;
+                asm volatile("" : "+v"(l[i]));  // (here, in the logit's register)
+            }
+            if ((KEEP || VPL > 32) && i % 8 == 7) __builtin_amdgcn_sched_barrier(0);  // (more would not fit the registers)
         }
         sum = team_sum<16>(sum);
-        if (!(m < INFINITY)) sum = NAN;
-        st = {(double)m, m == LOW ? 0.0 : 1.0 / sum};
+        if (odd) sum = NAN;
+        st = {(double)m, m == LOW ? 0.0 : (double)(1 << UP) / sum};
     }
 };
 
@@ -954,7 +970,10 @@ struct ScoreGradArgs {
 };
 
 // 16 lanes per token, four tokens to a wave: lane j < k has slot j; the slots' values go
-// into the rows' place in LDS, from which whole rows are written. Bound by writing
+// into the rows' place in LDS, from which whole rows are written. In the whole-row form
+// they are the brackets of s_e (scale d_w - scale dot), made in 64 bits: for a row of one large score
+// the two terms are nearly equal. Brackets, 1 / sum and exponentials are rounded to 32 bits each
+// and multiplied there: 5 2^-24 of a gradient. Bound by writing
 // [T, E] (and reading it, where every logit has a gradient): 16384 tokens of 256 experts, fp32,
 // 7.2 us, and 8.9 with the whole row's gradient.
 template <bool F32, bool SIGMOID, bool RENORM, bool PARTS, int VPL>
@@ -972,7 +991,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
         const int64_t row = row0 + team;
         const bool live = row < a.T;
         const int64_t t = live ? row : row0;
-        Row16<F32, VPL> r;
+        Row16<F32, VPL, true> r;
         r.st = {0.0, 0.0};
         if constexpr (WHOLE) {
             asm volatile("" : "+v"(p));  // (what follows from it is made where it is used: most waves have one round)
@@ -993,16 +1012,27 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
             dw = a.d_w[t * k + p];
         }
         // zeros to the rows' place
-        for (int i = 4 * lane; i < 4 * EP; i += 256) *reinterpret_cast<float4*>(lds + i) = float4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (!WHOLE)
+            for (int i = 4 * lane; i < 4 * EP; i += 256) *reinterpret_cast<float4*>(lds + i) = float4{0.f, 0.f, 0.f, 0.f};
         const bool outside = p < k && (id < 0 || id >= E);
         const bool bad = ((__ballot(outside) >> (16 * team)) & 0xFFFF) != 0;
         const float ls = logit<F32>(a.logits, t * E + (bad ? 0 : id));
-        if constexpr (WHOLE) r.sums(E, p);
+        if constexpr (WHOLE) {
+            r.sums(E, p);
+            asm volatile("" : "+v"(p));  // (its columns are not kept over the sums)
+        }
         const double s = score<F32, SIGMOID>(ls, r.st);
         const double h = share<F32, SIGMOID, 16>(ls, s, p, k, RENORM);
         double dot = 0.0;
         if constexpr (RENORM || WHOLE) dot = team_sum<16>(p < k ? h * (double)dw : 0.0);
-        // the slot's gradient of its own logit; WHOLE: of its score
+        // the slot's gradient of its own logit; WHOLE: of its score, -scale dot that of every other
+        const double all = WHOLE ? (double)a.scale * dot : 0.0;
+        if constexpr (WHOLE) {
+            const float v = bad ? 0.f : (float)-all;
+#pragma unroll
+            for (int j = 0; j < VPL / 4; ++j)
+                if (64 * j + 4 * p < E) *reinterpret_cast<float4*>(mine + 64 * j + 4 * p) = float4{v, v, v, v};
+        }
         double c = WHOLE ? (double)a.scale * (double)dw : (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
         if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-ls);
         wave_sync();
@@ -1020,10 +1050,10 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
             c = sum;
         }
         wave_sync();
-        if (on) mine[id] = (float)c;
+        if (on) mine[id] = (float)(c - all);
         wave_sync();
         if constexpr (WHOLE) {
-            const float scaled = bad ? 0.f : (float)((double)a.scale * dot), inv = bad ? 0.f : (float)r.st.inv;
+            const float inv = bad ? 0.f : (float)r.st.inv;
             char* out = static_cast<char*>(a.d_logits) + t * E * (F32 ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < VPL / 4; ++j) {
@@ -1032,11 +1062,7 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
                 const float4 q = *reinterpret_cast<const float4*>(mine + e);
                 float v[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (by the root of the score: exp2 gives no values below the normal range)
-                    const float l = r.l[4 * j + i], root = exp32(0.5f * (l - r.m));
-                    v[i] = l == LOW ? 0.f : root * (root * (inv * (v[i] - scaled)));
-                }
+                for (int i = 0; i < 4; ++i) v[i] = r.l[4 * j + i] * (inv * v[i]) * (1.0f / (1 << r.UP));
                 if (e + 4 <= E) {
                     if constexpr (F32) *reinterpret_cast<f4u*>(out + e * 4) = f4u{v[0], v[1], v[2], v[3]};
                     else *reinterpret_cast<h4u*>(out + e * 2) = h4u{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
@@ -1045,6 +1071,16 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
                         if constexpr (F32) reinterpret_cast<float*>(out)[e + i] = v[i];
                         else reinterpret_cast<uint16_t*>(out)[e + i] = (uint16_t)f32_to_bf16(v[i]);
                     }
+                }
+            }
+            if (__ballot(live && r.odd && !bad)) {
+#pragma unroll 1
+                for (int i = 0; i < VPL; ++i) {
+                    const int e = 64 * (i >> 2) + 4 * p + (i & 3);
+                    const float v = (r.there >> i) & 1 ? NAN : 0.f;
+                    if (!live || !r.odd || bad || e >= E) continue;
+                    if constexpr (F32) reinterpret_cast<float*>(out)[e] = v;
+                    else reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)f32_to_bf16(v);
                 }
             }
         } else {

@@ -90,3 +90,42 @@ def test_softmax_weights_are_rounded_once(kind, T, E, k, groups, top_groups):
         tol = (R.ROUND["f32"] + 2.0 ** -46) * want + R.TINY["f32"]
         close(w, want, tol, "w")
         close(ops.replay_scored(rec, 0, 0, lg, sc)[1], want, tol, "replayed w")
+
+
+def plain_softmax_gradient(s, ids, d_w, scale):
+    """(d_logits, size of the terms of its bracket times the score) of s_e (scale sum d_w - scale dot)."""
+    T, E = s.shape
+    i64 = ids.astype(np.int64)
+    sel = np.take_along_axis(s, i64, axis=1)
+    own, big = np.zeros((T, E)), np.zeros((T, E))
+    at = (np.repeat(np.arange(T), ids.shape[1]), i64.ravel())
+    np.add.at(own, at, scale * d_w.ravel())
+    np.add.at(big, at, scale * np.abs(d_w).ravel())
+    return (s * (own - scale * (sel * d_w).sum(axis=1, keepdims=True)),
+            s * (big + scale * np.abs(sel * d_w).sum(axis=1, keepdims=True)))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(2001, 4, 1), (1203, 60, 2), (1202, 64, 1), (3001, 256, 1), (3001, 256, 8), (801, 510, 3),
+                                   (803, 1024, 1), (803, 1000, 16), (1, 256, 1)])
+def test_plain_softmax_gradients_of_confident_rows(kind, T, E, k):
+    """Gaps up to 25 between the largest logit and the rest: its gradient is scale d_w s (1 - s).
+    Five roundings to 32 bits (bracket, 1 / sum, exponential, two products), then that to bf16."""
+    scale = 1.5
+    for chosen in ("best", "any", "twice"):
+        say(f"plain softmax gradient T={T} E={E} k={k} {kind} {chosen}")
+        rng = np.random.default_rng(44)
+        lg = torch.tensor(softmax_rows(T, E, 45)).to(dict(f32=torch.float32, bf16=torch.bfloat16)[kind]).to(DEV)
+        l = np64(lg)
+        s = R.scores(l, kind, "softmax")
+        order = np.argsort(-l if chosen == "best" else rng.random((T, E)), axis=1, kind="stable")
+        ids = np.ascontiguousarray(order[:, :k].astype(np.int32))
+        if chosen == "twice":
+            ids[:, k // 2:] = order[:, :1]
+        d_w = (0.5 + rng.random((T, k))).astype(np.float32)
+        d_w[::2] = d_w[::2, :1]
+        got = ops.route_scored_backward(torch.tensor(d_w).to(DEV), lg, torch.tensor(ids).to(DEV),
+                                        ops.Scoring("softmax", renorm=False, scale=scale))
+        g, size = plain_softmax_gradient(s, ids, d_w.astype(np.float64), scale)
+        tol = (5 * U * 1.001 + (R.ROUND["bf16"] if kind == "bf16" else 0.0)) * np.abs(g) + R.TINY[kind] + 2.0 ** -46 * size
+        close(got, g, tol, "d_logits")
