@@ -168,8 +168,9 @@ int moe_replay_scored(const int32_t* rec, int32_t n_layers, int32_t k, int64_t s
  *     sigmoid:            dl_j = scale d_w_j s_j (1 - s_j)
  *     softmax, renorm:    dl_j = w_j (d_w_j - sum_i d_w_i w_i / scale)
  *     softmax:            dl_e = s_e (scale sum over {j: id_j = e} of d_w_j - sum_i d_w_i w_i)
- * summed over the slots of an expert, 0 at the others.  A token with an id
- * outside [0, E) gets 0.
+ * summed over the slots of an expert, 0 at the others and at masked experts (also where
+ * a NaN or an infinity makes the token's other gradients NaN).  A token with an
+ * id outside [0, E) gets 0.
  *   d_w [T, k] fp32, logits as given to the forward, ids [T, k]; d_logits [T, E]
  *   of logits' type.  scale = 0 counts as the limit (all gradients 0).          */
 int moe_route_scored_backward(const float* d_w, const void* logits, int32_t logits_type, const int32_t* ids, int64_t T,

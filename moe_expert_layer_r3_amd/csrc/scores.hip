@@ -1034,7 +1034,8 @@ __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
                 if (64 * j + 4 * p < E) *reinterpret_cast<float4*>(mine + 64 * j + 4 * p) = float4{v, v, v, v};
         }
         double c = WHOLE ? (double)a.scale * (double)dw : (double)a.scale * h * ((double)dw - (RENORM ? dot : 0.0));
-        if constexpr (SIGMOID) c = is_masked<F32>(ls) ? 0.0 : c * sigmoid_near(-ls);
+        if constexpr (SIGMOID) c *= sigmoid_near(-ls);
+        if (!WHOLE && is_masked<F32>(ls)) c = 0.0;  // (next to a chosen NaN too)
         wave_sync();
         const bool on = p < k && !bad;
         if (on) reinterpret_cast<int*>(mine)[id] = p;

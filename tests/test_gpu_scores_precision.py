@@ -129,3 +129,62 @@ def test_plain_softmax_gradients_of_confident_rows(kind, T, E, k):
         g, size = plain_softmax_gradient(s, ids, d_w.astype(np.float64), scale)
         tol = (5 * U * 1.001 + (R.ROUND["bf16"] if kind == "bf16" else 0.0)) * np.abs(g) + R.TINY[kind] + 2.0 ** -46 * size
         close(got, g, tol, "d_logits")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("E,k", [(9, 3), (64, 4), (256, 8), (510, 2), (1000, 16)])
+def test_gradients_of_odd_logits(score, renorm, E, k, kind):
+    """NaN and infinite logits, masked experts among the chosen ones, ids outside [0, E): NaN
+    where a score is NaN in the formula, 0 at masked experts and for tokens with such an id."""
+    say(f"odd gradients {score} renorm={renorm} E={E} k={k} {kind}")
+    T, scale = 403, 1.5
+    rng = np.random.default_rng(46)
+    l = rng.standard_normal((T, E)) * 1.3
+    l[rng.random((T, E)) < 0.2] = -np.inf
+    l[rng.random((T, E)) < 0.1] = R.LOWEST[kind]
+    odd = rng.random((T, E)) < 0.5 / E
+    l[odd] = rng.choice([np.nan, np.inf], size=odd.sum())
+    l[5] = np.nan
+    l[6] = -np.inf
+    l[7], l[7, 1::2] = -np.inf, np.inf
+    l[8], l[8, ::3] = np.nan, R.LOWEST[kind]
+    lg = torch.tensor(l).to(dict(f32=torch.float32, bf16=torch.bfloat16)[kind]).to(DEV)
+    ids = np.ascontiguousarray(np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32))
+    ids[3::11, k // 2] = rng.choice([-1, E, E + 5, -(1 << 31), (1 << 31) - 1], size=len(ids[3::11]))
+    bad = ((ids < 0) | (ids >= E)).any(axis=1)
+    assert bad[(np.isnan(l) | (l == np.inf)).any(axis=1)].any()
+    d_w = rng.standard_normal((T, k)).astype(np.float32)
+    got = ops.route_scored_backward(torch.tensor(d_w).to(DEV), lg, torch.tensor(ids).to(DEV),
+                                    ops.Scoring(score, renorm=renorm, scale=scale))
+    l, dw = np64(lg), d_w.astype(np.float64)
+    i64 = np.where(bad[:, None], 0, ids).astype(np.int64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        s = R.scores(l, kind, score)
+        if score == "softmax":
+            s = np.where((l == np.inf).any(axis=1, keepdims=True) & ~R.masked(l, kind), np.nan, s)
+        if score == "softmax" and not renorm:
+            g, size = plain_softmax_gradient(s, i64, dw, scale)
+        else:
+            if score == "softmax" and renorm:      # of the chosen logits alone
+                some = np.isnan(np.take_along_axis(l, i64, axis=1)) | (np.take_along_axis(l, i64, axis=1) == np.inf)
+                _, share = R.weights(l, s, kind, i64, score, True, scale)
+                share = np.where(some.any(axis=1, keepdims=True), np.nan, share)
+            else:
+                _, share = R.weights(l, s, kind, i64, score, renorm, scale)
+            dot = (share * dw).sum(axis=1, keepdims=True) if renorm else 0.0
+            own = scale * share * (dw - dot)
+            size = np.abs(scale * share * dw)
+            if renorm:
+                size = size + np.abs(scale * share) * np.abs(share * dw).sum(axis=1, keepdims=True)
+            if score == "sigmoid":
+                far = 1.0 / (1.0 + np.exp(np.take_along_axis(l, i64, axis=1)))
+                own, size = own * far, size * far
+            g, big = np.zeros((T, E)), np.zeros((T, E))
+            np.put_along_axis(g, i64, own, axis=1)
+            np.put_along_axis(big, i64, size, axis=1)
+            size = big
+    g, size = np.where(R.masked(l, kind), 0.0, g), np.where(R.masked(l, kind), 0.0, size)
+    g[bad], size[bad] = 0.0, 0.0
+    tol = (5 * U * 1.001 + R.ROUND[kind]) * np.abs(g) + R.TINY[kind] + 2.0 ** -46 * size
+    close(got, g, tol, "d_logits")
