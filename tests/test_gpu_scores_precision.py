@@ -188,3 +188,33 @@ def test_gradients_of_odd_logits(score, renorm, E, k, kind):
     g[bad], size[bad] = 0.0, 0.0
     tol = (5 * U * 1.001 + R.ROUND[kind]) * np.abs(g) + R.TINY[kind] + 2.0 ** -46 * size
     close(got, g, tol, "d_logits")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("score,renorm", [("sigmoid", True), ("sigmoid", False), ("softmax", True), ("softmax", False)])
+@pytest.mark.parametrize("E,k", [(16, 4), (256, 8), (600, 3)])
+def test_weights_of_very_negative_logits(score, renorm, E, k, kind):
+    """Scores next to fp32's smallest values and below them: chosen where nothing larger is there
+    (sigmoid), and replayed, of softmax next to a large one."""
+    say(f"very negative {score} renorm={renorm} E={E} k={k} {kind}")
+    T = 300
+    rng = np.random.default_rng(47)
+    l = rng.uniform(-106.0, -84.0, size=(T, E))
+    if score == "softmax":
+        l[:, 0] = 0.0
+    lg = torch.tensor(l).to(dict(f32=torch.float32, bf16=torch.bfloat16)[kind]).to(DEV)
+    l = np64(lg)
+    s = R.scores(l, kind, score)
+    sc = ops.Scoring(score, renorm=renorm)
+    if score == "sigmoid":
+        ids, w = ops.route_scored(lg, k, sc)
+        ref = R.choices(l, s, kind, k)
+        assert np.array_equal(ids.cpu().numpy(), ref)
+        want, _ = R.weights(l, s, kind, ref, score, renorm, 1.0)
+        close(w, want, (R.ROUND["f32"] + 2.0 ** -46) * want + R.TINY["f32"], "w")
+    ids = np.ascontiguousarray(1 + np.argsort(rng.random((T, E - 1)), axis=1)[:, :k].astype(np.int32))
+    rec = torch.tensor(np.ascontiguousarray(ids.T[None])).to(DEV)
+    _, w = ops.replay_scored(rec, 0, 0, lg, sc)
+    want, _ = R.weights(l, s, kind, ids, score, renorm, 1.0)
+    assert renorm or want.min() < 2.0 ** -145 < 2.0 ** -126 < want.max()    # subnormal ones and others
+    close(w, want, (R.ROUND["f32"] + 2.0 ** -46) * want + R.TINY["f32"], "replayed w")
