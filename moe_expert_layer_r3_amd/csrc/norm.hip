@@ -23,6 +23,7 @@ struct JoinArgs {
     void* r_out;
     uint16_t* h;
     float *rstd_post, *rstd_pre;
+    float part, parts;  // set by the launch: see square_of
 };
 
 struct JoinGradArgs {
@@ -110,6 +111,15 @@ __device__ __forceinline__ float gate_value(float x, int act) {
 }
 __device__ __forceinline__ float gate_slope(float x, int act) { return gate_of(x, act).slope; }
 
+// Squares are taken of values times part = 2^-n, 4^n >= d, and their sum divided by
+// parts = d 4^-n: it then passes fp32's range where the mean itself does, not d times before.
+// (Powers of two: nothing is rounded but squares that are subnormal then, next to which even an
+// eps of 1e-28 is large.)
+__device__ __forceinline__ float square_of(float v, float part) {
+    const float q = v * part;
+    return q * q;
+}
+
 // Sum over the workgroup, the same in every thread; `slot` alternates so that one
 // barrier does.
 __device__ __forceinline__ float block_sum(float v, float (*lds)[NT / 64], int& slot) {
@@ -159,9 +169,9 @@ __global__ __launch_bounds__(NT) void join_kernel(JoinArgs a) {
                 float v[8];
                 load8(v, y, c, false);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s += v[j] * v[j];
+                for (int j = 0; j < 8; ++j) s += square_of(v[j], a.part);
             }
-            rho_y = 1.0f / sqrtf(block_sum(s, lds, slot) / (float)d + a.eps);
+            rho_y = 1.0f / sqrtf(block_sum(s, lds, slot) / a.parts + a.eps);
             if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rho_y;
         }
         const void* r = RF32 ? (const void*)(static_cast<const float*>(a.r) + t * a.ldr)
@@ -182,13 +192,10 @@ __global__ __launch_bounds__(NT) void join_kernel(JoinArgs a) {
                 store8(a.r_out, t * d + c, RF32, rv);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float q = stored(rv[j], RF32);
-                s += q * q;
-            }
+            for (int j = 0; j < 8; ++j) s += square_of(stored(rv[j], RF32), a.part);
         }
         if (!a.w_pre) continue;
-        const float rho = 1.0f / sqrtf(block_sum(s, lds, slot) / (float)d + a.eps);
+        const float rho = 1.0f / sqrtf(block_sum(s, lds, slot) / a.parts + a.eps);
         if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rho;
         for (int64_t c = threadIdx.x * 8; c < d; c += NT * 8) {
             float rv[8], w[8];
@@ -471,9 +478,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a
             if (a.w_post) {
                 float s[1] = {0.f};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[0] += y[j] * y[j];
+                for (int j = 0; j < 8; ++j) s[0] += square_of(y[j], a.part);
                 team_sum<WAVE>(s, L, lds, slot);
-                rho_y = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+                rho_y = 1.0f / sqrtf(s[0] / a.parts + a.eps);
                 if (a.rstd_post && live && tm.c == 0) a.rstd_post[t] = rho_y;
             }
             float gt = 1.0f;
@@ -492,9 +499,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void join_rows_kernel(JoinArgs a
         if (!a.w_pre) continue;
         float s[1] = {0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += rv[j] * rv[j];
+        for (int j = 0; j < 8; ++j) s[0] += square_of(rv[j], a.part);
         team_sum<WAVE>(s, L, lds, slot);
-        const float rho = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+        const float rho = 1.0f / sqrtf(s[0] / a.parts + a.eps);
         if (live && tm.on) {
             if (a.rstd_pre && tm.c == 0) a.rstd_pre[t] = rho;
 #pragma unroll
@@ -703,9 +710,9 @@ __global__ __launch_bounds__(1024) void join_long_kernel(JoinArgs a) {
 #pragma unroll
                 for (int k = 0; k < LONG; ++k)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s[0] += y[k][j] * y[k][j];
+                    for (int j = 0; j < 8; ++j) s[0] += square_of(y[k][j], a.part);
                 team_sum<false>(s, 64, lds, slot);
-                rho_y = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+                rho_y = 1.0f / sqrtf(s[0] / a.parts + a.eps);
                 if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rho_y;
             }
             float gt = 1.0f;
@@ -734,9 +741,9 @@ __global__ __launch_bounds__(1024) void join_long_kernel(JoinArgs a) {
 #pragma unroll
         for (int k = 0; k < LONG; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] += r[k][j] * r[k][j];
+            for (int j = 0; j < 8; ++j) s[0] += square_of(r[k][j], a.part);
         team_sum<false>(s, 64, lds, slot);
-        const float rho = 1.0f / sqrtf(s[0] / (float)d + a.eps);
+        const float rho = 1.0f / sqrtf(s[0] / a.parts + a.eps);
         if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rho;
 #pragma unroll
         for (int k = 0; k < LONG; ++k) {
@@ -1043,7 +1050,9 @@ void launch_join_backward(const JoinGradArgs& a, hipStream_t stream) {
     });
 }
 
-int launch_forward(const JoinArgs& a, bool r_f32, hipStream_t stream) {
+int launch_forward(JoinArgs a, bool r_f32, hipStream_t stream) {
+    a.part = 1.0f;
+    for (a.parts = (float)a.d; a.parts > 1.0f; a.parts *= 0.25f) a.part *= 0.5f;
     if (r_f32) launch_join<true>(a, stream);
     else launch_join<false>(a, stream);
     MOE_LAUNCH_CHECK("join_rows_kernel");
