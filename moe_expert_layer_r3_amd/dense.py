@@ -181,7 +181,7 @@ class MoELayerPlan:
     Needs every expert on this GPU (L == E): under expert parallelism d_logits
     has to be summed over the GPUs between the parts."""
 
-    def __init__(self, T, d, f, E, k, fs, act="silu", act8=False, router_bias=False, scoring=None, device="cuda"):
+    def __init__(self, T, d, f, E, k, fs, act="silu", act8=False, router_bias=False, device="cuda", scoring=None):
         self.T, self.d = T, d
         self.router = LinearPlan(T, d, E, out_dtype=torch.float32, train=True, bias=router_bias, device=device)
         dv = self.router.device
