@@ -84,7 +84,7 @@ class RoutePlan:
     def capture(self, logits, bias=None, load=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture);
         the warm-up calls count into load too."""
-        return capture_graph(lambda: self.forward(logits, bias=bias, load=load), warmup)
+        return capture_graph(lambda: self.forward(logits, bias=bias, load=load), warmup, self.device)
 
 
 class NormPlan:
@@ -129,7 +129,7 @@ class NormPlan:
 
     def capture(self, x, w, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
-        return capture_graph(lambda: self.forward(x, w), warmup)
+        return capture_graph(lambda: self.forward(x, w), warmup, self.device)
 
 
 class JoinPlan:
@@ -221,7 +221,7 @@ class JoinPlan:
 
     def capture(self, y, r, w_post=None, gate=None, w_pre=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
-        return capture_graph(lambda: self.forward(y, r, w_post=w_post, gate=gate, w_pre=w_pre), warmup)
+        return capture_graph(lambda: self.forward(y, r, w_post=w_post, gate=gate, w_pre=w_pre), warmup, self.device)
 
 
 class MoEBlockPlan:

@@ -81,7 +81,7 @@ class LinearPlan:
 
     def capture(self, x, W, bias=None, residual=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
-        return capture_graph(lambda: self.forward(x, W, bias=bias, residual=residual), warmup)
+        return capture_graph(lambda: self.forward(x, W, bias=bias, residual=residual), warmup, self.device)
 
 
 class GatedFFNPlan:
@@ -161,7 +161,7 @@ class GatedFFNPlan:
 
     def capture(self, x, W13, W2, b13=None, b2=None, residual=None, warmup=1):
         """``forward`` over these exact buffers as a HIP graph (see ForwardPlan.capture)."""
-        return capture_graph(lambda: self.forward(x, W13, W2, b13=b13, b2=b2, residual=residual), warmup)
+        return capture_graph(lambda: self.forward(x, W13, W2, b13=b13, b2=b2, residual=residual), warmup, self.device)
 
 
 class MoELayerPlan:

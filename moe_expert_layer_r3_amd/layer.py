@@ -186,20 +186,22 @@ class ForwardPlan:
         return capture_graph(lambda: self.forward(x, logits, wts, replay=replay), warmup)
 
 
-def capture_graph(fn, warmup=1):
+def capture_graph(fn, warmup=1, device=None):
     """Record the launches ``fn`` issues on the current stream into a HIP graph
     (torch.cuda.CUDAGraph), after ``warmup`` eager calls on a side stream.  fn
     must only launch library kernels on preallocated buffers: no allocation,
-    host synchronisation or memset."""
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):
-        for _ in range(warmup):
+    host synchronisation or memset.  device: the one fn launches on, where it is
+    not the current one (streams and graph are then of that device)."""
+    with torch.cuda.device(torch.cuda.current_device() if device is None else device):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(warmup):
+                fn()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
             fn()
-    torch.cuda.current_stream().wait_stream(side)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        fn()
     return graph
 
 
