@@ -172,7 +172,9 @@ int moe_replay_scored(const int32_t* rec, int32_t n_layers, int32_t k, int64_t s
  * a NaN or an infinity makes the token's other gradients NaN).  A token with an
  * id outside [0, E) gets 0.
  *   d_w [T, k] fp32, logits as given to the forward, ids [T, k]; d_logits [T, E]
- *   of logits' type.  scale = 0 counts as the limit (all gradients 0).          */
+ *   of logits' type.  scale = 0 counts as the limit (all gradients 0).
+ * Evaluated in 64 bits and rounded once; softmax without renorm: the bracket, and
+ * four more roundings to fp32 (values from 2^104 on come out infinite).         */
 int moe_route_scored_backward(const float* d_w, const void* logits, int32_t logits_type, const int32_t* ids, int64_t T,
                               int32_t k, int32_t E, int32_t score, int32_t renorm, float scale, void* d_logits,
                               hipStream_t stream);

@@ -447,8 +447,13 @@ __device__ __forceinline__ float max_of_numbers(float a, float b) {
 //
 // Bound by vector instructions (80% of the cycles), not by memory: 131072 rows of 256, sigmoid,
 // bias, 4 of 8 groups, take 45 us, of which reading 128 MiB needs 27; one wave per row and
-// 64-bit scores took 228. Lanes of a row: as few as hold its groups and logits, since every
-// step of the merge is done by all of them.
+// 64-bit scores took 228. Softmax without groups: 37 us renormalised, 57 with the row's sum in
+// 64 bits for weights that are not (51 with 32-bit terms, which made them up to 2 ln E + 3 roundings
+// off). Lanes of a row: as few as hold its groups and logits, since every step of the merge is
+// done by all of them. The picks' logits are read again for their weights, from memory: 59 of the
+// 194 MB that are fetched (the next rows' have taken their place in L2).
+// Rows that 32 bits do not decide cost a wave each: 16384 (131072) of 256 equal logits with a bias
+// 37 (207) us, of a softmax with one logit 15 in front and a bias of zero 46 (262).
 template <bool F32, bool SIGMOID, bool BIAS, int LPR, int VPL, int VL, int KT>
 __global__ __launch_bounds__(256, LPR == 32 ? 3 : 4) void score_topk_kernel(ScoreArgs a) {
     extern __shared__ float lds_all[];
@@ -920,8 +925,10 @@ struct Row16 {
     }
 };
 
-// 16 lanes per token where the whole row does (softmax without renorm). Bound by reading
-// the rows: 16384 tokens of 256 experts (16 MiB) 7.0 us.
+// 16 lanes per token where the whole row does (softmax without renorm). 16384 tokens of 256
+// experts (16 MiB, 3.4 us of reading) take 7.5 us: one round of four waves to a SIMD, whose loads
+// come back at about the same time, and then 18 64-bit operations for each logit (7.0 with
+// 32-bit exponentials).
 template <bool F32, int VPL>
 __global__ __launch_bounds__(256) void score_replay_row_kernel(ScoreArgs a, int32_t* status) {
     const int lane = threadIdx.x & 15, E = a.E, k = a.k;
@@ -973,9 +980,9 @@ struct ScoreGradArgs {
 // into the rows' place in LDS, from which whole rows are written. In the whole-row form
 // they are the brackets of s_e (scale d_w - scale dot), made in 64 bits: for a row of one large score
 // the two terms are nearly equal. Brackets, 1 / sum and exponentials are rounded to 32 bits each
-// and multiplied there: 5 2^-24 of a gradient. Bound by writing
-// [T, E] (and reading it, where every logit has a gradient): 16384 tokens of 256 experts, fp32,
-// 7.2 us, and 8.9 with the whole row's gradient.
+// and multiplied there: 5 2^-24 of a gradient. Bound by the latency of one round of waves, in
+// which the stores wait for ids, their logits and exponentials: 16384 tokens of 256 experts,
+// fp32, 7.4 us (writing them 3.4), and 9.0 with the whole row's gradient (reading and writing 6.7).
 template <bool F32, bool SIGMOID, bool RENORM, bool PARTS, int VPL>
 __global__ __launch_bounds__(256) void score_backward_kernel(ScoreGradArgs a) {
     constexpr bool WHOLE = !SIGMOID && !RENORM;
